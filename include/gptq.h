@@ -321,6 +321,111 @@ gptq_status gptq_dequant_matmul(const void* X_fp16, int64_t T, const uint32_t* c
 gptq_status gptq_dequant_matmul_check(void* workspace, int device, void* cuda_stream);
 
 /* ---------------------------------------------------------------------------------------
+ * A packed layer in a model: the product with its epilogue, and the experts of a
+ * mixture-of-experts layer ("模型量化实战：从 INT8 PTQ 到 GPTQ 的精度保持与推理加速全解析" §4.3,
+ * and the group sizes that "GPTQ量化损失深度解析：原理、影响与优化策略" gives for MoE layers).
+ *
+ * A packed layer is what gptq_quantize_layer, gptq_rtn_quantize or gptq_awq_quantize wrote:
+ *   W[r][k] = (code[r][k] - zero[r][k / g]) * scale[r][k / g]        (sweep order k)
+ * The zeros are integers in [0, 2^bits - 1].  Unlike gptq_dequant_matmul, the products below do
+ * not round W to 16 bits: code - zero is exact in the activations' type and the scale multiplies
+ * each group's fp32 sum.
+ *   codes  : device uint32 [m x n*bits/32], 16-byte aligned; scales, zeros: device fp32 [m x n/g]
+ *   perm   : device int32 [n], 16-byte aligned (sweep position k holds original column perm[k]),
+ *            or NULL for the identity order
+ *   n % 128 == 0, 128 <= n <= 65536, 1 <= m <= 2^24; qp.sym is not read (the zeros hold it) */
+typedef struct {
+  const uint32_t* codes;
+  const float* scales;
+  const float* zeros;
+  const int32_t* perm;
+  int64_t m, n;
+  gptq_qparams qp;
+} gptq_packed;
+
+/* Type of the activations, bias, residual and 16-bit outputs. */
+enum { GPTQ_FP16 = 0, GPTQ_BF16 = 1 };
+/* Activations of the epilogues: none, ReLU (z if z > 0, else 0), GELU (z times the normal
+ * distribution function), SiLU (z / (1 + e^-z)). */
+enum { GPTQ_ACT_NONE = 0, GPTQ_ACT_RELU = 1, GPTQ_ACT_GELU = 2, GPTQ_ACT_SILU = 3 };
+
+/* The linear layer:
+ *   Z = X[:, perm] W^T + bias,   Y = act(Z) + residual
+ * in fp32, each output rounded once.
+ *   X        : device, dtype, [T x n] in original column order, row stride ld_x elements
+ *              (ld_x >= n, ld_x % 8 == 0, 16-byte aligned base); 0 <= T <= 2^24 (0 is a no-op)
+ *   bias     : device, dtype, [m], or NULL
+ *   residual : device, dtype, [T x m] with row stride ld_res >= m, or NULL; may be Y itself when
+ *              the strides and types agree
+ *   Y        : device [T x m] with row stride ld_y >= m, dtype, or fp32 when y_fp32 is 1; must not
+ *              overlap X
+ *   preact   : device, dtype, [T x m] contiguous, receives Z (the backward pass's input), or NULL
+ *   workspace: device, 256-byte aligned, at least gptq_dequant_linear_workspace_bytes (a status
+ *              word for gptq_dequant_matmul_check and, with a perm, X in sweep order); owned by the
+ *              caller, may be reused by later calls on the same stream; calls that can run at the
+ *              same time need one each
+ * Asynchronous on cuda_stream; no allocation and no synchronization, so a call can be captured
+ * into a graph; arguments are checked before any launch; the result is deterministic. */
+typedef struct {
+  const void* X;
+  int64_t T, ld_x;
+  int dtype;
+  gptq_packed W;
+  const void* bias;
+  const void* residual;
+  int64_t ld_res;
+  int act;
+  void* Y;
+  int64_t ld_y;
+  int y_fp32;
+  void* preact;
+  void* workspace;
+  size_t workspace_bytes;
+} gptq_linear_args;
+
+size_t gptq_dequant_linear_workspace_bytes(int64_t T, int64_t n, int act_order);
+gptq_status gptq_dequant_linear(const gptq_linear_args* args, int device, void* cuda_stream);
+
+/* The mixture-of-experts layer for a few tokens, experts packed:
+ *   p = softmax(X R^T) over the experts (64-bit); a token's top_k experts are those of the largest
+ *   p, in descending order, ties to the lower expert (a NaN is chosen last); their weights are p,
+ *   divided by their sum when renormalize is 1
+ *   h = act(x Wg_e^T) * (x Wu_e^T)     rounded to dtype (the second product's operand)
+ *   Y = sum over the token's experts of weight * h Wd_e^T, + residual
+ *   X         : device, dtype, [T x H], row stride ld_x (as gptq_dequant_linear); 0 <= T <= 128
+ *   router    : device, dtype, [E x H], 16-byte aligned; 1 <= E <= 256, 1 <= top_k <= min(E, 16)
+ *   gate_up   : the experts' gate and up weights, stacked: m = 2 I rows of n = H inputs per expert,
+ *               rows 0 .. I-1 gate, I .. 2I-1 up; codes [E x 2I x H*bits/32], scales and zeros
+ *               [E x 2I x H/g], perm [E x H] (both halves share their input's order) or NULL
+ *   down      : m = H rows of n = I inputs per expert; perm must be NULL: the order of an act-order
+ *               down projection is folded into the rows of gate and up (gptq.stack_experts)
+ *   residual  : as in gptq_dequant_linear; Y: [T x H], dtype, row stride ld_y
+ *   ids_out   : device int32 [T x top_k], or NULL;  weights_out: device fp32 [T x top_k], or NULL
+ *   workspace : device, 256-byte aligned, gptq_dequant_moe_workspace_bytes, as above
+ * H and I are multiples of 128, at most 65536; gate_up and down may differ in qp.group_size but not
+ * in qp.bits.  Asynchronous on cuda_stream, capturable, deterministic. */
+typedef struct {
+  const void* X;
+  int64_t T, ld_x;
+  int dtype;
+  const void* router;
+  int64_t E;
+  int top_k, renormalize, act;
+  gptq_packed gate_up, down;
+  const void* residual;
+  int64_t ld_res;
+  void* Y;
+  int64_t ld_y;
+  int32_t* ids_out;
+  float* weights_out;
+  void* workspace;
+  size_t workspace_bytes;
+} gptq_moe_args;
+
+size_t gptq_dequant_moe_workspace_bytes(int64_t T, int64_t E, int top_k, int64_t H, int64_t I, int act_order);
+gptq_status gptq_dequant_moe(const gptq_moe_args* args, int device, void* cuda_stream);
+
+/* ---------------------------------------------------------------------------------------
  * Sequential (cross-layer) quantization ("GPTQ算法原理深度解析" §2.1: the quantization error of a
  * layer reaches the next layer through its input): layer l+1 is calibrated on the outputs of
  * the already-quantized layer l, y = X_l W16_l^T (gptq_dequant_matmul), through the model's

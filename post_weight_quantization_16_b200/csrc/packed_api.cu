@@ -1,0 +1,280 @@
+// packed_api.cu — the C ABI of the products on packed layers (include/gptq.h: gptq_dequant_linear,
+// gptq_dequant_moe): argument checks, workspace layout and launches.
+#include <algorithm>
+#include <utility>
+
+#include "api_common.cuh"
+#include "packed_decode.cuh"
+#include "packed_moe.cuh"
+
+using namespace gptq;
+
+namespace {
+
+constexpr int64_t kPackedMaxN = 65536;
+constexpr int64_t kPackedMaxM = int64_t(1) << 24;
+constexpr int64_t kPackedMaxT = int64_t(1) << 24;
+constexpr int kSms = 148;
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
+bool aligned_to(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+bool valid_width(int64_t n) { return n >= 128 && n <= kPackedMaxN && n % 128 == 0; }
+
+bool valid_packed(const gptq_packed& w) {
+  gptq_qparams qp = w.qp;
+  qp.sym = 0;  // not read
+  return w.codes && w.scales && w.zeros && valid_width(w.n) && w.m >= 1 && w.m <= kPackedMaxM &&
+         valid_qparams(qp, w.n) && aligned16(w.codes) && aligned_to(w.scales, 4) && aligned_to(w.zeros, 4) &&
+         (!w.perm || aligned16(w.perm));
+}
+
+int group_width(const gptq_packed& w) { return w.qp.group_size == -1 ? static_cast<int>(w.n) : w.qp.group_size; }
+
+GroupIndex group_index(int g) {
+  GroupIndex gi;
+  gi.units_per_chunk_shift = g == 32 ? 2 : g == 64 ? 1 : 0;
+  gi.div = g >= 128 ? g / 128 : 1;
+  gi.magic = gi.div > 1 ? static_cast<uint32_t>(((uint64_t(1) << 32) + gi.div - 1) / gi.div) : 0u;
+  return gi;
+}
+
+gptq_status check_device(int device) {
+  int ndev = 0;
+  if (cudaGetDeviceCount(&ndev) != cudaSuccess || device < 0 || device >= ndev) {
+    cudaGetLastError();
+    return GPTQ_ERR_CUDA;
+  }
+  return GPTQ_OK;
+}
+
+template <typename F>
+cudaError_t by_bits(int bits, F&& f) {
+  switch (bits) {
+    case 2: return f(std::integral_constant<int, 2>());
+    case 3: return f(std::integral_constant<int, 3>());
+    case 4: return f(std::integral_constant<int, 4>());
+    default: return f(std::integral_constant<int, 8>());
+  }
+}
+
+// Blocks of a cluster that split k: enough that `tiles` row tiles give every SM about two blocks,
+// while a warp keeps at least one chunk.
+int k_split(int64_t tiles, int chunks) {
+  int cs = 1;
+  while (cs < 8 && tiles * cs < 2 * kSms && chunks >= 2 * cs * DEC_WARPS) cs *= 2;
+  return cs;
+}
+
+size_t linear_workspace(int64_t T, int64_t n, int act_order) {
+  return 256 + (act_order ? up256(static_cast<size_t>(T) * n * 2) : 0);
+}
+
+struct MoeLayout {
+  size_t logits, ids, weights, active, expert, begin, count, pair, pweight, x, h, total;
+};
+bool moe_layout(int64_t T, int64_t E, int64_t top_k, int64_t H, int64_t I, int act_order, MoeLayout* l) {
+  if (T < 0 || T > MOE_MAX_T || E < 1 || E > MOE_MAX_E || top_k < 1 || top_k > E || top_k > MOE_MAX_TOPK ||
+      !valid_width(H) || !valid_width(I))
+    return false;
+  size_t off = 256;  // status word
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off += up256(bytes);
+    return at;
+  };
+  const size_t pairs = static_cast<size_t>(T) * top_k;
+  l->logits = take(static_cast<size_t>(T) * E * 8);
+  l->ids = take(pairs * 4);
+  l->weights = take(pairs * 4);
+  l->active = take(4);
+  l->expert = take(E * 4);
+  l->begin = take(E * 4);
+  l->count = take(E * 4);
+  l->pair = take(pairs * 4);
+  l->pweight = take(pairs * 4);
+  l->x = take(act_order ? pairs * H * 2 : 0);
+  l->h = take(pairs * I * 2);
+  l->total = off;
+  return true;
+}
+
+}  // namespace
+
+extern "C" size_t gptq_dequant_linear_workspace_bytes(int64_t T, int64_t n, int act_order) {
+  if (T < 0 || T > kPackedMaxT || !valid_width(n)) return 0;
+  return linear_workspace(T, n, act_order);
+}
+
+extern "C" gptq_status gptq_dequant_linear(const gptq_linear_args* args, int device, void* cuda_stream) {
+  if (!args) return GPTQ_ERR_ARG;
+  const gptq_linear_args& a = *args;
+  if (a.T < 0 || a.T > kPackedMaxT || !valid_packed(a.W)) return GPTQ_ERR_ARG;
+  if (a.dtype != GPTQ_FP16 && a.dtype != GPTQ_BF16) return GPTQ_ERR_ARG;
+  if (a.act < GPTQ_ACT_NONE || a.act > GPTQ_ACT_SILU || (a.y_fp32 != 0 && a.y_fp32 != 1)) return GPTQ_ERR_ARG;
+  if (a.T == 0) return GPTQ_OK;
+  if (!a.X || !a.Y || !a.workspace) return GPTQ_ERR_ARG;
+  if (!aligned16(a.X) || a.ld_x < a.W.n || a.ld_x % 8 || !aligned256(a.workspace)) return GPTQ_ERR_ARG;
+  if (a.ld_y < a.W.m || !aligned_to(a.Y, a.y_fp32 ? 4 : 2) || !aligned_to(a.bias, 2) || !aligned_to(a.preact, 2))
+    return GPTQ_ERR_ARG;
+  if (a.residual && (a.ld_res < a.W.m || !aligned_to(a.residual, 2))) return GPTQ_ERR_ARG;
+  if (a.workspace_bytes < linear_workspace(a.T, a.W.n, a.W.perm ? 1 : 0)) return GPTQ_ERR_ARG;
+  const gptq_status ds = check_device(device);
+  if (ds != GPTQ_OK) return ds;
+  DeviceGuard dg(device);
+  cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  const int n = static_cast<int>(a.W.n), T = static_cast<int>(a.T), m = static_cast<int>(a.W.m);
+  const int g = group_width(a.W);
+  const uint16_t* X = static_cast<const uint16_t*>(a.X);
+  int64_t ldx = a.ld_x;
+  LinearDecodeArgs d;
+  for (int t0 = 0; a.W.perm && t0 < T; t0 += 65535)
+    CK(launch_pdl(gather_x_kernel, dim3((n + 1023) / 1024, std::min(65535, T - t0)), dim3(256), 0, 1, st,
+                  X + static_cast<size_t>(t0) * ldx, ldx, n, a.W.perm,
+                  reinterpret_cast<uint16_t*>(ws + 256) + static_cast<size_t>(t0) * n));
+  if (a.W.perm) {
+    X = reinterpret_cast<const uint16_t*>(ws + 256);
+    ldx = n;
+  }
+  d.early = a.W.perm ? 1 : 0;
+  d.X = X;
+  d.ldx = ldx;
+  d.codes = a.W.codes;
+  d.scales = a.W.scales;
+  d.zeros = a.W.zeros;
+  d.T = T;
+  d.m = m;
+  d.chunks = n / 128;
+  d.G = n / g;
+  d.gi = group_index(g);
+  d.bias = static_cast<const uint16_t*>(a.bias);
+  d.residual = static_cast<const uint16_t*>(a.residual);
+  d.ld_res = a.ld_res;
+  d.ldy = a.ld_y;
+  d.Y = a.Y;
+  d.preact = static_cast<uint16_t*>(a.preact);
+  d.act = a.act;
+  d.y_fp32 = a.y_fp32;
+  d.status = reinterpret_cast<int*>(ws);
+  DecodeLaunch l;
+  l.bf16 = a.dtype == GPTQ_BF16;
+  l.unit = std::min(g, 128);
+  l.nt = T <= 8 ? 1 : 2;
+  l.rt = 1;
+  l.cluster = k_split((m + 15) / 16, d.chunks);
+  l.device = device;
+  l.stream = st;
+  CK(by_bits(a.W.qp.bits, [&](auto b) { return launch_linear_decode<decltype(b)::value>(l, d); }));
+  return GPTQ_OK;
+}
+
+extern "C" size_t gptq_dequant_moe_workspace_bytes(int64_t T, int64_t E, int top_k, int64_t H, int64_t I,
+                                                   int act_order) {
+  MoeLayout l;
+  return moe_layout(T, E, top_k, H, I, act_order, &l) ? l.total : 0;
+}
+
+extern "C" gptq_status gptq_dequant_moe(const gptq_moe_args* args, int device, void* cuda_stream) {
+  if (!args) return GPTQ_ERR_ARG;
+  const gptq_moe_args& a = *args;
+  const int64_t H = a.gate_up.n, I = a.down.n;
+  MoeLayout lay;
+  if (!valid_packed(a.gate_up) || !valid_packed(a.down) || a.gate_up.m != 2 * I || a.down.m != H || a.down.perm ||
+      a.gate_up.qp.bits != a.down.qp.bits)
+    return GPTQ_ERR_ARG;
+  if (!moe_layout(a.T, a.E, a.top_k, H, I, a.gate_up.perm ? 1 : 0, &lay)) return GPTQ_ERR_ARG;
+  if ((a.dtype != GPTQ_FP16 && a.dtype != GPTQ_BF16) || (a.renormalize != 0 && a.renormalize != 1) ||
+      a.act < GPTQ_ACT_NONE || a.act > GPTQ_ACT_SILU)
+    return GPTQ_ERR_ARG;
+  if (a.T == 0) return GPTQ_OK;
+  if (!a.X || !a.router || !a.Y || !a.workspace) return GPTQ_ERR_ARG;
+  if (!aligned16(a.X) || a.ld_x < H || a.ld_x % 8 || !aligned16(a.router) || !aligned256(a.workspace))
+    return GPTQ_ERR_ARG;
+  if (a.ld_y < H || !aligned_to(a.Y, 2) || (a.residual && (a.ld_res < H || !aligned_to(a.residual, 2))) ||
+      !aligned_to(a.ids_out, 4) || !aligned_to(a.weights_out, 4))
+    return GPTQ_ERR_ARG;
+  if (a.workspace_bytes < lay.total) return GPTQ_ERR_ARG;
+  const gptq_status ds = check_device(device);
+  if (ds != GPTQ_OK) return ds;
+  DeviceGuard dg(device);
+  cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  const bool bf = a.dtype == GPTQ_BF16;
+  const int pairs = static_cast<int>(a.T) * a.top_k;
+
+  RouterArgs r;
+  r.X = static_cast<const uint16_t*>(a.X);
+  r.ldx = a.ld_x;
+  r.R = static_cast<const uint16_t*>(a.router);
+  r.T = static_cast<int>(a.T);
+  r.E = static_cast<int>(a.E);
+  r.H = static_cast<int>(H);
+  r.top_k = a.top_k;
+  r.renorm = a.renormalize;
+  r.logits = reinterpret_cast<double*>(ws + lay.logits);
+  r.ids = reinterpret_cast<int32_t*>(ws + lay.ids);
+  r.weights = reinterpret_cast<float*>(ws + lay.weights);
+  r.ids_out = a.ids_out;
+  r.weights_out = a.weights_out;
+  r.plan.active = reinterpret_cast<int*>(ws + lay.active);
+  r.plan.expert = reinterpret_cast<int*>(ws + lay.expert);
+  r.plan.begin = reinterpret_cast<int*>(ws + lay.begin);
+  r.plan.count = reinterpret_cast<int*>(ws + lay.count);
+  r.plan.pair = reinterpret_cast<int*>(ws + lay.pair);
+  r.plan.weight = reinterpret_cast<float*>(ws + lay.pweight);
+  r.status = reinterpret_cast<int*>(ws);
+  CK(launch_pdl(bf ? moe_router_kernel<true> : moe_router_kernel<false>, dim3(ROUTER_CLUSTER), dim3(ROUTER_WARPS * 32), 0,
+                ROUTER_CLUSTER, st, r));
+
+  MoeArgs m;
+  m.X = r.X;
+  m.ldx = a.ld_x;
+  m.gathered = a.gate_up.perm ? 1 : 0;
+  if (a.gate_up.perm) {
+    uint16_t* xg = reinterpret_cast<uint16_t*>(ws + lay.x);
+    CK(launch_pdl(moe_gather_kernel, dim3(static_cast<unsigned>((H + 1023) / 1024), pairs), dim3(256), 0, 1, st, r.X,
+                  a.ld_x, static_cast<int>(H), a.gate_up.perm, r.plan, a.top_k, static_cast<const int32_t*>(r.ids),
+                  xg));
+    m.X = xg;
+    m.ldx = H;
+  }
+  m.plan = r.plan;
+  m.T = r.T;
+  m.E = r.E;
+  m.top_k = a.top_k;
+  m.H = r.H;
+  m.I = static_cast<int>(I);
+  m.gu_codes = a.gate_up.codes;
+  m.gu_scales = a.gate_up.scales;
+  m.gu_zeros = a.gate_up.zeros;
+  m.dn_codes = a.down.codes;
+  m.dn_scales = a.down.scales;
+  m.dn_zeros = a.down.zeros;
+  const int gg = group_width(a.gate_up), gd = group_width(a.down);
+  m.gu_G = m.H / gg;
+  m.dn_G = m.I / gd;
+  m.gu_gi = group_index(gg);
+  m.dn_gi = group_index(gd);
+  m.act = a.act;
+  m.h = reinterpret_cast<uint16_t*>(ws + lay.h);
+  m.residual = static_cast<const uint16_t*>(a.residual);
+  m.ld_res = a.ld_res;
+  m.ldy = a.ld_y;
+  m.Y = static_cast<uint16_t*>(a.Y);
+  DecodeLaunch l;
+  l.bf16 = bf;
+  l.nt = a.T <= 8 ? 1 : 2;
+  l.rt = 1;
+  l.device = device;
+  l.stream = st;
+  l.unit = std::min(gg, 128);
+  l.cluster = 1;
+  const int slots = static_cast<int>(std::min<int64_t>(a.E, pairs));
+  CK(by_bits(a.gate_up.qp.bits, [&](auto b) { return launch_moe_gate_up<decltype(b)::value>(l, m, slots); }));
+  l.unit = std::min(gd, 128);
+  l.cluster = k_split((m.H + 15) / 16, slots * (m.I / 128));
+  CK(by_bits(a.down.qp.bits, [&](auto b) { return launch_moe_down<decltype(b)::value>(l, m); }));
+  return GPTQ_OK;
+}

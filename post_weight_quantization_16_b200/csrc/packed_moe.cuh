@@ -1,0 +1,238 @@
+// packed_moe.cuh — routing of the mixture-of-experts layer: router product, softmax, top-k and the
+// lists of tokens per expert, in one launch of one cluster; and the gathers of activations into
+// sweep order.
+#pragma once
+
+#include "packed_decode.cuh"
+
+namespace gptq {
+
+// out[t][k] = X[t][perm[k]] (perm null: a copy into rows of n).  Grid (n / 1024 rounded up, tokens);
+// four columns a thread.
+__global__ void __launch_bounds__(256) gather_x_kernel(const uint16_t* __restrict__ X, int64_t ldx, int n,
+                                                       const int32_t* __restrict__ perm, uint16_t* __restrict__ out) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int k = (blockIdx.x * 256 + threadIdx.x) * 4;
+  if (k >= n) return;
+  const uint16_t* src = X + static_cast<size_t>(blockIdx.y) * ldx;
+  const int4 i = perm ? *reinterpret_cast<const int4*>(perm + k) : make_int4(k, k + 1, k + 2, k + 3);
+  const ushort4 v = make_ushort4(src[i.x], src[i.y], src[i.z], src[i.w]);
+  *reinterpret_cast<ushort4*>(out + static_cast<size_t>(blockIdx.y) * n + k) = v;
+}
+
+// The activations of list position blockIdx.y in its expert's sweep order.
+__global__ void __launch_bounds__(256) moe_gather_kernel(const uint16_t* __restrict__ X, int64_t ldx, int n,
+                                                         const int32_t* __restrict__ perm, MoePlan plan, int top_k,
+                                                         const int32_t* __restrict__ ids,
+                                                         uint16_t* __restrict__ out) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int k = (blockIdx.x * 256 + threadIdx.x) * 4;
+  if (k >= n) return;
+  const int pair = plan.pair[blockIdx.y], e = ids[pair];
+  const uint16_t* src = X + static_cast<size_t>(pair / top_k) * ldx;
+  const int4 i = *reinterpret_cast<const int4*>(perm + static_cast<size_t>(e) * n + k);
+  const ushort4 v = make_ushort4(src[i.x], src[i.y], src[i.z], src[i.w]);
+  *reinterpret_cast<ushort4*>(out + static_cast<size_t>(blockIdx.y) * n + k) = v;
+}
+
+// ------------------------------------------------------------------------------------------
+// router
+// ------------------------------------------------------------------------------------------
+constexpr int ROUTER_CLUSTER = 8;
+constexpr int ROUTER_WARPS = 16;
+
+struct RouterArgs {
+  const uint16_t* X;
+  int64_t ldx;
+  const uint16_t* R;  // [E x H]
+  int T, E, H, top_k, renorm;
+  double* logits;      // [T x E] (workspace)
+  int32_t* ids;        // [T x top_k] (workspace)
+  float* weights;      // [T x top_k] (workspace)
+  int32_t* ids_out;    // the caller's copies, or null
+  float* weights_out;
+  MoePlan plan;
+  int* status;
+};
+
+// One cluster.  (1) Logits: tiles of 16 experts x 8 tokens go round the blocks, a tile's 16 warps
+// split H; products of 16-bit values are exact in fp32, 128 columns are summed on the tensor cores
+// and the partial sums of those in fp64, so the order of the choices is that of the 64-bit logits
+// but for logits that agree to about 1e-7.  (2) Softmax and top-k: a warp per token, in fp64; equal
+// values go to the lower expert; a NaN logit is chosen last (its weights are NaN).  (3) The lists:
+// block 0, a warp per expert, by ballots over the T * top_k choices, so positions are deterministic.
+template <bool BF>
+__global__ void __launch_bounds__(ROUTER_WARPS * 32) moe_router_kernel(const RouterArgs p) {
+  __shared__ double red[ROUTER_WARPS][128];
+  __shared__ int counts[MOE_MAX_E];
+  __shared__ int begins[MOE_MAX_E];
+  __shared__ int slots[MOE_MAX_E];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  const int rank = static_cast<int>(cluster_ctarank());
+  if (rank == 0 && threadIdx.x == 0) *p.status = 0;
+  const int et = (p.E + 15) / 16, tt = (p.T + 7) / 8, blocks = p.H / 32;
+  for (int tile = rank; tile < et * tt; tile += ROUTER_CLUSTER) {
+    const int e0 = (tile % et) * 16, t0 = (tile / et) * 8;
+    const uint16_t* ra = p.R + static_cast<size_t>(min(e0 + g, p.E - 1)) * p.H + q * 8;
+    const uint16_t* rb = p.R + static_cast<size_t>(min(e0 + g + 8, p.E - 1)) * p.H + q * 8;
+    const uint16_t* x = p.X + static_cast<size_t>(min(t0 + g, p.T - 1)) * p.ldx + q * 8;
+    double acc[4] = {0.0, 0.0, 0.0, 0.0};
+    const int b0 = blocks * warp / ROUTER_WARPS, b1 = blocks * (warp + 1) / ROUTER_WARPS;
+    for (int b = b0; b < b1; b += 4) {
+      float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (b + j < b1) {
+          const uint4 va = *reinterpret_cast<const uint4*>(ra + (b + j) * 32);
+          const uint4 vb = *reinterpret_cast<const uint4*>(rb + (b + j) * 32);
+          const uint4 vx = *reinterpret_cast<const uint4*>(x + (b + j) * 32);
+          mma_16816<BF>(d, va.x, vb.x, va.y, vb.y, vx.x, vx.y);
+          mma_16816<BF>(d, va.z, vb.z, va.w, vb.w, vx.z, vx.w);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[j] += static_cast<double>(d[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) red[warp][lane * 4 + j] = acc[j];
+    __syncthreads();
+    if (threadIdx.x < 128) {
+      double v = 0.0;
+#pragma unroll
+      for (int w = 0; w < ROUTER_WARPS; ++w) v += red[w][threadIdx.x];
+      const int l = threadIdx.x >> 2, j = threadIdx.x & 3;
+      const int e = e0 + (l >> 2) + 8 * (j >> 1), t = t0 + 2 * (l & 3) + (j & 1);
+      if (e < p.E && t < p.T) p.logits[static_cast<size_t>(t) * p.E + e] = v;
+    }
+    __syncthreads();
+  }
+  cluster_sync();  // the logits are written
+
+  constexpr int PER = MOE_MAX_E / 32;
+  for (int t = rank * ROUTER_WARPS + warp; t < p.T; t += ROUTER_CLUSTER * ROUTER_WARPS) {
+    double v[PER];
+    double best_all = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int e = lane + 32 * i;
+      v[i] = e < p.E ? __ldcg(p.logits + static_cast<size_t>(t) * p.E + e) : -INFINITY;
+      best_all = fmax(best_all, v[i]);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) best_all = fmax(best_all, __shfl_xor_sync(0xffffffffu, best_all, o));
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (lane + 32 * i < p.E) sum += exp(v[i] - best_all);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    unsigned used = 0;
+    int my_id = 0;
+    double my_p = 0.0, chosen = 0.0;
+    for (int k = 0; k < p.top_k; ++k) {
+      double bv = 0.0;
+      int bi = 1 << 30;  // none yet
+      bool bn = true;    // the best so far is a NaN (or none)
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int e = lane + 32 * i;
+        if (e < p.E && !((used >> i) & 1u)) {
+          const bool isn = v[i] != v[i];
+          const bool better = bi == (1 << 30) || (bn && !isn) || (!bn && !isn && v[i] > bv);
+          if (better) {
+            bv = v[i];
+            bi = e;
+            bn = isn;
+          }
+        }
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) {
+        const double ov = __shfl_xor_sync(0xffffffffu, bv, o);
+        const int oi = __shfl_xor_sync(0xffffffffu, bi, o);
+        const bool on = __shfl_xor_sync(0xffffffffu, static_cast<int>(bn), o) != 0;
+        const bool none = bi == (1 << 30), onone = oi == (1 << 30);
+        const bool take = !onone && (none || (bn && !on) ||
+                                     (bn == on && ((!bn && ov > bv) || ((bn || ov == bv) && oi < bi))));
+        if (take) {
+          bv = ov;
+          bi = oi;
+          bn = on;
+        }
+      }
+      const double pk = exp(bv - best_all) / sum;
+      if ((bi & 31) == lane) used |= 1u << (bi >> 5);
+      if (lane == k) {
+        my_id = bi;
+        my_p = pk;
+      }
+      chosen += pk;
+    }
+    if (lane < p.top_k) {
+      const size_t o = static_cast<size_t>(t) * p.top_k + lane;
+      const float w = static_cast<float>(p.renorm ? my_p / chosen : my_p);
+      p.ids[o] = my_id;
+      p.weights[o] = w;
+      if (p.ids_out) p.ids_out[o] = my_id;
+      if (p.weights_out) p.weights_out[o] = w;
+    }
+  }
+  cluster_sync();  // the choices are written
+  if (rank != 0) return;
+
+  const int pairs = p.T * p.top_k;
+  for (int e = warp; e < p.E; e += ROUTER_WARPS) {
+    int n = 0;
+    for (int i = lane; i < (pairs + 31) / 32 * 32; i += 32)
+      n += __popc(__ballot_sync(0xffffffffu, i < pairs && __ldcg(p.ids + i) == e));
+    if (lane == 0) counts[e] = n;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int base = 0, slot = 0;
+    for (int e0 = 0; e0 < p.E; e0 += 32) {
+      const int e = e0 + lane;
+      const int n = e < p.E ? counts[e] : 0;
+      int inc = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += u;
+      }
+      const unsigned has = __ballot_sync(0xffffffffu, n > 0);
+      if (e < p.E) {
+        begins[e] = base + inc - n;
+        slots[e] = slot + __popc(has & ((1u << lane) - 1u));
+      }
+      base += __shfl_sync(0xffffffffu, inc, 31);
+      slot += __popc(has);
+    }
+    if (lane == 0) *p.plan.active = slot;
+  }
+  __syncthreads();
+  for (int e = warp; e < p.E; e += ROUTER_WARPS) {
+    if (counts[e] == 0) continue;
+    int at = begins[e];
+    for (int i = lane; i < (pairs + 31) / 32 * 32; i += 32) {
+      const bool mine = i < pairs && __ldcg(p.ids + i) == e;
+      const unsigned m = __ballot_sync(0xffffffffu, mine);
+      if (mine) {
+        const int o = at + __popc(m & ((1u << lane) - 1u));
+        p.plan.pair[o] = i;
+        p.plan.weight[o] = __ldcg(p.weights + i);
+      }
+      at += __popc(m);
+    }
+    if (lane == 0) {
+      p.plan.expert[slots[e]] = e;
+      p.plan.begin[slots[e]] = begins[e];
+      p.plan.count[slots[e]] = counts[e];
+    }
+  }
+}
+
+}  // namespace gptq

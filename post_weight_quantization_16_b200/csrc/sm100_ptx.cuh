@@ -125,7 +125,7 @@ __device__ __forceinline__ bool mbar_wait_bounded_cl(uint32_t bar, uint32_t pari
 
 // One CTA waits on a barrier nobody arrives on, with a short limit: the failure path of the
 // bounded wait (records ST_TIMEOUT and returns; used by the tests of failure detection).
-__global__ void bounded_wait_probe_kernel(uint64_t limit_ns, int* status) {
+static __global__ void bounded_wait_probe_kernel(uint64_t limit_ns, int* status) {
   __shared__ __align__(8) uint64_t bar;
   __shared__ int abort_flag;
   if (threadIdx.x == 0) {

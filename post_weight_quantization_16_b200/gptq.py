@@ -48,6 +48,31 @@ class KernelStat(ctypes.Structure):
                 ("flops", ctypes.c_double), ("bytes", ctypes.c_double)]
 
 
+class PackedLayer(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("zeros", ctypes.c_void_p),
+                ("perm", ctypes.c_void_p), ("m", ctypes.c_int64), ("n", ctypes.c_int64), ("qp", QParams)]
+
+
+class LinearArgs(ctypes.Structure):
+    _fields_ = [("X", ctypes.c_void_p), ("T", ctypes.c_int64), ("ld_x", ctypes.c_int64), ("dtype", ctypes.c_int),
+                ("W", PackedLayer), ("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p),
+                ("ld_res", ctypes.c_int64), ("act", ctypes.c_int), ("Y", ctypes.c_void_p), ("ld_y", ctypes.c_int64),
+                ("y_fp32", ctypes.c_int), ("preact", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_size_t)]
+
+
+class MoeArgs(ctypes.Structure):
+    _fields_ = [("X", ctypes.c_void_p), ("T", ctypes.c_int64), ("ld_x", ctypes.c_int64), ("dtype", ctypes.c_int),
+                ("router", ctypes.c_void_p), ("E", ctypes.c_int64), ("top_k", ctypes.c_int),
+                ("renormalize", ctypes.c_int), ("act", ctypes.c_int), ("gate_up", PackedLayer), ("down", PackedLayer),
+                ("residual", ctypes.c_void_p), ("ld_res", ctypes.c_int64), ("Y", ctypes.c_void_p),
+                ("ld_y", ctypes.c_int64), ("ids_out", ctypes.c_void_p), ("weights_out", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_SILU = range(4)
+_DTYPES = {torch.float16: 0, torch.bfloat16: 1}
+
 _LIB = None
 _P = ctypes.c_void_p
 _SIGS = {
@@ -74,6 +99,11 @@ _SIGS = {
     "gptq_dequant_matmul": (ctypes.c_int, [_P, ctypes.c_int64, _P, _P, _P, _P, ctypes.c_int64, ctypes.c_int64,
                                            QParams, _P, _P, ctypes.c_size_t, ctypes.c_int, _P]),
     "gptq_dequant_matmul_check": (ctypes.c_int, [_P, ctypes.c_int, _P]),
+    "gptq_dequant_linear_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int]),
+    "gptq_dequant_linear": (ctypes.c_int, [ctypes.POINTER(LinearArgs), ctypes.c_int, _P]),
+    "gptq_dequant_moe_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int,
+                                                           ctypes.c_int64, ctypes.c_int64, ctypes.c_int]),
+    "gptq_dequant_moe": (ctypes.c_int, [ctypes.POINTER(MoeArgs), ctypes.c_int, _P]),
     "gptq_quantize_layers": (ctypes.c_int, [ctypes.POINTER(LayerJob), ctypes.c_int, ctypes.c_int, _P]),
     "gptq_pipeline_create": (ctypes.c_int, [ctypes.POINTER(_P), ctypes.POINTER(ctypes.c_int64),
                                             ctypes.POINTER(ctypes.c_int64), ctypes.c_int, ctypes.c_int, _P]),
@@ -304,6 +334,155 @@ def dequant_matmul(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, z
                                      _ptr(out), _ptr(workspace), workspace.numel(), dev.index,
                                      ctypes.c_void_p(stream.cuda_stream)), "gptq_dequant_matmul")
     return out
+
+
+def _packed(codes, scales, zeros, perm, bits: int, group_size: int, dev: torch.device, experts: int = 0) -> PackedLayer:
+    """The C description of a packed layer (of `experts` stacked ones), its tensors checked."""
+    lead = (experts,) if experts else ()
+    if codes.dim() != 2 + len(lead) or tuple(codes.shape[:-2]) != lead:
+        raise ValueError(f"codes must be {'[E, m, words]' if lead else '[m, words]'}, got {tuple(codes.shape)}")
+    m, words = codes.shape[-2:]
+    if bits not in (2, 3, 4, 8) or words * 32 % bits:
+        raise ValueError(f"bits must be 2, 3, 4 or 8 and fit the rows of codes, got {bits}")
+    n = words * 32 // bits
+    g = n if group_size == -1 else group_size
+    if g < 32 or n % g:
+        raise ValueError(f"group_size {group_size} does not divide {n} columns")
+    want = (*lead, m, n // g)
+    for name, t, dt, shape in (("codes", codes, torch.int32, codes.shape), ("scales", scales, torch.float32, want),
+                               ("zeros", zeros, torch.float32, want), ("perm", perm, torch.int32, (*lead, n))):
+        if t is None and name == "perm":
+            continue
+        if t.dtype != dt or t.shape != shape or not t.is_contiguous() or t.device != dev:
+            raise ValueError(f"{name} must be a contiguous {dt} {tuple(shape)} tensor on {dev}")
+    return PackedLayer(codes.data_ptr(), scales.data_ptr(), zeros.data_ptr(), None if perm is None else perm.data_ptr(),
+                       m, n, QParams(bits, group_size, 0))
+
+
+def _rows(name: str, t: torch.Tensor | None, shape: tuple, dtype: torch.dtype, dev: torch.device):
+    """(pointer, row stride) of an optional row-major matrix with unit column stride."""
+    if t is None:
+        return None, 0
+    if t.dtype != dtype or t.shape != shape or t.device != dev or (t.stride(1) != 1 and shape[1] > 1):
+        raise ValueError(f"{name} must be a {dtype} {tuple(shape)} tensor with unit column stride on {dev}")
+    return t.data_ptr(), t.stride(0) if shape[0] > 1 else max(t.stride(0), shape[1])
+
+
+def _activations(name: str, X: torch.Tensor, n: int):
+    """Checks of the left operand: (pointer, tokens, row stride, dtype code)."""
+    if X.dim() != 2 or X.shape[1] != n or X.dtype not in _DTYPES or not X.is_cuda or (X.stride(1) != 1 and n > 1):
+        raise ValueError(f"{name} must be an fp16 or bf16 [T, {n}] device tensor with unit column stride")
+    ld = X.stride(0) if X.shape[0] > 1 else n
+    if ld % 8 or ld < n or X.data_ptr() % 16:
+        raise ValueError(f"{name} needs a 16-byte aligned base and a row stride that is a multiple of 8 elements "
+                         "and no smaller than a row")
+    return X.data_ptr(), X.shape[0], ld, _DTYPES[X.dtype]
+
+
+class _on:
+    """Allocations and launches of a call on `stream` (None: the device's current stream)."""
+
+    def __init__(self, dev: torch.device, stream: torch.cuda.Stream | None):
+        current = torch.cuda.current_stream(dev)
+        self.handle = (current if stream is None else stream).cuda_stream
+        self.ctx = None if self.handle == current.cuda_stream else torch.cuda.stream(stream)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return self.handle
+
+    def __exit__(self, *a):
+        if self.ctx is not None:
+            self.ctx.__exit__(*a)
+
+
+def _workspace(need: int, workspace: torch.Tensor | None, dev: torch.device) -> torch.Tensor:
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=dev)
+    if workspace.dtype != torch.uint8 or workspace.device != dev or not workspace.is_contiguous() \
+            or workspace.numel() < need:
+        raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {need} bytes on {dev}")
+    return workspace
+
+
+def dequant_linear(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor,
+                   perm: torch.Tensor | None, bits: int, group_size: int, bias: torch.Tensor | None = None,
+                   act: int = ACT_NONE, residual: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
+                   want_preact: bool = False, out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                   stream: torch.cuda.Stream | None = None):
+    """Y = act(X[:, perm] W^T + bias) + residual with a packed W (gptq_dequant_linear).  X: fp16 or
+    bf16 [T, n] device tensor in original column order (row stride a multiple of 8); codes, scales,
+    zeros, perm as quantize_layer (or rtn_quantize, awq_quantize: perm None) wrote them; bias [m] and
+    residual [T, m] in X's type; act one of ACT_NONE, ACT_RELU, ACT_GELU, ACT_SILU.  Returns Y [T, m]
+    in X's type (or fp32 with out_dtype=torch.float32), and with want_preact also Z, the value the
+    activation was applied to, which dequant_linear_backward takes.  `out` may be `residual`.
+    Asynchronous on `stream`; capturable into a graph when out and workspace are given or the
+    capture owns the allocations."""
+    dev = X.device
+    W = _packed(codes, scales, zeros, perm, bits, group_size, dev)
+    m, n = W.m, W.n
+    x_ptr, T, ldx, dt = _activations("X", X, n)
+    if out_dtype not in (None, X.dtype, torch.float32):
+        raise ValueError("out_dtype must be X's type or torch.float32")
+    if bias is not None and (bias.dtype != X.dtype or bias.shape != (m,) or not bias.is_contiguous()
+                             or bias.device != dev):
+        raise ValueError(f"bias must be a contiguous {X.dtype} [{m}] tensor on {dev}")
+    r_ptr, ldr = _rows("residual", residual, (T, m), X.dtype, dev)
+    y_type = X.dtype if out_dtype is None else out_dtype
+    with _on(dev, stream) as handle:
+        if out is None:
+            out = torch.empty((T, m), dtype=y_type, device=dev)
+        y_ptr, ldy = _rows("out", out, (T, m), y_type, dev)
+        z = torch.empty((T, m), dtype=X.dtype, device=dev) if want_preact else None
+        need = int(lib().gptq_dequant_linear_workspace_bytes(T, n, int(perm is not None)))
+        if need == 0:
+            raise GPTQError(ERR_ARG, "gptq_dequant_linear_workspace_bytes")
+        ws = _workspace(need, workspace, dev)
+        a = LinearArgs(x_ptr, T, ldx, dt, W, None if bias is None else bias.data_ptr(), r_ptr, ldr, int(act), y_ptr, ldy,
+                       int(y_type == torch.float32), None if z is None else z.data_ptr(), ws.data_ptr(), ws.numel())
+        _check(lib().gptq_dequant_linear(ctypes.byref(a), dev.index, handle), "gptq_dequant_linear")
+    return (out, z) if want_preact else out
+
+
+def dequant_moe(X: torch.Tensor, router: torch.Tensor, gate_up: tuple, down: tuple, perm: torch.Tensor | None,
+                bits: int, group_size: int, top_k: int, renormalize: bool = True, act: int = ACT_SILU,
+                residual: torch.Tensor | None = None, down_group_size: int | None = None,
+                out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                stream: torch.cuda.Stream | None = None):
+    """The mixture-of-experts layer for at most 128 tokens on packed experts (gptq_dequant_moe).
+    X: fp16 or bf16 [T, H]; router [E, H] in X's type; gate_up = (codes [E, 2 I, words], scales, zeros)
+    with the gate rows first; down = (codes [E, H, words], scales, zeros); perm: int32 [E, H], the
+    act-order of each expert's gate and up, or None (stack_experts builds these from quantized
+    layers).  Returns Y [T, H], the chosen experts [T, top_k] (int32, by descending probability) and
+    their weights [T, top_k] (fp32).  Asynchronous on `stream`."""
+    dev = X.device
+    E = router.shape[0] if router.dim() == 2 else 0
+    if E == 0:
+        raise ValueError("router must be [E, H] with at least one expert")
+    gu = _packed(*gate_up, perm, bits, group_size, dev, E)
+    dn = _packed(*down, None, bits, group_size if down_group_size is None else down_group_size, dev, E)
+    H, I = gu.n, dn.n
+    if gu.m != 2 * I or dn.m != H:
+        raise ValueError(f"gate_up [E, {gu.m}, {H} columns] and down [E, {dn.m}, {I} columns] do not fit together")
+    x_ptr, T, ldx, dt = _activations("X", X, H)
+    if router.dtype != X.dtype or router.shape[1] != H or not router.is_contiguous() or router.device != dev:
+        raise ValueError(f"router must be a contiguous {X.dtype} [E, {H}] tensor on {dev}")
+    r_ptr, ldr = _rows("residual", residual, (T, H), X.dtype, dev)
+    with _on(dev, stream) as handle:
+        if out is None:
+            out = torch.empty((T, H), dtype=X.dtype, device=dev)
+        y_ptr, ldy = _rows("out", out, (T, H), X.dtype, dev)
+        ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+        weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+        need = int(lib().gptq_dequant_moe_workspace_bytes(T, E, top_k, H, I, int(perm is not None)))
+        if need == 0:
+            raise GPTQError(ERR_ARG, "gptq_dequant_moe_workspace_bytes")
+        ws = _workspace(need, workspace, dev)
+        a = MoeArgs(x_ptr, T, ldx, dt, router.data_ptr(), E, int(top_k), int(bool(renormalize)), int(act), gu, dn, r_ptr,
+                    ldr, y_ptr, ldy, ids.data_ptr(), weights.data_ptr(), ws.data_ptr(), ws.numel())
+        _check(lib().gptq_dequant_moe(ctypes.byref(a), dev.index, handle), "gptq_dequant_moe")
+    return out, ids, weights
 
 
 def _jobs(layers: list, dev: torch.device):
