@@ -353,7 +353,7 @@ enum { GPTQ_ACT_NONE = 0, GPTQ_ACT_RELU = 1, GPTQ_ACT_GELU = 2, GPTQ_ACT_SILU = 
  *   Z = X[:, perm] W^T + bias,   Y = act(Z) + residual
  * in fp32, each output rounded once.
  *   X        : device, dtype, [T x n] in original column order, row stride ld_x elements
- *              (ld_x >= n, ld_x % 8 == 0, 16-byte aligned base); 0 <= T <= 2^24 (0 is a no-op)
+ *              (ld_x >= n, ld_x % 8 == 0, 16-byte aligned base); 0 <= T <= 2^22 (0 is a no-op)
  *   bias     : device, dtype, [m], or NULL
  *   residual : device, dtype, [T x m] with row stride ld_res >= m, or NULL; may be Y itself when
  *              the strides and types agree

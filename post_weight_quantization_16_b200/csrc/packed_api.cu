@@ -6,6 +6,7 @@
 #include "api_common.cuh"
 #include "packed_decode.cuh"
 #include "packed_moe.cuh"
+#include "packed_tc.cuh"
 
 using namespace gptq;
 
@@ -13,7 +14,7 @@ namespace {
 
 constexpr int64_t kPackedMaxN = 65536;
 constexpr int64_t kPackedMaxM = int64_t(1) << 24;
-constexpr int64_t kPackedMaxT = int64_t(1) << 24;
+constexpr int64_t kPackedMaxT = int64_t(1) << 22;
 constexpr int kSms = 148;
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
@@ -69,6 +70,77 @@ int k_split(int64_t tiles, int chunks) {
 
 size_t linear_workspace(int64_t T, int64_t n, int act_order) {
   return 256 + (act_order ? up256(static_cast<size_t>(T) * n * 2) : 0);
+}
+
+// Tokens up to which the warp-level kernel runs; beyond, tcgen05.
+constexpr int kDecodeTokens = 16;
+
+// Row-major 2-D tensor map: `cols` x `rows` elements of a type, boxes of box_cols x box_rows.
+gptq_status encode_map(CUtensorMap* map, CUtensorMapDataType type, int elem, const void* base, int64_t cols,
+                       int64_t rows, int64_t ld, int box_cols, int box_rows, CUtensorMapSwizzle swizzle) {
+  PFN_cuTensorMapEncodeTiled_v12000 encode = get_encode();
+  if (!encode) return GPTQ_ERR_CUDA;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * elem};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[2] = {1, 1};
+  return encode(map, type, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? GPTQ_OK
+             : GPTQ_ERR_CUDA;
+}
+
+gptq_status encode_codes(CUtensorMap* map, const gptq_packed& w) {
+  const int64_t words = w.n * w.qp.bits / 32;
+  return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, w.codes, words, w.m, words, 4 * w.qp.bits, TC_BM,
+                    CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+gptq_status encode_act(CUtensorMap* map, int dtype, const void* base, int64_t cols, int64_t rows, int64_t ld,
+                       int box_rows) {
+  return encode_map(map, dtype == GPTQ_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+                    base, cols, rows, ld, 64, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// The linear layer on tcgen05: X in sweep order.
+gptq_status linear_many_tokens(const gptq_linear_args& a, const uint16_t* X, int64_t ldx, int device,
+                               cudaStream_t st) {
+  const int m = static_cast<int>(a.W.m), n = static_cast<int>(a.W.n), T = static_cast<int>(a.T);
+  const int g = group_width(a.W);
+  LinearTcArgs d;
+  d.T = T;
+  d.m = m;
+  d.chunks = n / 128;
+  d.G = n / g;
+  d.gi = group_index(g);
+  d.tn = T <= 32 ? 32 : T <= 64 ? 64 : TC_MAX_TN;
+  d.scales = a.W.scales;
+  d.zeros = a.W.zeros;
+  d.bias = static_cast<const uint16_t*>(a.bias);
+  d.residual = static_cast<const uint16_t*>(a.residual);
+  d.ld_res = a.ld_res;
+  d.ldy = a.ld_y;
+  d.Y = a.Y;
+  d.preact = static_cast<uint16_t*>(a.preact);
+  d.act = a.act;
+  d.y_fp32 = a.y_fp32;
+  d.vec = a.ld_y % 4 == 0 && aligned_to(a.Y, a.y_fp32 ? 16 : 8) &&
+          (!a.residual || (a.ld_res % 4 == 0 && aligned_to(a.residual, 8))) &&
+          (!a.preact || (m % 4 == 0 && aligned_to(a.preact, 8)));
+  d.status = static_cast<int*>(a.workspace);
+  CUtensorMap cmap, xmap;
+  gptq_status s = encode_codes(&cmap, a.W);
+  if (s == GPTQ_OK) s = encode_act(&xmap, a.dtype, X, n, T, ldx, d.tn);
+  if (s != GPTQ_OK) return s;
+  TcLaunch l;
+  l.bf16 = a.dtype == GPTQ_BF16;
+  l.unit = std::min(g, 128);
+  const int64_t tiles = static_cast<int64_t>((m + TC_BM - 1) / TC_BM) * ((T + d.tn - 1) / d.tn);
+  l.cluster = 1;
+  while (l.cluster < 8 && tiles * l.cluster * 2 <= kSms && d.chunks >= 4 * l.cluster) l.cluster *= 2;
+  l.device = device;
+  l.stream = st;
+  CK(by_bits(a.W.qp.bits, [&](auto b) { return launch_linear_tc<decltype(b)::value>(l, cmap, xmap, d); }));
+  return GPTQ_OK;
 }
 
 struct MoeLayout {
@@ -129,7 +201,6 @@ extern "C" gptq_status gptq_dequant_linear(const gptq_linear_args* args, int dev
   const int g = group_width(a.W);
   const uint16_t* X = static_cast<const uint16_t*>(a.X);
   int64_t ldx = a.ld_x;
-  LinearDecodeArgs d;
   for (int t0 = 0; a.W.perm && t0 < T; t0 += 65535)
     CK(launch_pdl(gather_x_kernel, dim3((n + 1023) / 1024, std::min(65535, T - t0)), dim3(256), 0, 1, st,
                   X + static_cast<size_t>(t0) * ldx, ldx, n, a.W.perm,
@@ -138,6 +209,8 @@ extern "C" gptq_status gptq_dequant_linear(const gptq_linear_args* args, int dev
     X = reinterpret_cast<const uint16_t*>(ws + 256);
     ldx = n;
   }
+  if (T > kDecodeTokens) return linear_many_tokens(a, X, ldx, device, st);
+  LinearDecodeArgs d;
   d.early = a.W.perm ? 1 : 0;
   d.X = X;
   d.ldx = ldx;

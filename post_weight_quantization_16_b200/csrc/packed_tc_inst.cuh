@@ -1,0 +1,32 @@
+// packed_tc_inst.cuh — the tensor-core kernels of one code width (PACKED_BITS).
+#include "packed_tc.cuh"
+
+namespace gptq {
+
+namespace {
+template <bool BF, int GU>
+cudaError_t linear_tc_of(const TcLaunch& l, const CUtensorMap& codes, const CUtensorMap& x, const LinearTcArgs& a) {
+  static std::atomic<uint64_t> done{0};
+  const auto kernel = linear_tc_kernel<PACKED_BITS, BF, GU>;
+  const cudaError_t e = raise_smem_limit(done, l.device, kernel, TC_SMEM_BUDGET);
+  if (e != cudaSuccess) return e;
+  const dim3 grid(static_cast<unsigned>((a.m + TC_BM - 1) / TC_BM * l.cluster),
+                  static_cast<unsigned>((a.T + a.tn - 1) / a.tn));
+  return launch_pdl(kernel, grid, dim3(TC_THREADS), tc_smem_bytes(a.tn, PACKED_BITS), l.cluster, l.stream, codes, x, a);
+}
+}  // namespace
+
+template <>
+cudaError_t launch_linear_tc<PACKED_BITS>(const TcLaunch& l, const CUtensorMap& codes, const CUtensorMap& x,
+                                          const LinearTcArgs& a) {
+  if (l.bf16) {
+    if (l.unit == 32) return linear_tc_of<true, 32>(l, codes, x, a);
+    if (l.unit == 64) return linear_tc_of<true, 64>(l, codes, x, a);
+    return linear_tc_of<true, 128>(l, codes, x, a);
+  }
+  if (l.unit == 32) return linear_tc_of<false, 32>(l, codes, x, a);
+  if (l.unit == 64) return linear_tc_of<false, 64>(l, codes, x, a);
+  return linear_tc_of<false, 128>(l, codes, x, a);
+}
+
+}  // namespace gptq
