@@ -386,6 +386,36 @@ typedef struct {
 size_t gptq_dequant_linear_workspace_bytes(int64_t T, int64_t n, int act_order);
 gptq_status gptq_dequant_linear(const gptq_linear_args* args, int device, void* cuda_stream);
 
+/* The gradient of the linear layer (W frozen: what adapters and the layers below train on):
+ *   dZ = dY * act'(Z),   dX[:, perm] = dZ W16,   dbias = sum over tokens of dZ
+ * (the residual's gradient is dY).  W16 is the fp16 weight of gptq_dequant_matmul: the sum runs
+ * over the rows, across which the scale varies, so the weights enter as 16-bit values.  dZ enters
+ * as fp16 values scaled by a power of two per token (two values, a high and a low part, when dtype
+ * is fp16 and act is GELU or SiLU); sums are fp32.
+ *   dY       : device, dtype, [T x m], row stride ld_dy >= m; 0 <= T <= 2^22
+ *   preact   : device, dtype, [T x m] contiguous: Z as gptq_dequant_linear gave it; not read when
+ *              act is none
+ *   dX       : device, dtype, [T x n], original column order, row stride ld_dx >= n; or NULL
+ *   dbias    : device fp32 [m], or NULL (zeros when T is 0)
+ *   workspace: as above, gptq_dequant_linear_backward_workspace_bytes
+ * At least one output.  Asynchronous on cuda_stream, capturable, deterministic. */
+typedef struct {
+  const void* dY;
+  int64_t T, ld_dy;
+  int dtype;
+  gptq_packed W;
+  int act;
+  const void* preact;
+  void* dX;
+  int64_t ld_dx;
+  float* dbias;
+  void* workspace;
+  size_t workspace_bytes;
+} gptq_linear_grad_args;
+
+size_t gptq_dequant_linear_backward_workspace_bytes(int64_t T, int64_t m, int64_t n, int act_order, int dtype, int act);
+gptq_status gptq_dequant_linear_backward(const gptq_linear_grad_args* args, int device, void* cuda_stream);
+
 /* The mixture-of-experts layer for a few tokens, experts packed:
  *   p = softmax(X R^T) over the experts (64-bit); a token's top_k experts are those of the largest
  *   p, in descending order, ties to the lower expert (a NaN is chosen last); their weights are p,

@@ -5,6 +5,7 @@
 
 #include "api_common.cuh"
 #include "packed_decode.cuh"
+#include "packed_grad.cuh"
 #include "packed_moe.cuh"
 #include "packed_tc.cuh"
 
@@ -143,6 +144,34 @@ gptq_status linear_many_tokens(const gptq_linear_args& a, const uint16_t* X, int
   return GPTQ_OK;
 }
 
+// What the gradient's product needs in the workspace.
+struct GradLayout {
+  int parts;       // 0: dY itself is the operand, else fp16 values of dz (1, or 2: high and low)
+  int64_t ldz;
+  size_t scale, hi, lo, dx, total;
+};
+bool grad_layout(int64_t T, int64_t m, int64_t n, int act_order, int dtype, int act, bool direct, GradLayout* l) {
+  if (T < 0 || T > kPackedMaxT || m < 1 || m > kPackedMaxM || !valid_width(n) ||
+      (dtype != GPTQ_FP16 && dtype != GPTQ_BF16) || act < GPTQ_ACT_NONE || act > GPTQ_ACT_SILU)
+    return false;
+  const bool smooth = act == GPTQ_ACT_GELU || act == GPTQ_ACT_SILU;
+  l->parts = direct && dtype == GPTQ_FP16 && act == GPTQ_ACT_NONE ? 0 : dtype == GPTQ_FP16 && smooth ? 2 : 1;
+  l->ldz = (m + 7) / 8 * 8;
+  size_t off = 256;  // status word
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off += up256(bytes);
+    return at;
+  };
+  const size_t dz = static_cast<size_t>(T) * l->ldz * 2;
+  l->scale = take(static_cast<size_t>(T) * 4);
+  l->hi = take(l->parts >= 1 ? dz : 0);
+  l->lo = take(l->parts == 2 ? dz : 0);
+  l->dx = take(act_order ? static_cast<size_t>(T) * n * 2 : 0);
+  l->total = off;
+  return true;
+}
+
 struct MoeLayout {
   size_t logits, ids, weights, active, expert, begin, count, pair, pweight, x, h, total;
 };
@@ -240,6 +269,101 @@ extern "C" gptq_status gptq_dequant_linear(const gptq_linear_args* args, int dev
   l.device = device;
   l.stream = st;
   CK(by_bits(a.W.qp.bits, [&](auto b) { return launch_linear_decode<decltype(b)::value>(l, d); }));
+  return GPTQ_OK;
+}
+
+extern "C" size_t gptq_dequant_linear_backward_workspace_bytes(int64_t T, int64_t m, int64_t n, int act_order,
+                                                               int dtype, int act) {
+  GradLayout l;
+  return grad_layout(T, m, n, act_order, dtype, act, false, &l) ? l.total : 0;
+}
+
+extern "C" gptq_status gptq_dequant_linear_backward(const gptq_linear_grad_args* args, int device,
+                                                    void* cuda_stream) {
+  if (!args) return GPTQ_ERR_ARG;
+  const gptq_linear_grad_args& a = *args;
+  GradLayout need, lay;
+  if (!valid_packed(a.W) || !grad_layout(a.T, a.W.m, a.W.n, a.W.perm ? 1 : 0, a.dtype, a.act, false, &need))
+    return GPTQ_ERR_ARG;
+  if (!a.dX && !a.dbias) return GPTQ_ERR_ARG;
+  if (!aligned_to(a.dbias, 4) || (a.T > 0 && a.ld_dy < a.W.m) || (a.T > 0 && a.dX && a.ld_dx < a.W.n) ||
+      !aligned_to(a.dX, 2))
+    return GPTQ_ERR_ARG;
+  if (a.T > 0 && (!a.dY || !aligned_to(a.dY, 2) || !a.workspace || !aligned256(a.workspace) ||
+                  a.workspace_bytes < need.total))
+    return GPTQ_ERR_ARG;
+  if (a.T > 0 && a.act != GPTQ_ACT_NONE && (!a.preact || !aligned_to(a.preact, 2))) return GPTQ_ERR_ARG;
+  if (a.T == 0 && !a.dbias) return GPTQ_OK;
+  const gptq_status ds = check_device(device);
+  if (ds != GPTQ_OK) return ds;
+  DeviceGuard dg(device);
+  cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  if (a.T == 0) {
+    CK(cudaMemsetAsync(a.dbias, 0, static_cast<size_t>(a.W.m) * 4, st));
+    return GPTQ_OK;
+  }
+  const bool bf = a.dtype == GPTQ_BF16;
+  const int T = static_cast<int>(a.T), m = static_cast<int>(a.W.m), n = static_cast<int>(a.W.n);
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  const uint16_t* dY = static_cast<const uint16_t*>(a.dY);
+  const uint16_t* Z = a.act == GPTQ_ACT_NONE ? nullptr : static_cast<const uint16_t*>(a.preact);
+  if (a.dbias)
+    CK(launch_pdl(bf ? dbias_kernel<true> : dbias_kernel<false>, dim3((m + 127) / 128 * DBIAS_CLUSTER), dim3(256), 0,
+                  DBIAS_CLUSTER, st, dY, a.ld_dy, Z, T, m, a.act, a.dbias));
+  if (!a.dX) return GPTQ_OK;
+  // dY is the operand itself when it is fp16, nothing is to be multiplied and TMA can read it
+  const bool direct = aligned16(dY) && a.ld_dy % 8 == 0;
+  grad_layout(a.T, m, n, a.W.perm ? 1 : 0, a.dtype, a.act, direct, &lay);
+  const uint16_t *hi = dY, *lo = dY;
+  int64_t ldz = a.ld_dy;
+  if (lay.parts >= 1) {
+    uint16_t* h = reinterpret_cast<uint16_t*>(ws + lay.hi);
+    uint16_t* o = lay.parts == 2 ? reinterpret_cast<uint16_t*>(ws + lay.lo) : nullptr;
+    ldz = lay.ldz;
+    CK(launch_pdl(bf ? act_grad_kernel<true> : act_grad_kernel<false>, dim3(T), dim3(256), 0, 1, st, dY, a.ld_dy, Z, m,
+                  a.act, h, o, ldz, reinterpret_cast<float*>(ws + lay.scale)));
+    hi = h;
+    lo = o ? o : h;
+  }
+  LinearBwdArgs d;
+  const int g = group_width(a.W);
+  d.T = T;
+  d.m = m;
+  d.n = n;
+  d.G = n / g;
+  d.gi = group_index(g);
+  d.parts = std::max(1, lay.parts);
+  d.tn = T <= 32 ? 32 : T <= 64 ? 64 : T <= 128 ? 128 : 256;
+  while (d.tn > 32 && bw_stages(d.tn, a.W.qp.bits, d.parts) < 2) d.tn /= 2;
+  d.row_chunks = (m + 127) / 128;
+  d.scales = a.W.scales;
+  d.zeros = a.W.zeros;
+  d.token_scale = lay.parts >= 1 ? reinterpret_cast<const float*>(ws + lay.scale) : nullptr;
+  d.dX = a.W.perm ? reinterpret_cast<uint16_t*>(ws + lay.dx) : static_cast<uint16_t*>(a.dX);
+  d.lddx = a.W.perm ? n : a.ld_dx;
+  d.bf16_out = bf ? 1 : 0;
+  d.vec = d.lddx % 4 == 0 && aligned_to(d.dX, 8);
+  d.status = reinterpret_cast<int*>(ws);
+  CUtensorMap cmap, hmap, lmap;
+  gptq_status s = encode_codes(&cmap, a.W);
+  if (s == GPTQ_OK) s = encode_act(&hmap, GPTQ_FP16, hi, m, T, ldz, d.tn);
+  if (s == GPTQ_OK) s = encode_act(&lmap, GPTQ_FP16, lo, m, T, ldz, d.tn);
+  if (s != GPTQ_OK) return s;
+  TcLaunch l;
+  l.bf16 = bf;
+  l.unit = std::min(g, 128);
+  const int64_t tiles = static_cast<int64_t>(n / 128) * ((T + d.tn - 1) / d.tn);
+  l.cluster = 1;
+  while (l.cluster < 8 && tiles * l.cluster * 2 <= kSms && d.row_chunks >= 4 * l.cluster) l.cluster *= 2;
+  l.device = device;
+  l.stream = st;
+  CK(by_bits(a.W.qp.bits, [&](auto b) { return launch_linear_bwd_tc<decltype(b)::value>(l, cmap, hmap, lmap, d); }));
+  if (a.W.perm) {
+    static std::atomic<uint64_t> done{0};
+    CK(raise_smem_limit(done, device, unpermute_kernel, static_cast<int>(kPackedMaxN) * 2));
+    CK(launch_pdl(unpermute_kernel, dim3(T), dim3(256), static_cast<size_t>(n) * 2, 1, st,
+                  static_cast<const uint16_t*>(d.dX), n, a.W.perm, static_cast<uint16_t*>(a.dX), a.ld_dx));
+  }
   return GPTQ_OK;
 }
 

@@ -406,6 +406,292 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
 }
 
 // ------------------------------------------------------------------------------------------
+// the gradient
+// ------------------------------------------------------------------------------------------
+//     dX[t][perm[k]] = scale_t * sum over rows r of W16[r][k] * dz[t][r],
+//     W16 = fp16( fp32(u - z) * s ),   dz[t][r] = dY[t][r] act'(Z[t][r]) / scale_t  in fp16
+// The sum runs over the rows, across which the scale varies, so the weights enter as their fp16
+// values (the library's dequantized weight) and both operands are fp16 whatever the type of the
+// activations: bf16 operands would lose three more bits of each.  scale_t is a power of two per
+// token that puts the token's largest dY at 2^13 or above, so the range of bf16 gradients fits.
+// With fp16 activations and a smooth act' the rounding of dz would be as large as that of dX
+// itself: dz then comes as a sum of two fp16 values (parts = 2) and each chunk takes two MMAs.
+//
+// One block = 128 columns of W (the MMA's M; the operand is read transposed, MN-major, straight
+// from the row-wise unpacked tile) x TN tokens, over a range of rows in chunks of 128.  Everything
+// accumulates in one tensor-memory buffer.  Roles as in the forward kernel, without a drain loop.
+constexpr int BW_THREADS = 10 * 32;
+constexpr int BW_MAX_TN = 256;
+
+__host__ __device__ inline int bw_stage_bytes(int tn, int bits, int parts) {
+  return tc_code_bytes(bits) + parts * tn * 256;
+}
+__host__ __device__ inline int bw_stages(int tn, int bits, int parts) {
+  const int s = (TC_SMEM_BUDGET - 2048 - TC_NA * TC_A_BYTES) / bw_stage_bytes(tn, bits, parts);
+  return s > 8 ? 8 : s;
+}
+__host__ __device__ inline int bw_smem_bytes(int tn, int bits, int parts) {
+  return 2048 + TC_NA * TC_A_BYTES + bw_stages(tn, bits, parts) * bw_stage_bytes(tn, bits, parts);
+}
+
+struct LinearBwdArgs {
+  int T, m, n, G, tn, parts;
+  int row_chunks;  // ceil(m / 128)
+  GroupIndex gi;
+  const float *scales, *zeros;
+  const float* token_scale;  // [T] or null (1)
+  uint16_t* dX;              // [T x n], sweep order
+  int64_t lddx;
+  int bf16_out;
+  int vec;  // dX allows 8-byte accesses
+  int* status;
+};
+
+// Eight codes -> their fp16 weights, adjacent pairs in order.  f + nzm is u - z exactly (2^23 + u
+// minus 2^23 + z), times s rounded to nearest in fp32, then to nearest fp16.
+template <int BITS>
+__device__ __forceinline__ void dequant8(uint32_t v, uint32_t v1, float2 nzm, float2 ss, uint32_t (&out)[4]) {
+  uint32_t f[8];
+  if (BITS == 4) {
+    const uint32_t ev = v & 0x0F0F0F0Fu, od = (v >> 4) & 0x0F0F0F0Fu;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __byte_perm(ev, 0x4B000000u, 0x7540u + i);
+      f[2 * i + 1] = __byte_perm(od, 0x4B000000u, 0x7540u + i);
+    }
+  } else if (BITS == 8) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = __byte_perm(i < 4 ? v : v1, 0x4B000000u, 0x7540u + (i & 3));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = ((v >> (BITS * i)) & ((1u << BITS) - 1u)) | 0x4B000000u;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 d = __fmul2_rn(
+        __fadd2_rn(make_float2(__uint_as_float(f[2 * i]), __uint_as_float(f[2 * i + 1])), nzm), ss);
+    out[i] = pack2<false>(d.x, d.y);
+  }
+}
+
+template <int BITS, int GU>
+__global__ void __launch_bounds__(BW_THREADS, 1)
+    linear_bwd_tc_kernel(const __grid_constant__ CUtensorMap codes_map, const __grid_constant__ CUtensorMap dz_map,
+                         const __grid_constant__ CUtensorMap dzlo_map, const LinearBwdArgs p) {
+  extern __shared__ uint8_t tc_smem_raw[];
+  const uint32_t raw_s = smem_u32(tc_smem_raw);
+  uint8_t* smem = tc_smem_raw + (((raw_s + 1023u) & ~1023u) - raw_s);
+  const uint32_t sbase = smem_u32(smem);
+  const int tn = p.tn, parts = p.parts;
+  const int stages = bw_stages(tn, BITS, parts);
+  const int stage_bytes = bw_stage_bytes(tn, BITS, parts);
+  const uint32_t a_base = sbase;
+  const uint32_t st_base = sbase + TC_NA * TC_A_BYTES;  // stages: dz atoms | (low part's atoms) | codes
+  const int code_off = parts * tn * 256;
+  const uint32_t bar = st_base + stages * stage_bytes;
+  const uint32_t bar_full = bar, bar_empty = bar + 64, bar_afull = bar + 128, bar_aempty = bar_afull + 8 * TC_NA,
+                 bar_acc = bar_aempty + 8 * TC_NA, bar_drain = bar_acc + 8;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + (bar_drain + 8 - sbase));
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int cs = static_cast<int>(cluster_nctarank()), rank = static_cast<int>(cluster_ctarank());
+  const int kc = static_cast<int>(blockIdx.x) / cs;  // chunk of 128 columns
+  const int t0 = static_cast<int>(blockIdx.y) * tn;
+  const int rc0 = static_cast<int>(static_cast<int64_t>(p.row_chunks) * rank / cs);
+  const int nk = static_cast<int>(static_cast<int64_t>(p.row_chunks) * (rank + 1) / cs) - rc0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(bar_full + 8 * s, 1);
+      mbar_init(bar_empty + 8 * s, 1);
+    }
+    for (int j = 0; j < TC_NA; ++j) {
+      mbar_init(bar_afull + 8 * j, 8);
+      mbar_init(bar_aempty + 8 * j, 1);
+    }
+    mbar_init(bar_acc, 1);
+    mbar_init(bar_drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), static_cast<uint32_t>(tn));
+    tmem_relinquish();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&codes_map);
+    tma_prefetch_desc(&dz_map);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  griddep_wait();
+  griddep_launch_dependents();
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) atomicExch(p.status, 0);
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int issued = 0;
+      for (int i = 0; i < nk; ++i) {
+        const int s = i % stages;
+        if (!mbar_wait_bounded(bar_empty + 8 * s, (static_cast<uint32_t>(i / stages) & 1u) ^ 1u, abort_flag)) break;
+        const uint32_t fb = bar_full + 8 * s, st = st_base + s * stage_bytes;
+        mbar_arrive_expect_tx(fb, static_cast<uint32_t>(stage_bytes));
+        const int r0 = (rc0 + i) * 128;
+        tma_load_2d(st + code_off, &codes_map, fb, kc * (TC_BK * BITS / 32), r0);
+        tma_load_2d(st, &dz_map, fb, r0, t0);
+        tma_load_2d(st + tn * 128, &dz_map, fb, r0 + 64, t0);
+        if (parts == 2) {
+          tma_load_2d(st + tn * 256, &dzlo_map, fb, r0, t0);
+          tma_load_2d(st + tn * 384, &dzlo_map, fb, r0 + 64, t0);
+        }
+        issued = i + 1;
+      }
+      for (int i = max(0, issued - stages); i < issued; ++i)
+        mbar_wait_drain(bar_full + 8 * (i % stages), static_cast<uint32_t>(i / stages) & 1u);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = idesc_make(0u, 0u, 1u, 0u, TC_BM, static_cast<uint32_t>(tn));  // f16; A is MN-major
+      bool ok = true;
+      for (int i = 0; i < nk; ++i) {
+        const int s = i % stages, j = i % TC_NA;
+        if (!mbar_wait_bounded(bar_full + 8 * s, static_cast<uint32_t>(i / stages) & 1u, abort_flag) ||
+            !mbar_wait_bounded(bar_afull + 8 * j, static_cast<uint32_t>(i / TC_NA) & 1u, abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t a_t = a_base + j * TC_A_BYTES, x_t = st_base + s * stage_bytes;
+        for (int part = 0; part < parts; ++part) {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            // 16 rows = two 8-row swizzle atoms of 1024 bytes; the 64-column halves 16 KB apart
+            const uint64_t ad = sdesc_sw128(a_t + kk * 2048, TC_ATOM, 1024);
+            const uint64_t bd = sdesc_sw128(x_t + part * (tn * 256) + (kk >> 2) * (tn * 128) + (kk & 3) * 32, 16, 1024);
+            umma_f16(tmem_base, ad, bd, idesc, (i > 0 || part > 0 || kk > 0) ? 1u : 0u);
+          }
+        }
+        umma_commit(bar_empty + 8 * s);
+        umma_commit(bar_aempty + 8 * j);
+      }
+      if (ok) {
+        umma_commit(bar_acc);
+      } else {
+        umma_commit(bar_drain);
+        mbar_wait_drain(bar_drain, 0);
+      }
+    }
+  } else {
+    // ---------------- unpack: two threads per row of W, 64 columns each ----------------
+    const int d = threadIdx.x - 64, r = d >> 1, h = d & 1, r7 = r & 7;
+    constexpr int ZN = GU == 32 ? 2 : 1;
+    auto load_sz = [&](int rc, float (&s)[ZN], float (&z)[ZN]) {
+      const int gr = rc * 128 + r;
+#pragma unroll
+      for (int j = 0; j < ZN; ++j) {
+        const size_t at = static_cast<size_t>(min(gr, p.m - 1)) * p.G +
+                          group_of<GU>(p.gi, kc, GU == 128 ? 0 : GU == 64 ? h : 2 * h + j);
+        s[j] = gr < p.m ? __ldg(p.scales + at) : 0.0f;  // rows past m: zero weights
+        z[j] = gr < p.m ? __ldg(p.zeros + at) : 0.0f;
+      }
+    };
+    float ns[ZN], nz[ZN];
+    if (nk > 0) load_sz(rc0, ns, nz);
+    bool ok = true;
+    for (int i = 0; i < nk; ++i) {
+      float2 ss[ZN], nzm[ZN];
+#pragma unroll
+      for (int j = 0; j < ZN; ++j) {
+        ss[j] = make_float2(ns[j], ns[j]);
+        nzm[j] = make_float2(-8388608.0f - nz[j], -8388608.0f - nz[j]);
+      }
+      if (i + 1 < nk) load_sz(rc0 + i + 1, ns, nz);
+      const int s = i % stages, j = i % TC_NA;
+      if (!warp_wait(bar_full + 8 * s, static_cast<uint32_t>(i / stages) & 1u, abort_flag, lane) ||
+          !warp_wait(bar_aempty + 8 * j, (static_cast<uint32_t>(i / TC_NA) & 1u) ^ 1u, abort_flag, lane)) {
+        ok = false;
+        break;
+      }
+      uint32_t w[2 * BITS];
+      load_half_row<BITS>(smem + (st_base - sbase) + s * stage_bytes + code_off, r, h, w);
+      const uint32_t dst = a_base + j * TC_A_BYTES + h * TC_ATOM + r * 128;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        uint32_t v, v1, q[4];
+        half_row_block<BITS>(w, c, v, v1);
+        dequant8<BITS>(v, v1, nzm[GU == 32 ? c >> 2 : 0], ss[GU == 32 ? c >> 2 : 0], q);
+        st_shared_v4(dst + ((c ^ r7) << 4), q[0], q[1], q[2], q[3]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_afull + 8 * j);
+    }
+    // accumulator -> [token][column] sums over the operand tiles
+    if (ok && nk > 0) ok = warp_wait(bar_acc, 0u, abort_flag, lane);
+    if (ok) {
+      tc_fence_after();
+      const int qd = warp & 3, half = (warp - 2) >> 2, col = qd * 32 + lane;
+      float* sums = reinterpret_cast<float*>(smem);
+      for (int cc = half; cc < tn / 16; cc += 2) {
+        uint32_t v[16];
+        if (nk > 0) {
+          tmem_ld_32x32b_x16(tmem_base + (static_cast<uint32_t>(qd * 32) << 16) + static_cast<uint32_t>(cc * 16), v);
+          tmem_ld_wait();
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j) sums[(cc * 16 + j) * TC_BM + col] = nk > 0 ? __uint_as_float(v[j]) : 0.0f;
+      }
+      tc_fence_before();
+    }
+  }
+
+  __syncthreads();
+  if (cs > 1) cluster_sync();
+  if (!*abort_flag) {
+    for (int t = rank + cs * warp; t < tn; t += cs * (BW_THREADS / 32)) {
+      const int tok = t0 + t;
+      if (tok >= p.T) continue;
+      const uint32_t at = sbase + static_cast<uint32_t>((t * TC_BM + 4 * lane) * 4);
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int o = 0; o < cs; ++o) {
+        const float4 w = cs > 1 ? ld_dsmem_f4(mapa_shared(at, o)) : *reinterpret_cast<const float4*>(smem + (at - sbase));
+        v.x += w.x;
+        v.y += w.y;
+        v.z += w.z;
+        v.w += w.w;
+      }
+      if (p.token_scale) {
+        const float s = p.token_scale[tok];
+        v.x *= s;
+        v.y *= s;
+        v.z *= s;
+        v.w *= s;
+      }
+      uint16_t* d = p.dX + static_cast<size_t>(tok) * p.lddx + kc * 128 + 4 * lane;
+      const uint32_t lo = p.bf16_out ? pack2<true>(v.x, v.y) : pack2<false>(v.x, v.y);
+      const uint32_t hi = p.bf16_out ? pack2<true>(v.z, v.w) : pack2<false>(v.z, v.w);
+      if (p.vec) {
+        *reinterpret_cast<uint2*>(d) = make_uint2(lo, hi);
+      } else {
+        d[0] = static_cast<uint16_t>(lo);
+        d[1] = static_cast<uint16_t>(lo >> 16);
+        d[2] = static_cast<uint16_t>(hi);
+        d[3] = static_cast<uint16_t>(hi >> 16);
+      }
+    }
+  }
+  if (cs > 1) cluster_sync();
+  if (threadIdx.x == 0 && *abort_flag) atomicOr(p.status, ST_TIMEOUT);
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, static_cast<uint32_t>(tn));
+  }
+}
+
+// ------------------------------------------------------------------------------------------
 // launches, one translation unit per code width (packed_tc_inst.cuh)
 // ------------------------------------------------------------------------------------------
 struct TcLaunch {
@@ -418,5 +704,8 @@ struct TcLaunch {
 
 template <int BITS>
 cudaError_t launch_linear_tc(const TcLaunch& l, const CUtensorMap& codes, const CUtensorMap& x, const LinearTcArgs& a);
+template <int BITS>
+cudaError_t launch_linear_bwd_tc(const TcLaunch& l, const CUtensorMap& codes, const CUtensorMap& dz,
+                                 const CUtensorMap& dz_lo, const LinearBwdArgs& a);
 
 }  // namespace gptq

@@ -61,6 +61,13 @@ class LinearArgs(ctypes.Structure):
                 ("workspace_bytes", ctypes.c_size_t)]
 
 
+class LinearGradArgs(ctypes.Structure):
+    _fields_ = [("dY", ctypes.c_void_p), ("T", ctypes.c_int64), ("ld_dy", ctypes.c_int64), ("dtype", ctypes.c_int),
+                ("W", PackedLayer), ("act", ctypes.c_int), ("preact", ctypes.c_void_p), ("dX", ctypes.c_void_p),
+                ("ld_dx", ctypes.c_int64), ("dbias", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_size_t)]
+
+
 class MoeArgs(ctypes.Structure):
     _fields_ = [("X", ctypes.c_void_p), ("T", ctypes.c_int64), ("ld_x", ctypes.c_int64), ("dtype", ctypes.c_int),
                 ("router", ctypes.c_void_p), ("E", ctypes.c_int64), ("top_k", ctypes.c_int),
@@ -101,6 +108,10 @@ _SIGS = {
     "gptq_dequant_matmul_check": (ctypes.c_int, [_P, ctypes.c_int, _P]),
     "gptq_dequant_linear_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int]),
     "gptq_dequant_linear": (ctypes.c_int, [ctypes.POINTER(LinearArgs), ctypes.c_int, _P]),
+    "gptq_dequant_linear_backward_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64,
+                                                                       ctypes.c_int64, ctypes.c_int, ctypes.c_int,
+                                                                       ctypes.c_int]),
+    "gptq_dequant_linear_backward": (ctypes.c_int, [ctypes.POINTER(LinearGradArgs), ctypes.c_int, _P]),
     "gptq_dequant_moe_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int,
                                                            ctypes.c_int64, ctypes.c_int64, ctypes.c_int]),
     "gptq_dequant_moe": (ctypes.c_int, [ctypes.POINTER(MoeArgs), ctypes.c_int, _P]),
@@ -443,6 +454,47 @@ def dequant_linear(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, z
                        int(y_type == torch.float32), None if z is None else z.data_ptr(), ws.data_ptr(), ws.numel())
         _check(lib().gptq_dequant_linear(ctypes.byref(a), dev.index, handle), "gptq_dequant_linear")
     return (out, z) if want_preact else out
+
+
+def dequant_linear_backward(dY: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor,
+                            perm: torch.Tensor | None, bits: int, group_size: int, act: int = ACT_NONE,
+                            preact: torch.Tensor | None = None, want_dx: bool = True, want_dbias: bool = False,
+                            out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                            stream: torch.cuda.Stream | None = None):
+    """The gradient of dequant_linear with W frozen (gptq_dequant_linear_backward).  dY: fp16 or bf16
+    [T, m]; preact: the Z that dequant_linear(want_preact=True) gave (needed unless act is ACT_NONE).
+    Returns dX [T, n] in dY's type, or (dX, dbias) with want_dbias (dbias fp32 [m]; dX is None with
+    want_dx=False).  The residual's gradient is dY itself.  Asynchronous on `stream`."""
+    dev = dY.device
+    W = _packed(codes, scales, zeros, perm, bits, group_size, dev)
+    m, n = W.m, W.n
+    if dY.dim() != 2 or dY.shape[1] != m or dY.dtype not in _DTYPES or not dY.is_cuda:
+        raise ValueError(f"dY must be an fp16 or bf16 [T, {m}] device tensor")
+    T = dY.shape[0]
+    dy_ptr, ld_dy = _rows("dY", dY, (T, m), dY.dtype, dev)
+    z_ptr = None
+    if act != ACT_NONE:
+        if preact is None or preact.dtype != dY.dtype or preact.shape != (T, m) or not preact.is_contiguous() \
+                or preact.device != dev:
+            raise ValueError(f"preact must be a contiguous {dY.dtype} [{T}, {m}] tensor on {dev}")
+        z_ptr = preact.data_ptr()
+    if not (want_dx or want_dbias):
+        raise ValueError("nothing to compute: want_dx and want_dbias are both off")
+    dt = _DTYPES[dY.dtype]
+    with _on(dev, stream) as handle:
+        dx = None
+        if want_dx:
+            dx = torch.empty((T, n), dtype=dY.dtype, device=dev) if out is None else out
+        dx_ptr, ld_dx = _rows("out", dx, (T, n), dY.dtype, dev)
+        db = torch.empty(m, dtype=torch.float32, device=dev) if want_dbias else None
+        need = int(lib().gptq_dequant_linear_backward_workspace_bytes(T, m, n, int(perm is not None), dt, int(act)))
+        if need == 0:
+            raise GPTQError(ERR_ARG, "gptq_dequant_linear_backward_workspace_bytes")
+        ws = _workspace(need, workspace, dev)
+        a = LinearGradArgs(dy_ptr, T, ld_dy, dt, W, int(act), z_ptr, dx_ptr, ld_dx, None if db is None else db.data_ptr(),
+                           ws.data_ptr(), ws.numel())
+        _check(lib().gptq_dequant_linear_backward(ctypes.byref(a), dev.index, handle), "gptq_dequant_linear_backward")
+    return (dx, db) if want_dbias else dx
 
 
 def dequant_moe(X: torch.Tensor, router: torch.Tensor, gate_up: tuple, down: tuple, perm: torch.Tensor | None,
