@@ -452,7 +452,7 @@ typedef struct {
   size_t workspace_bytes;
 } gptq_moe_args;
 
-size_t gptq_dequant_moe_workspace_bytes(int64_t T, int64_t E, int top_k, int64_t H, int64_t I, int act_order);
+size_t gptq_dequant_moe_workspace_bytes(int64_t T, int64_t E, int top_k, int64_t H, int64_t I);
 gptq_status gptq_dequant_moe(const gptq_moe_args* args, int device, void* cuda_stream);
 
 /* ---------------------------------------------------------------------------------------

@@ -36,7 +36,6 @@ int group_width(const gptq_packed& w) { return w.qp.group_size == -1 ? static_ca
 
 GroupIndex group_index(int g) {
   GroupIndex gi;
-  gi.units_per_chunk_shift = g == 32 ? 2 : g == 64 ? 1 : 0;
   gi.div = g >= 128 ? g / 128 : 1;
   gi.magic = gi.div > 1 ? static_cast<uint32_t>(((uint64_t(1) << 32) + gi.div - 1) / gi.div) : 0u;
   return gi;
@@ -61,20 +60,21 @@ cudaError_t by_bits(int bits, F&& f) {
   }
 }
 
-// Blocks of a cluster that split k: enough that `tiles` row tiles give every SM about two blocks,
-// while a warp keeps at least one chunk.
+// Blocks of a cluster that split k: as many as two blocks per SM allow for `tiles` row tiles, each
+// with at least two chunks.
 int k_split(int64_t tiles, int chunks) {
   int cs = 1;
-  while (cs < 8 && tiles * cs < 2 * kSms && chunks >= 2 * cs * DEC_WARPS) cs *= 2;
+  while (cs < 8 && tiles * (cs + 1) <= 2 * kSms && chunks >= 2 * (cs + 1)) ++cs;
   return cs;
-}
-
-size_t linear_workspace(int64_t T, int64_t n, int act_order) {
-  return 256 + (act_order ? up256(static_cast<size_t>(T) * n * 2) : 0);
 }
 
 // Tokens up to which the warp-level kernel runs; beyond, tcgen05.
 constexpr int kDecodeTokens = 16;
+
+size_t linear_workspace(int64_t T, int64_t n, int act_order) {
+  const size_t rows = T <= kDecodeTokens ? static_cast<size_t>((T + 7) / 8 * 8) : act_order ? static_cast<size_t>(T) : 0;
+  return 256 + up256(rows * n * 2);
+}
 
 // Row-major 2-D tensor map: `cols` x `rows` elements of a type, boxes of box_cols x box_rows.
 gptq_status encode_map(CUtensorMap* map, CUtensorMapDataType type, int elem, const void* base, int64_t cols,
@@ -91,9 +91,10 @@ gptq_status encode_map(CUtensorMap* map, CUtensorMapDataType type, int elem, con
              : GPTQ_ERR_CUDA;
 }
 
-gptq_status encode_codes(CUtensorMap* map, const gptq_packed& w) {
+// The codes of `layers` stacked matrices, boxes of one 128-column chunk of box_rows rows.
+gptq_status encode_codes(CUtensorMap* map, const gptq_packed& w, int box_rows, int64_t layers = 1) {
   const int64_t words = w.n * w.qp.bits / 32;
-  return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, w.codes, words, w.m, words, 4 * w.qp.bits, TC_BM,
+  return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, w.codes, words, w.m * layers, words, 4 * w.qp.bits, box_rows,
                     CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 gptq_status encode_act(CUtensorMap* map, int dtype, const void* base, int64_t cols, int64_t rows, int64_t ld,
@@ -129,7 +130,7 @@ gptq_status linear_many_tokens(const gptq_linear_args& a, const uint16_t* X, int
           (!a.preact || (m % 4 == 0 && aligned_to(a.preact, 8)));
   d.status = static_cast<int*>(a.workspace);
   CUtensorMap cmap, xmap;
-  gptq_status s = encode_codes(&cmap, a.W);
+  gptq_status s = encode_codes(&cmap, a.W, TC_BM);
   if (s == GPTQ_OK) s = encode_act(&xmap, a.dtype, X, n, T, ldx, d.tn);
   if (s != GPTQ_OK) return s;
   TcLaunch l;
@@ -172,10 +173,14 @@ bool grad_layout(int64_t T, int64_t m, int64_t n, int act_order, int dtype, int 
   return true;
 }
 
+// Tiles of a segment for T tokens: an expert gets a token at most once.
+int moe_nt(int64_t T) { return T <= 8 ? 1 : T <= 16 ? 2 : 4; }
+
 struct MoeLayout {
-  size_t logits, ids, weights, active, expert, begin, count, pair, pweight, x, h, total;
+  int max_segments, max_tiles;
+  size_t logits, ids, weights, segments, tiles, expert, begin, count, tile0, tile_seg, pair, pweight, x, h, total;
 };
-bool moe_layout(int64_t T, int64_t E, int64_t top_k, int64_t H, int64_t I, int act_order, MoeLayout* l) {
+bool moe_layout(int64_t T, int64_t E, int64_t top_k, int64_t H, int64_t I, MoeLayout* l) {
   if (T < 0 || T > MOE_MAX_T || E < 1 || E > MOE_MAX_E || top_k < 1 || top_k > E || top_k > MOE_MAX_TOPK ||
       !valid_width(H) || !valid_width(I))
     return false;
@@ -185,18 +190,24 @@ bool moe_layout(int64_t T, int64_t E, int64_t top_k, int64_t H, int64_t I, int a
     off += up256(bytes);
     return at;
   };
-  const size_t pairs = static_cast<size_t>(T) * top_k;
+  const int64_t pairs = T * top_k;
+  // experts with a token, and what more than one segment (tile) of an expert adds
+  l->max_segments = static_cast<int>(std::min(pairs, std::min(E, pairs) + pairs / (8 * moe_nt(T))));
+  l->max_tiles = static_cast<int>(std::min(pairs, std::min(E, pairs) + pairs / 8));
   l->logits = take(static_cast<size_t>(T) * E * 8);
   l->ids = take(pairs * 4);
   l->weights = take(pairs * 4);
-  l->active = take(4);
-  l->expert = take(E * 4);
-  l->begin = take(E * 4);
-  l->count = take(E * 4);
+  l->segments = take(4);
+  l->tiles = take(4);
+  l->expert = take(l->max_segments * 4);
+  l->begin = take(l->max_segments * 4);
+  l->count = take(l->max_segments * 4);
+  l->tile0 = take(l->max_segments * 4);
+  l->tile_seg = take(l->max_tiles * 4);
   l->pair = take(pairs * 4);
   l->pweight = take(pairs * 4);
-  l->x = take(act_order ? pairs * H * 2 : 0);
-  l->h = take(pairs * I * 2);
+  l->x = take(static_cast<size_t>(l->max_tiles) * (H / 128) * FRAG_BYTES);
+  l->h = take(static_cast<size_t>(l->max_tiles) * (I / 128) * FRAG_BYTES);
   l->total = off;
   return true;
 }
@@ -230,27 +241,26 @@ extern "C" gptq_status gptq_dequant_linear(const gptq_linear_args* args, int dev
   const int g = group_width(a.W);
   const uint16_t* X = static_cast<const uint16_t*>(a.X);
   int64_t ldx = a.ld_x;
-  for (int t0 = 0; a.W.perm && t0 < T; t0 += 65535)
-    CK(launch_pdl(gather_x_kernel, dim3((n + 1023) / 1024, std::min(65535, T - t0)), dim3(256), 0, 1, st,
-                  X + static_cast<size_t>(t0) * ldx, ldx, n, a.W.perm,
-                  reinterpret_cast<uint16_t*>(ws + 256) + static_cast<size_t>(t0) * n));
-  if (a.W.perm) {
-    X = reinterpret_cast<const uint16_t*>(ws + 256);
-    ldx = n;
+  if (T > kDecodeTokens) {
+    if (a.W.perm) {
+      uint16_t* xs = reinterpret_cast<uint16_t*>(ws + 256);
+      for (int t0 = 0; t0 < T; t0 += 65535)
+        CK(launch_pdl(gather_x_kernel, dim3((n + 1023) / 1024, std::min(65535, T - t0)), dim3(256), 0, 1, st,
+                      X + static_cast<size_t>(t0) * ldx, ldx, n, a.W.perm, xs + static_cast<size_t>(t0) * n));
+      X = xs;
+      ldx = n;
+    }
+    return linear_many_tokens(a, X, ldx, device, st);
   }
-  if (T > kDecodeTokens) return linear_many_tokens(a, X, ldx, device, st);
   LinearDecodeArgs d;
-  d.early = a.W.perm ? 1 : 0;
-  d.X = X;
-  d.ldx = ldx;
-  d.codes = a.W.codes;
-  d.scales = a.W.scales;
-  d.zeros = a.W.zeros;
   d.T = T;
+  d.tiles = (T + 7) / 8;
   d.m = m;
   d.chunks = n / 128;
   d.G = n / g;
   d.gi = group_index(g);
+  d.scales = a.W.scales;
+  d.zeros = a.W.zeros;
   d.bias = static_cast<const uint16_t*>(a.bias);
   d.residual = static_cast<const uint16_t*>(a.residual);
   d.ld_res = a.ld_res;
@@ -260,15 +270,20 @@ extern "C" gptq_status gptq_dequant_linear(const gptq_linear_args* args, int dev
   d.act = a.act;
   d.y_fp32 = a.y_fp32;
   d.status = reinterpret_cast<int*>(ws);
+  d.x = ws + 256;
   DecodeLaunch l;
   l.bf16 = a.dtype == GPTQ_BF16;
   l.unit = std::min(g, 128);
-  l.nt = T <= 8 ? 1 : 2;
-  l.rt = 1;
-  l.cluster = k_split((m + 15) / 16, d.chunks);
+  l.nt = d.tiles <= 2 ? d.tiles : 4;
+  l.cluster = k_split((m + DEC_ROWS - 1) / DEC_ROWS, d.chunks);
   l.device = device;
   l.stream = st;
-  CK(by_bits(a.W.qp.bits, [&](auto b) { return launch_linear_decode<decltype(b)::value>(l, d); }));
+  CUtensorMap cmap;
+  const gptq_status s = encode_codes(&cmap, a.W, 64);
+  if (s != GPTQ_OK) return s;
+  CK(launch_pdl(fragment_kernel, dim3(d.chunks, d.tiles), dim3(128), 0, 1, st, X, ldx, T, l.unit, a.W.perm,
+                reinterpret_cast<uint4*>(ws + 256), d.status));
+  CK(by_bits(a.W.qp.bits, [&](auto b) { return launch_linear_decode<decltype(b)::value>(l, cmap, d); }));
   return GPTQ_OK;
 }
 
@@ -345,7 +360,7 @@ extern "C" gptq_status gptq_dequant_linear_backward(const gptq_linear_grad_args*
   d.vec = d.lddx % 4 == 0 && aligned_to(d.dX, 8);
   d.status = reinterpret_cast<int*>(ws);
   CUtensorMap cmap, hmap, lmap;
-  gptq_status s = encode_codes(&cmap, a.W);
+  gptq_status s = encode_codes(&cmap, a.W, TC_BM);
   if (s == GPTQ_OK) s = encode_act(&hmap, GPTQ_FP16, hi, m, T, ldz, d.tn);
   if (s == GPTQ_OK) s = encode_act(&lmap, GPTQ_FP16, lo, m, T, ldz, d.tn);
   if (s != GPTQ_OK) return s;
@@ -367,10 +382,9 @@ extern "C" gptq_status gptq_dequant_linear_backward(const gptq_linear_grad_args*
   return GPTQ_OK;
 }
 
-extern "C" size_t gptq_dequant_moe_workspace_bytes(int64_t T, int64_t E, int top_k, int64_t H, int64_t I,
-                                                   int act_order) {
+extern "C" size_t gptq_dequant_moe_workspace_bytes(int64_t T, int64_t E, int top_k, int64_t H, int64_t I) {
   MoeLayout l;
-  return moe_layout(T, E, top_k, H, I, act_order, &l) ? l.total : 0;
+  return moe_layout(T, E, top_k, H, I, &l) ? l.total : 0;
 }
 
 extern "C" gptq_status gptq_dequant_moe(const gptq_moe_args* args, int device, void* cuda_stream) {
@@ -381,7 +395,7 @@ extern "C" gptq_status gptq_dequant_moe(const gptq_moe_args* args, int device, v
   if (!valid_packed(a.gate_up) || !valid_packed(a.down) || a.gate_up.m != 2 * I || a.down.m != H || a.down.perm ||
       a.gate_up.qp.bits != a.down.qp.bits)
     return GPTQ_ERR_ARG;
-  if (!moe_layout(a.T, a.E, a.top_k, H, I, a.gate_up.perm ? 1 : 0, &lay)) return GPTQ_ERR_ARG;
+  if (!moe_layout(a.T, a.E, a.top_k, H, I, &lay) || 2 * I * a.E > INT32_MAX || H * a.E > INT32_MAX) return GPTQ_ERR_ARG;
   if ((a.dtype != GPTQ_FP16 && a.dtype != GPTQ_BF16) || (a.renormalize != 0 && a.renormalize != 1) ||
       a.act < GPTQ_ACT_NONE || a.act > GPTQ_ACT_SILU)
     return GPTQ_ERR_ARG;
@@ -410,68 +424,68 @@ extern "C" gptq_status gptq_dequant_moe(const gptq_moe_args* args, int device, v
   r.H = static_cast<int>(H);
   r.top_k = a.top_k;
   r.renorm = a.renormalize;
+  r.seg_pairs = 8 * moe_nt(a.T);
   r.logits = reinterpret_cast<double*>(ws + lay.logits);
   r.ids = reinterpret_cast<int32_t*>(ws + lay.ids);
   r.weights = reinterpret_cast<float*>(ws + lay.weights);
   r.ids_out = a.ids_out;
   r.weights_out = a.weights_out;
-  r.plan.active = reinterpret_cast<int*>(ws + lay.active);
+  r.plan.segments = reinterpret_cast<int*>(ws + lay.segments);
+  r.plan.tiles = reinterpret_cast<int*>(ws + lay.tiles);
   r.plan.expert = reinterpret_cast<int*>(ws + lay.expert);
   r.plan.begin = reinterpret_cast<int*>(ws + lay.begin);
   r.plan.count = reinterpret_cast<int*>(ws + lay.count);
+  r.plan.tile0 = reinterpret_cast<int*>(ws + lay.tile0);
+  r.plan.tile_seg = reinterpret_cast<int*>(ws + lay.tile_seg);
   r.plan.pair = reinterpret_cast<int*>(ws + lay.pair);
   r.plan.weight = reinterpret_cast<float*>(ws + lay.pweight);
   r.status = reinterpret_cast<int*>(ws);
+  CUtensorMap gmap, dmap;
+  gptq_status s = encode_codes(&gmap, a.gate_up, 64, a.E);
+  if (s == GPTQ_OK) s = encode_codes(&dmap, a.down, 64, a.E);
+  if (s != GPTQ_OK) return s;
   CK(launch_pdl(bf ? moe_router_kernel<true> : moe_router_kernel<false>, dim3(ROUTER_CLUSTER), dim3(ROUTER_WARPS * 32), 0,
                 ROUTER_CLUSTER, st, r));
 
+  const int gg = group_width(a.gate_up), gd = group_width(a.down);
+  CK(launch_pdl(moe_fragment_kernel, dim3(static_cast<unsigned>(H / 128), lay.max_tiles), dim3(128), 0, 1, st, r.X, a.ld_x,
+                r.H, std::min(gg, 128), a.gate_up.perm, r.plan, a.top_k, reinterpret_cast<uint4*>(ws + lay.x)));
+
   MoeArgs m;
-  m.X = r.X;
-  m.ldx = a.ld_x;
-  m.gathered = a.gate_up.perm ? 1 : 0;
-  if (a.gate_up.perm) {
-    uint16_t* xg = reinterpret_cast<uint16_t*>(ws + lay.x);
-    CK(launch_pdl(moe_gather_kernel, dim3(static_cast<unsigned>((H + 1023) / 1024), pairs), dim3(256), 0, 1, st, r.X,
-                  a.ld_x, static_cast<int>(H), a.gate_up.perm, r.plan, a.top_k, static_cast<const int32_t*>(r.ids),
-                  xg));
-    m.X = xg;
-    m.ldx = H;
-  }
+  m.x = ws + lay.x;
   m.plan = r.plan;
   m.T = r.T;
   m.E = r.E;
   m.top_k = a.top_k;
   m.H = r.H;
   m.I = static_cast<int>(I);
-  m.gu_codes = a.gate_up.codes;
   m.gu_scales = a.gate_up.scales;
   m.gu_zeros = a.gate_up.zeros;
-  m.dn_codes = a.down.codes;
   m.dn_scales = a.down.scales;
   m.dn_zeros = a.down.zeros;
-  const int gg = group_width(a.gate_up), gd = group_width(a.down);
   m.gu_G = m.H / gg;
   m.dn_G = m.I / gd;
   m.gu_gi = group_index(gg);
   m.dn_gi = group_index(gd);
   m.act = a.act;
-  m.h = reinterpret_cast<uint16_t*>(ws + lay.h);
+  m.dn_unit = std::min(gd, 128);
+  m.h = ws + lay.h;
+  m.status = r.status;
   m.residual = static_cast<const uint16_t*>(a.residual);
   m.ld_res = a.ld_res;
   m.ldy = a.ld_y;
   m.Y = static_cast<uint16_t*>(a.Y);
   DecodeLaunch l;
   l.bf16 = bf;
-  l.nt = a.T <= 8 ? 1 : 2;
-  l.rt = 1;
+  l.nt = moe_nt(a.T);
   l.device = device;
   l.stream = st;
   l.unit = std::min(gg, 128);
-  l.cluster = 1;
-  const int slots = static_cast<int>(std::min<int64_t>(a.E, pairs));
-  CK(by_bits(a.gate_up.qp.bits, [&](auto b) { return launch_moe_gate_up<decltype(b)::value>(l, m, slots); }));
-  l.unit = std::min(gd, 128);
-  l.cluster = k_split((m.H + 15) / 16, slots * (m.I / 128));
-  CK(by_bits(a.down.qp.bits, [&](auto b) { return launch_moe_down<decltype(b)::value>(l, m); }));
+  l.cluster = k_split(I / 64 * std::min<int64_t>(a.E, pairs), m.H / 128);
+  CK(by_bits(a.gate_up.qp.bits,
+             [&](auto b) { return launch_moe_gate_up<decltype(b)::value>(l, gmap, m, lay.max_segments); }));
+  l.unit = m.dn_unit;
+  l.cluster = k_split(m.H / DEC_ROWS, static_cast<int>(std::min<int64_t>(a.E, pairs)) * (m.I / 128));
+  CK(by_bits(a.down.qp.bits, [&](auto b) { return launch_moe_down<decltype(b)::value>(l, dmap, m); }));
   return GPTQ_OK;
 }

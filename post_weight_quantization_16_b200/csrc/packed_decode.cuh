@@ -15,15 +15,18 @@
 // lop3) and one packed subtraction or fused multiply-add; the pair order is matched on the
 // activations' side by byte permutes, once per token tile.
 //
-// One warp owns 16 * RT weight rows and a range of 128-column chunks; mma.sync m16n8k16 takes the
-// weights as the 16-row operand and eight tokens as the columns.  The order of k inside an MMA is
-// free as long as both operands agree: the lane of quad position q owns GU / 4 consecutive columns
-// of every unit of GU = min(group, 128) columns, so codes arrive as 16-byte loads straight from the
-// framework's row format (no repacking, no shared memory) and a unit never mixes two groups.
-// The block's warps and the blocks of a cluster split k; partial sums meet in shared memory and
-// over distributed shared memory in a fixed order, so results are deterministic and need no
-// workspace.  tcgen05 is not used here: with at most 16 tokens its operand would have to pass
-// through shared memory, which costs more than the product itself.
+// mma.sync m16n8k16 takes the weights as the 16-row operand and eight tokens as the columns; the
+// order of k inside an MMA is free as long as both operands agree: the lane of quad position q owns
+// GU / 4 consecutive columns of every unit of GU = min(group, 128) columns, so a unit never mixes
+// two groups and a lane's codes are one 16-byte word group of the framework's row format (no
+// repacking).  A block owns 128 rows (a warp 16) and a range of 128-column chunks.  One producer
+// lane streams the codes by TMA, and the activations by bulk copies, through a ring of shared-memory
+// stages deep enough to cover HBM's latency; the activations come in "fragment order" (below), which
+// a small kernel lays out first, so that a warp reads them as conflict-free 16-byte words that are
+// the MMA operand as they stand.  The blocks of a cluster split k; their sums meet over distributed
+// shared memory in a fixed order, so results are deterministic.  tcgen05 is not used here: with
+// this few tokens its operand would have to pass through shared memory once more, which costs more
+// than the product.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -165,15 +168,21 @@ __device__ __forceinline__ void unpack8(uint32_t v, uint32_t v1, const ZeroTerm&
 }
 
 // ------------------------------------------------------------------------------------------
-// a lane's share of one 128-column chunk of one packed row
+// a lane's share of one 128-column chunk of one packed row (shared memory)
 // ------------------------------------------------------------------------------------------
-__device__ __forceinline__ uint32_t ldg32(const uint32_t* p) { return __ldg(p); }
-__device__ __forceinline__ uint2 ldg64(const uint32_t* p) { return __ldg(reinterpret_cast<const uint2*>(p)); }
-__device__ __forceinline__ uint4 ldg128(const uint32_t* p) {
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
   return v;
 }
 
@@ -187,38 +196,38 @@ struct RawChunk {
                                         : (BITS == 8 ? 2 : BITS == 3 ? 2 : 1);
   uint32_t w[UNITS * WPU];
 
-  // base: the row's words of this chunk
-  __device__ __forceinline__ void load(const uint32_t* base, int q) {
+  // base: shared-memory address of the row's 16 * BITS bytes of this chunk
+  __device__ __forceinline__ void load(uint32_t base, int q) {
 #pragma unroll
     for (int u = 0; u < UNITS; ++u) {
-      const uint32_t* ub = base + u * (GU * BITS / 32);
+      const uint32_t ub = base + u * (GU * BITS / 8);
       uint32_t* d = w + u * WPU;
       if (BITS == 3) {
         if (GU == 128) {
 #pragma unroll
-          for (int j = 0; j < WPU; ++j) d[j] = ldg32(ub + 3 * q + j);
+          for (int j = 0; j < WPU; ++j) d[j] = lds32(ub + 4 * (3 * q + j));
         } else {
           const int i = GU == 64 ? (3 * q) >> 1 : (24 * q) >> 5;
-          d[0] = ldg32(ub + i);
-          d[1 % WPU] = ldg32(ub + (GU == 64 ? i + 1 : min(i + 1, 2)));
+          d[0] = lds32(ub + 4 * i);
+          d[1 % WPU] = lds32(ub + 4 * (GU == 64 ? i + 1 : min(i + 1, 2)));
         }
       } else if (BITS == 2 && GU == 32) {
-        d[0] = __ldg(reinterpret_cast<const uint16_t*>(ub) + q);
+        d[0] = lds32(ub + 4 * (q >> 1)) >> (16 * (q & 1));
       } else if (WPU % 4 == 0) {
 #pragma unroll
         for (int j = 0; j < WPU / 4; ++j) {
-          const uint4 x = ldg128(ub + q * WPU + 4 * j);
+          const uint4 x = lds128(ub + 4 * (q * WPU + 4 * j));
           d[4 * j] = x.x;
           d[(4 * j + 1) % WPU] = x.y;
           d[(4 * j + 2) % WPU] = x.z;
           d[(4 * j + 3) % WPU] = x.w;
         }
       } else if (WPU == 2) {
-        const uint2 x = ldg64(ub + q * 2);
+        const uint2 x = lds64(ub + 8 * q);
         d[0] = x.x;
         d[1 % WPU] = x.y;
       } else {
-        d[0] = ldg32(ub + q);
+        d[0] = lds32(ub + 4 * q);
       }
     }
   }
@@ -249,12 +258,60 @@ struct RawChunk {
 };
 
 // ------------------------------------------------------------------------------------------
-// the stream of a warp: 16 * RT rows x NT * 8 tokens over chunks [c0, c1)
+// activations in fragment order
+// ------------------------------------------------------------------------------------------
+// A tile is eight tokens.  Of every 128-column chunk it takes FRAG_BYTES = 2 KB: four blocks x 32
+// lanes x 16 bytes; lane (token n, quad position q) of block kb holds the eight columns
+// frag_column(kb, q) .. + 7 in the pair order (0, 4), (1, 5), (2, 6), (3, 7) of unpack8.
+constexpr int FRAG_BYTES = 2048;
+
+// First column (within the chunk) of block kb (0 .. 3) of quad position q for units of gu columns.
+__device__ __forceinline__ int frag_column(int gu, int kb, int q) {
+  if (gu == 128) return q * 32 + kb * 8;
+  if (gu == 64) return (kb >> 1) * 64 + q * 16 + (kb & 1) * 8;
+  return kb * 32 + q * 8;
+}
+// Offset, in 16-bit values inside the chunk's FRAG_BYTES, of column c of token n.
+__device__ __forceinline__ int frag_offset(int gu, int n, int c) {
+  int kb, q;
+  if (gu == 128) {
+    q = c >> 5;
+    kb = (c >> 3) & 3;
+  } else if (gu == 64) {
+    q = (c >> 4) & 3;
+    kb = ((c >> 6) << 1) | ((c >> 3) & 1);
+  } else {
+    q = (c >> 3) & 3;
+    kb = c >> 5;
+  }
+  const int i = c & 7;
+  return (kb * 32 + n * 4 + q) * 8 + 2 * (i & 3) + (i >> 2);
+}
+// The 16 bytes of one lane from a token's row: eight columns from `col`, through perm if there is one.
+__device__ __forceinline__ uint4 frag_gather(const uint16_t* row, const int32_t* perm, int col) {
+  uint4 v;
+  if (perm) {
+    const int4 a = *reinterpret_cast<const int4*>(perm + col), b = *reinterpret_cast<const int4*>(perm + col + 4);
+    v.x = static_cast<uint32_t>(row[a.x]) | (static_cast<uint32_t>(row[b.x]) << 16);
+    v.y = static_cast<uint32_t>(row[a.y]) | (static_cast<uint32_t>(row[b.y]) << 16);
+    v.z = static_cast<uint32_t>(row[a.z]) | (static_cast<uint32_t>(row[b.z]) << 16);
+    v.w = static_cast<uint32_t>(row[a.w]) | (static_cast<uint32_t>(row[b.w]) << 16);
+  } else {
+    const uint4 r = *reinterpret_cast<const uint4*>(row + col);
+    v.x = __byte_perm(r.x, r.z, 0x5410);
+    v.y = __byte_perm(r.x, r.z, 0x7632);
+    v.z = __byte_perm(r.y, r.w, 0x5410);
+    v.w = __byte_perm(r.y, r.w, 0x7632);
+  }
+  return v;
+}
+
+// ------------------------------------------------------------------------------------------
+// the stream of a block: 128 rows x up to NT tiles of tokens over ranges of chunks
 // ------------------------------------------------------------------------------------------
 struct GroupIndex {
-  int units_per_chunk_shift;  // group < 128: log2(128 / group) groups in a chunk, else 0
-  int div;                    // group >= 128: chunks per group
-  uint32_t magic;             // ceil(2^32 / div), exact for chunk < 2^14 and div <= 2^14
+  int div;         // group >= 128: chunks per group
+  uint32_t magic;  // ceil(2^32 / div), exact for chunk < 2^14 and div <= 2^14
 };
 // Index of the group of unit u in chunk c.
 template <int GU>
@@ -263,107 +320,159 @@ __device__ __forceinline__ int group_of(const GroupIndex& gi, int c, int u) {
   return gi.div == 1 ? c : static_cast<int>(__umulhi(static_cast<uint32_t>(c), gi.magic));
 }
 
-template <int BITS, bool BF, int GU, int NT, int RT>
-struct Stream {
+constexpr int DEC_WARPS = 8;                        // consumer warps: 16 rows each
+constexpr int DEC_ROWS = 16 * DEC_WARPS;            // rows of a block
+constexpr int DEC_THREADS = (DEC_WARPS + 1) * 32;   // and the producer warp
+constexpr int DEC_MAX_STAGES = 12;
+constexpr int DEC_SMEM = 94 * 1024;                 // ring of a block: two blocks per SM
+
+__host__ __device__ constexpr int dec_code_bytes(int bits) { return DEC_ROWS * 16 * bits; }
+__host__ __device__ constexpr int dec_stage_bytes(int bits, int nt) { return dec_code_bytes(bits) + nt * FRAG_BYTES; }
+__host__ __device__ constexpr int dec_stages(int bits, int nt) {
+  const int s = DEC_SMEM / dec_stage_bytes(bits, nt);
+  return s > DEC_MAX_STAGES ? DEC_MAX_STAGES : s;
+}
+__host__ __device__ constexpr int dec_ring_bytes(int bits, int nt) { return 128 + dec_stages(bits, nt) * dec_stage_bytes(bits, nt); }
+
+// Start of the dynamic shared memory at the next multiple of 128 bytes.
+__device__ __forceinline__ uint8_t* align128(uint8_t* raw) {
+  const uint32_t a = smem_u32(raw);
+  return raw + (((a + 127u) & ~127u) - a);
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+// A range of chunks of one weight matrix and the activations it meets.
+struct Segment {
+  int row_a, row_b;     // tensor-map rows of the stage's rows 0-63 and 64-127
+  int c0, c1;           // chunks
+  int tiles;            // token tiles, 1 .. NT
+  const uint8_t* x;     // fragment order, [chunk][tiles][FRAG_BYTES]
+};
+
+template <int BITS, bool BF, int GU, int NT>
+struct Ring {
   using Raw = RawChunk<BITS, GU>;
   static constexpr int UNITS = Raw::UNITS, BLOCKS = Raw::BLOCKS;
-  static constexpr int DEPTH = 2;  // chunks whose codes are in flight
+  static constexpr int STAGES = dec_stages(BITS, NT), STAGE = dec_stage_bytes(BITS, NT), CODES = dec_code_bytes(BITS);
 
-  struct Stage {
-    Raw raw[RT][2];
-    float s[RT][2][UNITS], z[RT][2][UNITS];
-  };
+  uint32_t base, full, empty;  // shared-memory addresses: stages, barriers
+  volatile int* abort_flag;
 
-  const uint32_t* code[RT][2];  // rows g and g + 8 of each 16-row tile
-  const float* scale[RT][2];
-  ptrdiff_t zoff;               // zeros - scales (elements)
-  GroupIndex gi;
-  int q;
-
-  __device__ __forceinline__ void fetch(Stage& st, int c) const {
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        st.raw[r][h].load(code[r][h] + static_cast<size_t>(c) * (4 * BITS), q);
-#pragma unroll
-        for (int u = 0; u < UNITS; ++u) {
-          const float* sp = scale[r][h] + group_of<GU>(gi, c, u);
-          st.s[r][h][u] = __ldg(sp);
-          st.z[r][h][u] = __ldg(sp + zoff);
-        }
+  __device__ __forceinline__ void init(uint32_t smem_base, uint64_t* bars, int* flag) {
+    base = smem_base;
+    full = smem_u32(bars);
+    empty = full + 8 * STAGES;
+    abort_flag = flag;
+    if (threadIdx.x == 0) {
+      for (int s = 0; s < STAGES; ++s) {
+        mbar_init(full + 8 * s, 1);
+        mbar_init(empty + 8 * s, DEC_WARPS);
       }
+      *flag = 0;
+      fence_mbar_init();
+    }
+    __syncthreads();
   }
 
-  __device__ __forceinline__ void compute(const Stage& st, int c, const uint16_t* const (&x)[NT],
-                                          float (&acc)[RT][NT][4]) const {
+  // Producer (one lane).  `it` counts stages over all segments of the block.
+  __device__ __forceinline__ bool codes(const CUtensorMap* map, const Segment& g, int c, int it) const {
+    const int s = it % STAGES;
+    if (!mbar_wait_bounded(empty + 8 * s, (static_cast<uint32_t>(it / STAGES) & 1u) ^ 1u, abort_flag)) return false;
+    const uint32_t fb = full + 8 * s, st = base + s * STAGE;
+    mbar_arrive_expect_tx(fb, static_cast<uint32_t>(CODES + g.tiles * FRAG_BYTES));
+    tma_load_2d(st, map, fb, c * (4 * BITS), g.row_a);
+    tma_load_2d(st + CODES / 2, map, fb, c * (4 * BITS), g.row_b);
+    return true;
+  }
+  __device__ __forceinline__ void acts(const Segment& g, int c, int it) const {
+    const int s = it % STAGES;
+    bulk_load(base + s * STAGE + CODES, g.x + static_cast<size_t>(c) * g.tiles * FRAG_BYTES,
+              static_cast<uint32_t>(g.tiles * FRAG_BYTES), full + 8 * s);
+  }
+  // No copy may be in flight when the block leaves.
+  __device__ __forceinline__ void drain(int issued) const {
+    for (int i = max(0, issued - STAGES); i < issued; ++i)
+      mbar_wait_drain(full + 8 * (i % STAGES), static_cast<uint32_t>(i / STAGES) & 1u);
+  }
+
+  // Consumer warp: its rows' scales and zero-points (rows g and g + 8 of its 16).
+  const float *scale_a, *scale_b;
+  ptrdiff_t zoff;  // zeros - scales (elements)
+  GroupIndex gi;
+
+  struct Params {
+    float s[2][UNITS], z[2][UNITS];
+  };
+  __device__ __forceinline__ void fetch(Params& p, int c) const {
 #pragma unroll
     for (int u = 0; u < UNITS; ++u) {
-      float sum[RT][NT][4];
+      const int g = group_of<GU>(gi, c, u);
+      p.s[0][u] = __ldg(scale_a + g);
+      p.z[0][u] = __ldg(scale_a + zoff + g);
+      p.s[1][u] = __ldg(scale_b + g);
+      p.z[1][u] = __ldg(scale_b + zoff + g);
+    }
+  }
+
+  // acc[t] += the warp's 16 rows x tile t over chunks [c0, c1); offa, offb: byte offsets of the
+  // lane's two rows in a stage.  `it` as in the producer.  False when a wait ran out.
+  __device__ __forceinline__ bool consume(int c0, int c1, int tiles, uint32_t offa, uint32_t offb, int q, int lane,
+                                          int& it, float (&acc)[NT][4]) const {
+    Params next;
+    if (c0 < c1) fetch(next, c0);
+    for (int c = c0; c < c1; ++c, ++it) {
+      const Params pr = next;
+      if (c + 1 < c1) fetch(next, c + 1);
+      const int s = it % STAGES;
+      // (all lanes leave together: the MMAs below need the whole warp)
+      if (!__all_sync(0xffffffffu,
+                      mbar_wait_bounded(full + 8 * s, static_cast<uint32_t>(it / STAGES) & 1u, abort_flag)))
+        return false;
+      const uint32_t st = base + s * STAGE;
+      Raw ra, rb;
+      ra.load(st + offa, q);
+      rb.load(st + offb, q);
 #pragma unroll
-      for (int r = 0; r < RT; ++r)
+      for (int u = 0; u < UNITS; ++u) {
+        float sum[NT][4];
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) sum[r][t][j] = 0.0f;
-      ZeroTerm zt[RT][2];
+          for (int j = 0; j < 4; ++j) sum[t][j] = 0.0f;
+        const ZeroTerm za = zero_term<BITS, BF>(pr.z[0][u]), zb = zero_term<BITS, BF>(pr.z[1][u]);
 #pragma unroll
-      for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) zt[r][h] = zero_term<BITS, BF>(st.z[r][h][u]);
-#pragma unroll
-      for (int b = 0; b < BLOCKS; ++b) {
-        uint32_t xb[NT][4];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          const uint4 v = *reinterpret_cast<const uint4*>(x[t] + c * 128 + u * GU + q * (GU / 4) + b * 8);
-          xb[t][0] = __byte_perm(v.x, v.z, 0x5410);
-          xb[t][1] = __byte_perm(v.x, v.z, 0x7632);
-          xb[t][2] = __byte_perm(v.y, v.w, 0x5410);
-          xb[t][3] = __byte_perm(v.y, v.w, 0x7632);
-        }
-#pragma unroll
-        for (int r = 0; r < RT; ++r) {
+        for (int b = 0; b < BLOCKS; ++b) {
           uint32_t pa[4], pb[4], v, v1;
-          st.raw[r][0].block(u, b, q, v, v1);
-          unpack8<BITS, BF>(v, v1, zt[r][0], pa);
-          st.raw[r][1].block(u, b, q, v, v1);
-          unpack8<BITS, BF>(v, v1, zt[r][1], pb);
+          ra.block(u, b, q, v, v1);
+          unpack8<BITS, BF>(v, v1, za, pa);
+          rb.block(u, b, q, v, v1);
+          unpack8<BITS, BF>(v, v1, zb, pb);
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
-            mma_16816<BF>(sum[r][t], pa[0], pb[0], pa[1], pb[1], xb[t][0], xb[t][1]);
-            mma_16816<BF>(sum[r][t], pa[2], pb[2], pa[3], pb[3], xb[t][2], xb[t][3]);
+            if (t < tiles) {
+              const uint4 x = lds128(st + CODES + t * FRAG_BYTES + (u * BLOCKS + b) * 512 + lane * 16);
+              mma_16816<BF>(sum[t], pa[0], pb[0], pa[1], pb[1], x.x, x.y);
+              mma_16816<BF>(sum[t], pa[2], pb[2], pa[3], pb[3], x.z, x.w);
+            }
           }
         }
-      }
-#pragma unroll
-      for (int r = 0; r < RT; ++r)
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          acc[r][t][0] = fmaf(st.s[r][0][u], sum[r][t][0], acc[r][t][0]);
-          acc[r][t][1] = fmaf(st.s[r][0][u], sum[r][t][1], acc[r][t][1]);
-          acc[r][t][2] = fmaf(st.s[r][1][u], sum[r][t][2], acc[r][t][2]);
-          acc[r][t][3] = fmaf(st.s[r][1][u], sum[r][t][3], acc[r][t][3]);
-        }
-    }
-  }
-
-  __device__ __forceinline__ void prologue(Stage (&st)[DEPTH], int c0, int c1) const {
-#pragma unroll
-    for (int d = 0; d < DEPTH; ++d)
-      if (c0 + d < c1) fetch(st[d], c0 + d);
-  }
-  __device__ __forceinline__ void run(Stage (&st)[DEPTH], int c0, int c1, const uint16_t* const (&x)[NT],
-                                      float (&acc)[RT][NT][4]) const {
-    for (int c = c0; c < c1; c += DEPTH) {
-#pragma unroll
-      for (int d = 0; d < DEPTH; ++d) {
-        if (c + d < c1) {
-          compute(st[d], c + d, x, acc);
-          if (c + d + DEPTH < c1) fetch(st[d], c + d + DEPTH);
+          acc[t][0] = fmaf(pr.s[0][u], sum[t][0], acc[t][0]);
+          acc[t][1] = fmaf(pr.s[0][u], sum[t][1], acc[t][1]);
+          acc[t][2] = fmaf(pr.s[1][u], sum[t][2], acc[t][2]);
+          acc[t][3] = fmaf(pr.s[1][u], sum[t][3], acc[t][3]);
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty + 8 * s);
     }
+    return true;
   }
 };
 
@@ -389,119 +498,114 @@ __device__ __forceinline__ float ld_dsmem_f(uint32_t addr) {
 // ------------------------------------------------------------------------------------------
 // the linear layer for few tokens
 // ------------------------------------------------------------------------------------------
-constexpr int DEC_WARPS = 8;  // warps of a block: they split k
+constexpr int DEC_MAX_TILES = 4;
 
 struct LinearDecodeArgs {
-  const uint16_t* X;  // [T x n], sweep order
-  int64_t ldx;
-  const uint32_t* codes;
+  const uint8_t* x;  // fragment order, [chunk][tiles][FRAG_BYTES]
   const float *scales, *zeros;
-  int T, m, chunks, G;
+  int T, tiles, m, chunks, G;
   GroupIndex gi;
   const uint16_t *bias, *residual;
   int64_t ld_res, ldy;
   void* Y;
   uint16_t* preact;  // [T x m] or null
   int act, y_fp32;
-  int early;    // 1: the launch before this one belongs to the same call, so weights may be read before it ends
-  int* status;  // cleared (this kernel waits on nothing)
+  int* status;
 };
 
-template <int BITS, bool BF, int GU, int NT, int RT>
-__global__ void __launch_bounds__(DEC_WARPS * 32) linear_decode_kernel(const LinearDecodeArgs p) {
-  __shared__ float4 red[DEC_WARPS][RT * NT * 32];
+template <int BITS, bool BF, int GU, int NT>
+__global__ void __launch_bounds__(DEC_THREADS)
+    linear_decode_kernel(const __grid_constant__ CUtensorMap codes_map, const LinearDecodeArgs p) {
+  extern __shared__ uint8_t dec_smem_raw[];
+  __shared__ __align__(8) uint64_t bars[2 * DEC_MAX_STAGES];
+  __shared__ int abort_flag;
+  __shared__ float4 red[DEC_WARPS * NT * 32];
+  uint8_t* dec_smem = align128(dec_smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   const int cs = static_cast<int>(cluster_nctarank()), rank = static_cast<int>(cluster_ctarank());
-  const int row0 = static_cast<int>(blockIdx.x) / cs * (16 * RT);
-  const int tok0 = static_cast<int>(blockIdx.y) * (8 * NT);
-  Stream<BITS, BF, GU, NT, RT> s;
-  s.q = q;
-  s.gi = p.gi;
-  s.zoff = p.zeros - p.scales;
-#pragma unroll
-  for (int r = 0; r < RT; ++r)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int row = min(row0 + 16 * r + 8 * h + g, p.m - 1);  // rows past m repeat the last one, unstored
-      s.code[r][h] = p.codes + static_cast<size_t>(row) * p.chunks * (4 * BITS);
-      s.scale[r][h] = p.scales + static_cast<size_t>(row) * p.G;
+  const int row0 = static_cast<int>(blockIdx.x) / cs * DEC_ROWS;
+  Ring<BITS, BF, GU, NT> r;
+  r.init(smem_u32(dec_smem), bars, &abort_flag);
+  Segment sg;
+  sg.row_a = row0;
+  sg.row_b = row0 + 64;
+  sg.c0 = p.chunks * rank / cs;
+  sg.c1 = p.chunks * (rank + 1) / cs;
+  sg.tiles = p.tiles;
+  sg.x = p.x;
+  bool ok = true;
+  if (warp == DEC_WARPS) {
+    if (lane == 0) {
+      // the launch before this one laid out x and had waited for all earlier work: the weights can
+      // be read before it ends, x cannot
+      const int ahead = min(Ring<BITS, BF, GU, NT>::STAGES, sg.c1 - sg.c0);
+      int it = 0;
+      for (; it < ahead; ++it) r.codes(&codes_map, sg, sg.c0 + it, it);
+      griddep_wait();
+      for (int i = 0; i < ahead; ++i) r.acts(sg, sg.c0 + i, i);
+      for (; it < sg.c1 - sg.c0; ++it) {
+        if (!r.codes(&codes_map, sg, sg.c0 + it, it)) break;
+        r.acts(sg, sg.c0 + it, it);
+      }
+      r.drain(it);
     }
-  const int slice = rank * DEC_WARPS + warp, slices = cs * DEC_WARPS;
-  const int c0 = static_cast<int>(static_cast<int64_t>(p.chunks) * slice / slices);
-  const int c1 = static_cast<int>(static_cast<int64_t>(p.chunks) * (slice + 1) / slices);
-  typename Stream<BITS, BF, GU, NT, RT>::Stage st[Stream<BITS, BF, GU, NT, RT>::DEPTH];
-  if (!p.early) griddep_wait();
-  s.prologue(st, c0, c1);
-  if (p.early) griddep_wait();
-  griddep_launch_dependents();
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.status = 0;
-  const uint16_t* x[NT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) x[t] = p.X + static_cast<size_t>(min(tok0 + 8 * t + g, p.T - 1)) * p.ldx;
-  float acc[RT][NT][4];
-#pragma unroll
-  for (int r = 0; r < RT; ++r)
+    griddep_launch_dependents();
+  } else {
+    float acc[NT][4];
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[r][t][j] = 0.0f;
-  s.run(st, c0, c1, x, acc);
-#pragma unroll
-  for (int r = 0; r < RT; ++r)
+      for (int j = 0; j < 4; ++j) acc[t][j] = 0.0f;
+    const int ra = warp * 16 + g, rb = ra + 8;  // rows past m repeat the last one's parameters, unstored
+    r.scale_a = p.scales + static_cast<size_t>(min(row0 + ra, p.m - 1)) * p.G;
+    r.scale_b = p.scales + static_cast<size_t>(min(row0 + rb, p.m - 1)) * p.G;
+    r.zoff = p.zeros - p.scales;
+    r.gi = p.gi;
+    int it = 0;
+    ok = r.consume(sg.c0, sg.c1, sg.tiles, ra * (16 * BITS), rb * (16 * BITS), q, lane, it, acc);
+    griddep_wait();  // (the residual and the outputs are touched from here on)
 #pragma unroll
     for (int t = 0; t < NT; ++t)
-      red[warp][(r * NT + t) * 32 + lane] = make_float4(acc[r][t][0], acc[r][t][1], acc[r][t][2], acc[r][t][3]);
-  __syncthreads();
-  // the block's warps in order, then the cluster's blocks in order
-  constexpr int ITEMS = RT * NT * 32;
-  for (int i = threadIdx.x; i < ITEMS; i += DEC_WARPS * 32) {
-    float4 v = red[0][i];
-#pragma unroll
-    for (int w = 1; w < DEC_WARPS; ++w) {
-      const float4 o = red[w][i];
-      v.x += o.x;
-      v.y += o.y;
-      v.z += o.z;
-      v.w += o.w;
-    }
-    red[0][i] = v;
+      red[(warp * NT + t) * 32 + lane] = make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
   }
   if (cs > 1) {
     cluster_sync();
   } else {
     __syncthreads();
   }
-  if (rank == 0) {
-    for (int i = threadIdx.x; i < ITEMS; i += DEC_WARPS * 32) {
-      float4 v = red[0][i];
-      for (int o = 1; o < cs; ++o) {
-        const float4 w = ld_dsmem_f4(mapa_shared(smem_u32(&red[0][i]), o));
-        v.x += w.x;
-        v.y += w.y;
-        v.z += w.z;
-        v.w += w.w;
-      }
-      const int l = i & 31, t = (i >> 5) % NT, r = (i >> 5) / NT;
-      const float e[4] = {v.x, v.y, v.z, v.w};
+  // the cluster's blocks in order; each block finishes its share of the items
+  constexpr int ITEMS = DEC_WARPS * NT * 32;
+  for (int i = rank * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x); i < ITEMS && !abort_flag;
+       i += cs * static_cast<int>(blockDim.x)) {
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int o = 0; o < cs; ++o) {
+      const float4 w = cs > 1 ? ld_dsmem_f4(mapa_shared(smem_u32(&red[i]), o)) : red[i];
+      v.x += w.x;
+      v.y += w.y;
+      v.z += w.z;
+      v.w += w.w;
+    }
+    const int l = i & 31, t = (i >> 5) % NT, w = (i >> 5) / NT;
+    const float e[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int row = row0 + 16 * r + (l >> 2) + 8 * (j >> 1);
-        const int tok = tok0 + 8 * t + 2 * (l & 3) + (j & 1);
-        if (row < p.m && tok < p.T) {
-          float z = e[j];
-          if (p.bias) z += h2f<BF>(p.bias[row]);
-          if (p.preact) p.preact[static_cast<size_t>(tok) * p.m + row] = f2h<BF>(z);
-          float y = act_apply(z, p.act);
-          if (p.residual) y += h2f<BF>(p.residual[static_cast<size_t>(tok) * p.ld_res + row]);
-          if (p.y_fp32)
-            static_cast<float*>(p.Y)[static_cast<size_t>(tok) * p.ldy + row] = y;
-          else
-            static_cast<uint16_t*>(p.Y)[static_cast<size_t>(tok) * p.ldy + row] = f2h<BF>(y);
-        }
+    for (int j = 0; j < 4; ++j) {
+      const int row = row0 + 16 * w + (l >> 2) + 8 * (j >> 1);
+      const int tok = 8 * t + 2 * (l & 3) + (j & 1);
+      if (row < p.m && tok < p.T) {
+        float z = e[j];
+        if (p.bias) z += h2f<BF>(p.bias[row]);
+        if (p.preact) p.preact[static_cast<size_t>(tok) * p.m + row] = f2h<BF>(z);
+        float y = act_apply(z, p.act);
+        if (p.residual) y += h2f<BF>(p.residual[static_cast<size_t>(tok) * p.ld_res + row]);
+        if (p.y_fp32)
+          static_cast<float*>(p.Y)[static_cast<size_t>(tok) * p.ldy + row] = y;
+        else
+          static_cast<uint16_t*>(p.Y)[static_cast<size_t>(tok) * p.ldy + row] = f2h<BF>(y);
       }
     }
   }
   if (cs > 1) cluster_sync();  // no block leaves while its sums may still be read
+  if (threadIdx.x == 0 && abort_flag) atomicOr(p.status, ST_TIMEOUT);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -511,199 +615,223 @@ constexpr int MOE_MAX_T = 128;      // "few tokens": the down product keeps a ro
 constexpr int MOE_MAX_E = 256;
 constexpr int MOE_MAX_TOPK = 16;
 
-// The routing of one call (workspace): the experts that got tokens, in ascending order, and their
-// (token, choice) pairs, ascending inside an expert.
+// The routing of one call (workspace).  The (token, choice) pairs are listed by expert, ascending
+// inside an expert; a segment is up to 8 NT consecutive pairs of one expert.  Its tiles of eight
+// pairs follow those of the segments before it.
 struct MoePlan {
-  int* active;        // [1]
-  int* expert;        // [E] expert of slot s
-  int* begin;         // [E] first list position of slot s
-  int* count;         // [E] pairs of slot s
-  int* pair;          // [T * top_k] pair (token * top_k + choice) at list position i
-  float* weight;      // [T * top_k] its routing weight
+  int* segments;   // [1]
+  int* expert;     // [segments]
+  int* begin;      // [segments] first list position
+  int* count;      // [segments] pairs
+  int* tile0;      // [segments] tiles of the segments before it
+  int* tiles;      // [1] all tiles
+  int* tile_seg;   // [tiles] segment of a tile
+  int* pair;       // [T * top_k] pair (token * top_k + choice) at a list position
+  float* weight;   // [T * top_k] its routing weight
 };
 
 struct MoeArgs {
-  const uint16_t* X;  // gathered: [T * top_k x H] in list order and the expert's sweep order; else [T x H]
-  int64_t ldx;
-  int gathered;
+  const uint8_t* x;  // fragment order: segment s at tile0[s] * (H / 128) * FRAG_BYTES, [chunk][tiles][FRAG_BYTES]
   MoePlan plan;
   int T, E, top_k, H, I;
-  const uint32_t *gu_codes, *dn_codes;
   const float *gu_scales, *gu_zeros, *dn_scales, *dn_zeros;
   int gu_G, dn_G;
   GroupIndex gu_gi, dn_gi;
-  int act;
-  uint16_t* h;  // [T * top_k x I], list order
+  int act, dn_unit;
+  uint8_t* h;  // fragment order, as x with I / 128 chunks
   const uint16_t* residual;
   int64_t ld_res, ldy;
   uint16_t* Y;
+  int* status;
 };
 
 // h = act(x Wg^T) * (x Wu^T), rounded to the activations' type (the operand type of the second
-// product).  Grid (I / (8 RT), slots): a block's 16-row tiles hold eight gate rows and, as rows
-// 8-15, the same eight up rows, so both halves of an h value end up in one lane.
-template <int BITS, bool BF, int GU, int NT, int RT>
-__global__ void __launch_bounds__(DEC_WARPS * 32) moe_gate_up_kernel(const MoeArgs p) {
-  __shared__ float4 red[DEC_WARPS][RT * NT * 32];
-  griddep_wait();
-  griddep_launch_dependents();
-  const int slot = static_cast<int>(blockIdx.y);
-  if (slot >= *p.plan.active) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-  const int e = p.plan.expert[slot], begin = p.plan.begin[slot], count = p.plan.count[slot];
-  const int i0 = static_cast<int>(blockIdx.x) * (8 * RT);
-  const int chunks = p.H / 128;
-  Stream<BITS, BF, GU, NT, RT> s;
-  s.q = q;
-  s.gi = p.gu_gi;
-  s.zoff = p.gu_zeros - p.gu_scales;
-#pragma unroll
-  for (int r = 0; r < RT; ++r)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const size_t row = static_cast<size_t>(e) * 2 * p.I + static_cast<size_t>(h) * p.I + (i0 + 8 * r + g);
-      s.code[r][h] = p.gu_codes + row * chunks * (4 * BITS);
-      s.scale[r][h] = p.gu_scales + row * p.gu_G;
-    }
-  const int c0 = chunks * warp / DEC_WARPS, c1 = chunks * (warp + 1) / DEC_WARPS;
-  for (int b0 = 0; b0 < count; b0 += 8 * NT) {
-    typename Stream<BITS, BF, GU, NT, RT>::Stage st[Stream<BITS, BF, GU, NT, RT>::DEPTH];
-    s.prologue(st, c0, c1);
-    const uint16_t* x[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int i = begin + min(b0 + 8 * t + g, count - 1);
-      x[t] = p.X + static_cast<size_t>(p.gathered ? i : p.plan.pair[i] / p.top_k) * p.ldx;
-    }
-    float acc[RT][NT][4];
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[r][t][j] = 0.0f;
-    s.run(st, c0, c1, x, acc);
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-        red[warp][(r * NT + t) * 32 + lane] = make_float4(acc[r][t][0], acc[r][t][1], acc[r][t][2], acc[r][t][3]);
-    __syncthreads();
-    for (int i = threadIdx.x; i < RT * NT * 32; i += DEC_WARPS * 32) {
-      float4 v = red[0][i];
-#pragma unroll
-      for (int w = 1; w < DEC_WARPS; ++w) {
-        const float4 o = red[w][i];
-        v.x += o.x;
-        v.y += o.y;
-        v.z += o.z;
-        v.w += o.w;
-      }
-      const int l = i & 31, t = (i >> 5) % NT, r = (i >> 5) / NT;
-      const int col = i0 + 8 * r + (l >> 2), n0 = b0 + 8 * t + 2 * (l & 3);
-      if (n0 < count) p.h[static_cast<size_t>(begin + n0) * p.I + col] = f2h<BF>(act_apply(v.x, p.act) * v.z);
-      if (n0 + 1 < count) p.h[static_cast<size_t>(begin + n0 + 1) * p.I + col] = f2h<BF>(act_apply(v.y, p.act) * v.w);
-    }
-    __syncthreads();
-  }
-}
-
-// y = sum over the token's experts of weight * h Wd^T, + residual.  A block owns 16 RT output
-// rows of every expert: its warps (and the cluster's blocks) split the list of (slot, chunk)
-// evenly, each adding its share of every expert into its own row of sums per token in shared
-// memory; the shares meet in a fixed order.  One pass, no sums in global memory, no atomics.
-template <int BITS, bool BF, int GU, int NT, int RT>
-__global__ void __launch_bounds__(DEC_WARPS * 32) moe_down_kernel(const MoeArgs p) {
-  extern __shared__ float ysum[];  // [DEC_WARPS][T][16 RT]
-  constexpr int ROWS = 16 * RT;
+// product).  Grid (I / 64 * cluster, segments): a block's stage holds 64 gate rows and the same 64
+// up rows; a warp takes eight of each as rows 0-7 and 8-15 of its MMA, so both halves of an h value
+// end up in one lane.
+template <int BITS, bool BF, int GU, int NT>
+__global__ void __launch_bounds__(DEC_THREADS)
+    moe_gate_up_kernel(const __grid_constant__ CUtensorMap codes_map, const MoeArgs p) {
+  extern __shared__ uint8_t dec_smem_raw[];
+  __shared__ __align__(8) uint64_t bars[2 * DEC_MAX_STAGES];
+  __shared__ int abort_flag;
+  __shared__ float4 red[DEC_WARPS * NT * 32];
+  uint8_t* dec_smem = align128(dec_smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   const int cs = static_cast<int>(cluster_nctarank()), rank = static_cast<int>(cluster_ctarank());
-  const int row0 = static_cast<int>(blockIdx.x) / cs * ROWS;
-  float* mine = ysum + static_cast<size_t>(warp) * p.T * ROWS;
-  for (int i = lane; i < p.T * ROWS; i += 32) mine[i] = 0.0f;
-  __syncwarp();
+  Ring<BITS, BF, GU, NT> r;
+  r.init(smem_u32(dec_smem), bars, &abort_flag);
   griddep_wait();
   griddep_launch_dependents();
-  const int chunks = p.I / 128;
-  const int64_t total = static_cast<int64_t>(*p.plan.active) * chunks;
-  const int slice = rank * DEC_WARPS + warp, slices = cs * DEC_WARPS;
-  const int64_t w0 = total * slice / slices, w1 = total * (slice + 1) / slices;
-  Stream<BITS, BF, GU, NT, RT> s;
-  s.q = q;
-  s.gi = p.dn_gi;
-  s.zoff = p.dn_zeros - p.dn_scales;
-  for (int64_t w = w0; w < w1;) {
-    const int slot = static_cast<int>(w / chunks);
-    const int c0 = static_cast<int>(w - static_cast<int64_t>(slot) * chunks);
-    const int c1 = static_cast<int>(min(static_cast<int64_t>(chunks), c0 + (w1 - w)));
-    w += c1 - c0;
-    const int e = p.plan.expert[slot], begin = p.plan.begin[slot], count = p.plan.count[slot];
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int rr = min(row0 + 16 * r + 8 * h + g, p.H - 1);
-        const size_t row = static_cast<size_t>(e) * p.H + rr;
-        s.code[r][h] = p.dn_codes + row * chunks * (4 * BITS);
-        s.scale[r][h] = p.dn_scales + row * p.dn_G;
+  const int seg = static_cast<int>(blockIdx.y);
+  if (seg >= *p.plan.segments) return;  // (the whole cluster)
+  const int e = p.plan.expert[seg], count = p.plan.count[seg], tile0 = p.plan.tile0[seg];
+  const int i0 = static_cast<int>(blockIdx.x) / cs * 64;
+  const int chunks = p.H / 128;
+  Segment sg;
+  sg.row_a = e * 2 * p.I + i0;
+  sg.row_b = sg.row_a + p.I;
+  sg.c0 = chunks * rank / cs;
+  sg.c1 = chunks * (rank + 1) / cs;
+  sg.tiles = (count + 7) / 8;
+  sg.x = p.x + static_cast<size_t>(tile0) * chunks * FRAG_BYTES;
+  if (warp == DEC_WARPS) {
+    if (lane == 0) {
+      int it = 0;
+      for (; it < sg.c1 - sg.c0; ++it) {
+        if (!r.codes(&codes_map, sg, sg.c0 + it, it)) break;
+        r.acts(sg, sg.c0 + it, it);
       }
-    for (int b0 = 0; b0 < count; b0 += 8 * NT) {
-      typename Stream<BITS, BF, GU, NT, RT>::Stage st[Stream<BITS, BF, GU, NT, RT>::DEPTH];
-      s.prologue(st, c0, c1);
-      const uint16_t* x[NT];
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-        x[t] = p.h + static_cast<size_t>(begin + min(b0 + 8 * t + g, count - 1)) * p.I;
-      float acc[RT][NT][4];
-#pragma unroll
-      for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[r][t][j] = 0.0f;
-      s.run(st, c0, c1, x, acc);
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int i = b0 + 8 * t + 2 * q + j;
-          if (i < count) {
-            const float wt = p.plan.weight[begin + i];
-            float* y = mine + static_cast<size_t>(p.plan.pair[begin + i] / p.top_k) * ROWS + g;
-#pragma unroll
-            for (int r = 0; r < RT; ++r) {
-              y[16 * r] = fmaf(wt, acc[r][t][j], y[16 * r]);
-              y[16 * r + 8] = fmaf(wt, acc[r][t][2 + j], y[16 * r + 8]);
-            }
-          }
-        }
-      __syncwarp();
+      r.drain(it);
     }
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < p.T * ROWS; i += DEC_WARPS * 32) {
-    float v = ysum[i];
+  } else {
+    float acc[NT][4];
 #pragma unroll
-    for (int k = 1; k < DEC_WARPS; ++k) v += ysum[static_cast<size_t>(k) * p.T * ROWS + i];
-    ysum[i] = v;
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[t][j] = 0.0f;
+    const int ra = warp * 8 + g;
+    r.scale_a = p.gu_scales + static_cast<size_t>(sg.row_a + ra) * p.gu_G;
+    r.scale_b = p.gu_scales + static_cast<size_t>(sg.row_b + ra) * p.gu_G;
+    r.zoff = p.gu_zeros - p.gu_scales;
+    r.gi = p.gu_gi;
+    int it = 0;
+    r.consume(sg.c0, sg.c1, sg.tiles, ra * (16 * BITS), (ra + 64) * (16 * BITS), q, lane, it, acc);
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+      red[(warp * NT + t) * 32 + lane] = make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
   }
   if (cs > 1) {
     cluster_sync();
   } else {
     __syncthreads();
   }
-  if (rank == 0) {
-    for (int i = threadIdx.x; i < p.T * ROWS; i += DEC_WARPS * 32) {
-      float v = ysum[i];
-      for (int o = 1; o < cs; ++o) v += ld_dsmem_f(mapa_shared(smem_u32(&ysum[i]), o));
-      const int tok = i / ROWS, row = row0 + i % ROWS;
-      if (row < p.H) {
-        if (p.residual) v += h2f<BF>(p.residual[static_cast<size_t>(tok) * p.ld_res + row]);
-        p.Y[static_cast<size_t>(tok) * p.ldy + row] = f2h<BF>(v);
-      }
+  constexpr int ITEMS = DEC_WARPS * NT * 32;
+  uint16_t* h = reinterpret_cast<uint16_t*>(p.h + static_cast<size_t>(tile0) * (p.I / 128) * FRAG_BYTES);
+  for (int i = rank * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x); i < ITEMS && !abort_flag;
+       i += cs * static_cast<int>(blockDim.x)) {
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int o = 0; o < cs; ++o) {
+      const float4 w = cs > 1 ? ld_dsmem_f4(mapa_shared(smem_u32(&red[i]), o)) : red[i];
+      v.x += w.x;
+      v.y += w.y;
+      v.z += w.z;
+      v.w += w.w;
+    }
+    const int l = i & 31, t = (i >> 5) % NT, w = (i >> 5) / NT;
+    const int col = i0 + 8 * w + (l >> 2), n = 2 * (l & 3);
+    if (t < sg.tiles) {
+      uint16_t* d = h + (static_cast<size_t>(col >> 7) * sg.tiles + t) * (FRAG_BYTES / 2);
+      d[frag_offset(p.dn_unit, n, col & 127)] = f2h<BF>(act_apply(v.x, p.act) * v.z);
+      d[frag_offset(p.dn_unit, n + 1, col & 127)] = f2h<BF>(act_apply(v.y, p.act) * v.w);
     }
   }
   if (cs > 1) cluster_sync();
+  if (threadIdx.x == 0 && abort_flag) atomicOr(p.status, ST_TIMEOUT);
+}
+
+// y = sum over the token's experts of weight * h Wd^T, + residual.  A block owns 128 output rows of
+// every expert and, in a cluster, an even share of the list of (segment, chunk); each segment's
+// sums are added, times the routing weight, into a row per token in shared memory (a warp owns its
+// 16 columns of it); the shares meet over the cluster in a fixed order.  One pass, no sums in global
+// memory, no atomics.
+template <int BITS, bool BF, int GU, int NT>
+__global__ void __launch_bounds__(DEC_THREADS)
+    moe_down_kernel(const __grid_constant__ CUtensorMap codes_map, const MoeArgs p) {
+  extern __shared__ uint8_t dec_smem_raw[];  // ring, then float [T][DEC_ROWS]
+  __shared__ __align__(8) uint64_t bars[2 * DEC_MAX_STAGES];
+  __shared__ int abort_flag;
+  uint8_t* dec_smem = align128(dec_smem_raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  const int cs = static_cast<int>(cluster_nctarank()), rank = static_cast<int>(cluster_ctarank());
+  const int row0 = static_cast<int>(blockIdx.x) / cs * DEC_ROWS;
+  float* ysum = reinterpret_cast<float*>(dec_smem + dec_ring_bytes(BITS, NT) - 128);
+  for (int i = threadIdx.x; i < p.T * DEC_ROWS; i += DEC_THREADS) ysum[i] = 0.0f;
+  Ring<BITS, BF, GU, NT> r;
+  r.init(smem_u32(dec_smem), bars, &abort_flag);
+  griddep_wait();
+  griddep_launch_dependents();
+  const int chunks = p.I / 128;
+  const int total = *p.plan.segments * chunks;
+  const int w0 = static_cast<int>(static_cast<int64_t>(total) * rank / cs);
+  const int w1 = static_cast<int>(static_cast<int64_t>(total) * (rank + 1) / cs);
+  auto segment_at = [&](int w, int& seg) {
+    Segment sg;
+    seg = w / chunks;
+    sg.c0 = w - seg * chunks;
+    sg.c1 = min(chunks, sg.c0 + (w1 - w));
+    sg.row_a = p.plan.expert[seg] * p.H + row0;
+    sg.row_b = sg.row_a + 64;
+    sg.tiles = (p.plan.count[seg] + 7) / 8;
+    sg.x = p.h + static_cast<size_t>(p.plan.tile0[seg]) * chunks * FRAG_BYTES;
+    return sg;
+  };
+  if (warp == DEC_WARPS) {
+    if (lane == 0) {
+      int it = 0;
+      bool ok = true;
+      for (int w = w0; w < w1 && ok;) {
+        int seg;
+        const Segment sg = segment_at(w, seg);
+        for (int c = sg.c0; c < sg.c1; ++c, ++it) {
+          if (!r.codes(&codes_map, sg, c, it)) {
+            ok = false;
+            break;
+          }
+          r.acts(sg, c, it);
+        }
+        w += sg.c1 - sg.c0;
+      }
+      r.drain(it);
+    }
+  } else {
+    int it = 0;
+    r.zoff = p.dn_zeros - p.dn_scales;
+    r.gi = p.dn_gi;
+    const int ra = warp * 16 + g, rb = ra + 8;
+    for (int w = w0; w < w1;) {
+      int seg;
+      const Segment sg = segment_at(w, seg);
+      w += sg.c1 - sg.c0;
+      float acc[NT][4];
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[t][j] = 0.0f;
+      r.scale_a = p.dn_scales + static_cast<size_t>(sg.row_a + ra) * p.dn_G;
+      r.scale_b = p.dn_scales + static_cast<size_t>(sg.row_a + rb) * p.dn_G;
+      if (!r.consume(sg.c0, sg.c1, sg.tiles, ra * (16 * BITS), rb * (16 * BITS), q, lane, it, acc)) break;
+      const int begin = p.plan.begin[seg], count = p.plan.count[seg];
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int i = 8 * t + 2 * q + j;
+          if (i < count) {
+            const float wt = p.plan.weight[begin + i];
+            float* y = ysum + p.plan.pair[begin + i] / p.top_k * DEC_ROWS + ra;
+            y[0] = fmaf(wt, acc[t][j], y[0]);
+            y[8] = fmaf(wt, acc[t][2 + j], y[8]);
+          }
+        }
+      __syncwarp();
+    }
+  }
+  if (cs > 1) {
+    cluster_sync();
+  } else {
+    __syncthreads();
+  }
+  for (int i = rank * DEC_THREADS + static_cast<int>(threadIdx.x); i < p.T * DEC_ROWS && !abort_flag;
+       i += cs * DEC_THREADS) {
+    float v = 0.0f;
+    for (int o = 0; o < cs; ++o) v += cs > 1 ? ld_dsmem_f(mapa_shared(smem_u32(&ysum[i]), o)) : ysum[i];
+    const int tok = i / DEC_ROWS, row = row0 + i % DEC_ROWS;
+    if (p.residual) v += h2f<BF>(p.residual[static_cast<size_t>(tok) * p.ld_res + row]);
+    p.Y[static_cast<size_t>(tok) * p.ldy + row] = f2h<BF>(v);
+  }
+  if (cs > 1) cluster_sync();
+  if (threadIdx.x == 0 && abort_flag) atomicOr(p.status, ST_TIMEOUT);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -712,18 +840,18 @@ __global__ void __launch_bounds__(DEC_WARPS * 32) moe_down_kernel(const MoeArgs 
 struct DecodeLaunch {
   bool bf16;
   int unit;      // 32, 64 or 128
-  int nt, rt;    // (1, 1) or (2, 2)
+  int nt;        // tiles a block holds sums for: 1, 2 or 4
   int cluster;   // blocks that split k
   int device;
   cudaStream_t stream;
 };
 
 template <int BITS>
-cudaError_t launch_linear_decode(const DecodeLaunch& l, const LinearDecodeArgs& a);
+cudaError_t launch_linear_decode(const DecodeLaunch& l, const CUtensorMap& codes, const LinearDecodeArgs& a);
 template <int BITS>
-cudaError_t launch_moe_gate_up(const DecodeLaunch& l, const MoeArgs& a, int slots);
+cudaError_t launch_moe_gate_up(const DecodeLaunch& l, const CUtensorMap& codes, const MoeArgs& a, int segments);
 template <int BITS>
-cudaError_t launch_moe_down(const DecodeLaunch& l, const MoeArgs& a);
+cudaError_t launch_moe_down(const DecodeLaunch& l, const CUtensorMap& codes, const MoeArgs& a);
 
 // A launch that may overlap the end of the kernel before it (every kernel here waits for that
 // kernel before it touches what it wrote).

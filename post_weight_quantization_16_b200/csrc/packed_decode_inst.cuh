@@ -5,41 +5,49 @@
 namespace gptq {
 
 namespace {
-template <bool BF, int GU, int NT, int RT>
-cudaError_t linear_of(const DecodeLaunch& l, const LinearDecodeArgs& a) {
-  const dim3 grid(static_cast<unsigned>((a.m + 16 * RT - 1) / (16 * RT) * l.cluster),
-                  static_cast<unsigned>((a.T + 8 * NT - 1) / (8 * NT)));
-  return launch_pdl(linear_decode_kernel<PACKED_BITS, BF, GU, NT, RT>, grid, dim3(DEC_WARPS * 32), 0, l.cluster,
-                    l.stream, a);
-}
-template <bool BF, int GU, int NT, int RT>
-cudaError_t gate_up_of(const DecodeLaunch& l, const MoeArgs& a, int slots) {
-  const dim3 grid(static_cast<unsigned>(a.I / (8 * RT)), static_cast<unsigned>(slots));
-  return launch_pdl(moe_gate_up_kernel<PACKED_BITS, BF, GU, NT, RT>, grid, dim3(DEC_WARPS * 32), 0, 1, l.stream, a);
-}
-template <bool BF, int GU, int NT, int RT>
-cudaError_t down_of(const DecodeLaunch& l, const MoeArgs& a) {
-  static std::atomic<uint64_t> done{0};
-  const auto kernel = moe_down_kernel<PACKED_BITS, BF, GU, NT, RT>;
-  const cudaError_t e = raise_smem_limit(done, l.device, kernel, DEC_WARPS * MOE_MAX_T * 16 * RT * 4);
-  if (e != cudaSuccess) return e;
-  const dim3 grid(static_cast<unsigned>((a.H + 16 * RT - 1) / (16 * RT) * l.cluster));
-  return launch_pdl(kernel, grid, dim3(DEC_WARPS * 32), static_cast<size_t>(DEC_WARPS) * a.T * 16 * RT * 4, l.cluster,
-                    l.stream, a);
-}
+template <bool BF, int GU, int NT>
+struct Of {
+  static cudaError_t linear(const DecodeLaunch& l, const CUtensorMap& codes, const LinearDecodeArgs& a) {
+    static std::atomic<uint64_t> done{0};
+    const auto kernel = linear_decode_kernel<PACKED_BITS, BF, GU, NT>;
+    const int smem = dec_ring_bytes(PACKED_BITS, NT);
+    const cudaError_t e = raise_smem_limit(done, l.device, kernel, smem);
+    if (e != cudaSuccess) return e;
+    const dim3 grid(static_cast<unsigned>((a.m + DEC_ROWS - 1) / DEC_ROWS * l.cluster));
+    return launch_pdl(kernel, grid, dim3(DEC_THREADS), smem, l.cluster, l.stream, codes, a);
+  }
+  static cudaError_t gate_up(const DecodeLaunch& l, const CUtensorMap& codes, const MoeArgs& a, int segments) {
+    static std::atomic<uint64_t> done{0};
+    const auto kernel = moe_gate_up_kernel<PACKED_BITS, BF, GU, NT>;
+    const int smem = dec_ring_bytes(PACKED_BITS, NT);
+    const cudaError_t e = raise_smem_limit(done, l.device, kernel, smem);
+    if (e != cudaSuccess) return e;
+    const dim3 grid(static_cast<unsigned>(a.I / 64 * l.cluster), static_cast<unsigned>(segments));
+    return launch_pdl(kernel, grid, dim3(DEC_THREADS), smem, l.cluster, l.stream, codes, a);
+  }
+  static cudaError_t down(const DecodeLaunch& l, const CUtensorMap& codes, const MoeArgs& a) {
+    static std::atomic<uint64_t> done{0};
+    const auto kernel = moe_down_kernel<PACKED_BITS, BF, GU, NT>;
+    const int ring = dec_ring_bytes(PACKED_BITS, NT);
+    const cudaError_t e = raise_smem_limit(done, l.device, kernel, ring + MOE_MAX_T * DEC_ROWS * 4);
+    if (e != cudaSuccess) return e;
+    const dim3 grid(static_cast<unsigned>(a.H / DEC_ROWS * l.cluster));
+    return launch_pdl(kernel, grid, dim3(DEC_THREADS), static_cast<size_t>(ring) + static_cast<size_t>(a.T) * DEC_ROWS * 4,
+                      l.cluster, l.stream, codes, a);
+  }
+};
 
 template <bool BF, int GU, typename F>
-cudaError_t by_tile(const DecodeLaunch& l, F&& f) {
-  if (l.nt == 1) return f(std::integral_constant<bool, BF>(), std::integral_constant<int, GU>(),
-                          std::integral_constant<int, 1>(), std::integral_constant<int, 1>());
-  return f(std::integral_constant<bool, BF>(), std::integral_constant<int, GU>(), std::integral_constant<int, 2>(),
-           std::integral_constant<int, 1>());
+cudaError_t by_tiles(const DecodeLaunch& l, F&& f) {
+  if (l.nt == 1) return f(Of<BF, GU, 1>());
+  if (l.nt == 2) return f(Of<BF, GU, 2>());
+  return f(Of<BF, GU, 4>());
 }
 template <bool BF, typename F>
 cudaError_t by_unit(const DecodeLaunch& l, F&& f) {
-  if (l.unit == 32) return by_tile<BF, 32>(l, f);
-  if (l.unit == 64) return by_tile<BF, 64>(l, f);
-  return by_tile<BF, 128>(l, f);
+  if (l.unit == 32) return by_tiles<BF, 32>(l, f);
+  if (l.unit == 64) return by_tiles<BF, 64>(l, f);
+  return by_tiles<BF, 128>(l, f);
 }
 template <typename F>
 cudaError_t by_type(const DecodeLaunch& l, F&& f) {
@@ -48,22 +56,18 @@ cudaError_t by_type(const DecodeLaunch& l, F&& f) {
 }  // namespace
 
 template <>
-cudaError_t launch_linear_decode<PACKED_BITS>(const DecodeLaunch& l, const LinearDecodeArgs& a) {
-  return by_type(l, [&](auto bf, auto gu, auto nt, auto rt) {
-    return linear_of<decltype(bf)::value, decltype(gu)::value, decltype(nt)::value, decltype(rt)::value>(l, a);
-  });
+cudaError_t launch_linear_decode<PACKED_BITS>(const DecodeLaunch& l, const CUtensorMap& codes,
+                                              const LinearDecodeArgs& a) {
+  return by_type(l, [&](auto of) { return decltype(of)::linear(l, codes, a); });
 }
 template <>
-cudaError_t launch_moe_gate_up<PACKED_BITS>(const DecodeLaunch& l, const MoeArgs& a, int slots) {
-  return by_type(l, [&](auto bf, auto gu, auto nt, auto rt) {
-    return gate_up_of<decltype(bf)::value, decltype(gu)::value, decltype(nt)::value, decltype(rt)::value>(l, a, slots);
-  });
+cudaError_t launch_moe_gate_up<PACKED_BITS>(const DecodeLaunch& l, const CUtensorMap& codes, const MoeArgs& a,
+                                            int segments) {
+  return by_type(l, [&](auto of) { return decltype(of)::gate_up(l, codes, a, segments); });
 }
 template <>
-cudaError_t launch_moe_down<PACKED_BITS>(const DecodeLaunch& l, const MoeArgs& a) {
-  return by_type(l, [&](auto bf, auto gu, auto nt, auto rt) {
-    return down_of<decltype(bf)::value, decltype(gu)::value, decltype(nt)::value, decltype(rt)::value>(l, a);
-  });
+cudaError_t launch_moe_down<PACKED_BITS>(const DecodeLaunch& l, const CUtensorMap& codes, const MoeArgs& a) {
+  return by_type(l, [&](auto of) { return decltype(of)::down(l, codes, a); });
 }
 
 }  // namespace gptq

@@ -7,8 +7,7 @@
 
 namespace gptq {
 
-// out[t][k] = X[t][perm[k]] (perm null: a copy into rows of n).  Grid (n / 1024 rounded up, tokens);
-// four columns a thread.
+// out[t][k] = X[t][perm[k]] in rows of n.  Grid (n / 1024 rounded up, tokens); four columns a thread.
 __global__ void __launch_bounds__(256) gather_x_kernel(const uint16_t* __restrict__ X, int64_t ldx, int n,
                                                        const int32_t* __restrict__ perm, uint16_t* __restrict__ out) {
   griddep_wait();
@@ -16,25 +15,42 @@ __global__ void __launch_bounds__(256) gather_x_kernel(const uint16_t* __restric
   const int k = (blockIdx.x * 256 + threadIdx.x) * 4;
   if (k >= n) return;
   const uint16_t* src = X + static_cast<size_t>(blockIdx.y) * ldx;
-  const int4 i = perm ? *reinterpret_cast<const int4*>(perm + k) : make_int4(k, k + 1, k + 2, k + 3);
+  const int4 i = *reinterpret_cast<const int4*>(perm + k);
   const ushort4 v = make_ushort4(src[i.x], src[i.y], src[i.z], src[i.w]);
   *reinterpret_cast<ushort4*>(out + static_cast<size_t>(blockIdx.y) * n + k) = v;
 }
 
-// The activations of list position blockIdx.y in its expert's sweep order.
-__global__ void __launch_bounds__(256) moe_gather_kernel(const uint16_t* __restrict__ X, int64_t ldx, int n,
-                                                         const int32_t* __restrict__ perm, MoePlan plan, int top_k,
-                                                         const int32_t* __restrict__ ids,
-                                                         uint16_t* __restrict__ out) {
+// Few tokens in fragment order, [chunk][tiles][FRAG_BYTES], for units of gu columns.  Grid (chunks,
+// tiles), 128 threads, one 16-byte piece each; tokens past T repeat the last one.
+__global__ void __launch_bounds__(128) fragment_kernel(const uint16_t* __restrict__ X, int64_t ldx, int T, int gu,
+                                                       const int32_t* __restrict__ perm, uint4* __restrict__ out,
+                                                       int* __restrict__ status) {
   griddep_wait();
   griddep_launch_dependents();
-  const int k = (blockIdx.x * 256 + threadIdx.x) * 4;
-  if (k >= n) return;
-  const int pair = plan.pair[blockIdx.y], e = ids[pair];
-  const uint16_t* src = X + static_cast<size_t>(pair / top_k) * ldx;
-  const int4 i = *reinterpret_cast<const int4*>(perm + static_cast<size_t>(e) * n + k);
-  const ushort4 v = make_ushort4(src[i.x], src[i.y], src[i.z], src[i.w]);
-  *reinterpret_cast<ushort4*>(out + static_cast<size_t>(blockIdx.y) * n + k) = v;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *status = 0;
+  const int kb = threadIdx.x >> 5, n = (threadIdx.x >> 2) & 7, q = threadIdx.x & 3;
+  const int t = min(static_cast<int>(blockIdx.y) * 8 + n, T - 1);
+  out[(static_cast<size_t>(blockIdx.x) * gridDim.y + blockIdx.y) * (FRAG_BYTES / 16) + threadIdx.x] =
+      frag_gather(X + t * ldx, perm, static_cast<int>(blockIdx.x) * 128 + frag_column(gu, kb, q));
+}
+
+// The experts' tokens in fragment order and their expert's sweep order.  Grid (chunks, tiles at most).
+__global__ void __launch_bounds__(128) moe_fragment_kernel(const uint16_t* __restrict__ X, int64_t ldx, int H, int gu,
+                                                           const int32_t* __restrict__ perm, MoePlan plan, int top_k,
+                                                           uint4* __restrict__ out) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int tile = static_cast<int>(blockIdx.y);
+  if (tile >= *plan.tiles) return;
+  const int seg = plan.tile_seg[tile], tile0 = plan.tile0[seg], count = plan.count[seg];
+  const int kb = threadIdx.x >> 5, n = (threadIdx.x >> 2) & 7, q = threadIdx.x & 3;
+  const int i = min((tile - tile0) * 8 + n, count - 1), tiles = (count + 7) / 8;
+  const int t = plan.pair[plan.begin[seg] + i] / top_k;
+  const size_t at = (static_cast<size_t>(tile0) * gridDim.x + static_cast<size_t>(blockIdx.x) * tiles + (tile - tile0)) *
+                        (FRAG_BYTES / 16) +
+                    threadIdx.x;
+  out[at] = frag_gather(X + t * ldx, perm ? perm + static_cast<size_t>(plan.expert[seg]) * H : nullptr,
+                        static_cast<int>(blockIdx.x) * 128 + frag_column(gu, kb, q));
 }
 
 // ------------------------------------------------------------------------------------------
@@ -48,6 +64,7 @@ struct RouterArgs {
   int64_t ldx;
   const uint16_t* R;  // [E x H]
   int T, E, H, top_k, renorm;
+  int seg_pairs;       // pairs of a segment at most
   double* logits;      // [T x E] (workspace)
   int32_t* ids;        // [T x top_k] (workspace)
   float* weights;      // [T x top_k] (workspace)
@@ -69,6 +86,7 @@ __global__ void __launch_bounds__(ROUTER_WARPS * 32) moe_router_kernel(const Rou
   __shared__ int counts[MOE_MAX_E];
   __shared__ int begins[MOE_MAX_E];
   __shared__ int slots[MOE_MAX_E];
+  __shared__ int tiles[MOE_MAX_E];
   griddep_wait();
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
@@ -193,29 +211,41 @@ __global__ void __launch_bounds__(ROUTER_WARPS * 32) moe_router_kernel(const Rou
   }
   __syncthreads();
   if (warp == 0) {
-    int base = 0, slot = 0;
+    // exclusive sums over the experts of pairs, segments and tiles
+    int base = 0, seg = 0, tile = 0;
     for (int e0 = 0; e0 < p.E; e0 += 32) {
       const int e = e0 + lane;
       const int n = e < p.E ? counts[e] : 0;
-      int inc = n;
+      const int ns = (n + p.seg_pairs - 1) / p.seg_pairs, nt = (n + 7) / 8;
+      int in = n, is = ns, it = nt;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += u;
+        const int un = __shfl_up_sync(0xffffffffu, in, o), us = __shfl_up_sync(0xffffffffu, is, o),
+                  ut = __shfl_up_sync(0xffffffffu, it, o);
+        if (lane >= o) {
+          in += un;
+          is += us;
+          it += ut;
+        }
       }
-      const unsigned has = __ballot_sync(0xffffffffu, n > 0);
       if (e < p.E) {
-        begins[e] = base + inc - n;
-        slots[e] = slot + __popc(has & ((1u << lane) - 1u));
+        begins[e] = base + in - n;
+        slots[e] = seg + is - ns;
+        tiles[e] = tile + it - nt;
       }
-      base += __shfl_sync(0xffffffffu, inc, 31);
-      slot += __popc(has);
+      base += __shfl_sync(0xffffffffu, in, 31);
+      seg += __shfl_sync(0xffffffffu, is, 31);
+      tile += __shfl_sync(0xffffffffu, it, 31);
     }
-    if (lane == 0) *p.plan.active = slot;
+    if (lane == 0) {
+      *p.plan.segments = seg;
+      *p.plan.tiles = tile;
+    }
   }
   __syncthreads();
   for (int e = warp; e < p.E; e += ROUTER_WARPS) {
-    if (counts[e] == 0) continue;
+    const int n = counts[e];
+    if (n == 0) continue;
     int at = begins[e];
     for (int i = lane; i < (pairs + 31) / 32 * 32; i += 32) {
       const bool mine = i < pairs && __ldcg(p.ids + i) == e;
@@ -227,11 +257,15 @@ __global__ void __launch_bounds__(ROUTER_WARPS * 32) moe_router_kernel(const Rou
       }
       at += __popc(m);
     }
-    if (lane == 0) {
-      p.plan.expert[slots[e]] = e;
-      p.plan.begin[slots[e]] = begins[e];
-      p.plan.count[slots[e]] = counts[e];
+    const int per = p.seg_pairs;  // a multiple of 8
+    for (int k = lane; k * per < n; k += 32) {
+      const int s = slots[e] + k;
+      p.plan.expert[s] = e;
+      p.plan.begin[s] = begins[e] + k * per;
+      p.plan.count[s] = min(per, n - k * per);
+      p.plan.tile0[s] = tiles[e] + k * (per / 8);
     }
+    for (int k = lane; k * 8 < n; k += 32) p.plan.tile_seg[tiles[e] + k] = slots[e] + k * 8 / per;
   }
 }
 

@@ -113,7 +113,7 @@ _SIGS = {
                                                                        ctypes.c_int]),
     "gptq_dequant_linear_backward": (ctypes.c_int, [ctypes.POINTER(LinearGradArgs), ctypes.c_int, _P]),
     "gptq_dequant_moe_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int,
-                                                           ctypes.c_int64, ctypes.c_int64, ctypes.c_int]),
+                                                           ctypes.c_int64, ctypes.c_int64]),
     "gptq_dequant_moe": (ctypes.c_int, [ctypes.POINTER(MoeArgs), ctypes.c_int, _P]),
     "gptq_quantize_layers": (ctypes.c_int, [ctypes.POINTER(LayerJob), ctypes.c_int, ctypes.c_int, _P]),
     "gptq_pipeline_create": (ctypes.c_int, [ctypes.POINTER(_P), ctypes.POINTER(ctypes.c_int64),
@@ -527,7 +527,7 @@ def dequant_moe(X: torch.Tensor, router: torch.Tensor, gate_up: tuple, down: tup
         y_ptr, ldy = _rows("out", out, (T, H), X.dtype, dev)
         ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
         weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
-        need = int(lib().gptq_dequant_moe_workspace_bytes(T, E, top_k, H, I, int(perm is not None)))
+        need = int(lib().gptq_dequant_moe_workspace_bytes(T, E, top_k, H, I))
         if need == 0:
             raise GPTQError(ERR_ARG, "gptq_dequant_moe_workspace_bytes")
         ws = _workspace(need, workspace, dev)
