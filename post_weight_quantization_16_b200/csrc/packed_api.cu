@@ -42,12 +42,16 @@ GroupIndex group_index(int g) {
 }
 
 gptq_status check_device(int device) {
-  int ndev = 0;
-  if (cudaGetDeviceCount(&ndev) != cudaSuccess || device < 0 || device >= ndev) {
-    cudaGetLastError();
-    return GPTQ_ERR_CUDA;
+  static std::atomic<int> known{0};  // devices; does not change during the process
+  int ndev = known.load(std::memory_order_relaxed);
+  if (ndev == 0) {
+    if (cudaGetDeviceCount(&ndev) != cudaSuccess) {
+      cudaGetLastError();
+      return GPTQ_ERR_CUDA;
+    }
+    known.store(ndev, std::memory_order_relaxed);
   }
-  return GPTQ_OK;
+  return device >= 0 && device < ndev ? GPTQ_OK : GPTQ_ERR_CUDA;
 }
 
 template <typename F>
@@ -70,6 +74,13 @@ int k_split(int64_t tiles, int chunks) {
 
 // Tokens up to which the warp-level kernel runs; beyond, tcgen05.
 constexpr int kDecodeTokens = 16;
+
+// Tokens that the decode kernels lay out themselves, chunk range by chunk range, instead of a launch
+// of its own before them: every block of 128 rows repeats the layout, which is cheap for plain
+// 16-byte loads and for one or two gathered rows.
+bool lay_out_locally(int64_t T, bool perm, int chunks_per_block) {
+  return T <= (perm ? 2 : 8) && T * chunks_per_block * 256 <= DEC_LOCAL_BYTES;
+}
 
 size_t linear_workspace(int64_t T, int64_t n, int act_order) {
   const size_t rows = T <= kDecodeTokens ? static_cast<size_t>((T + 7) / 8 * 8) : act_order ? static_cast<size_t>(T) : 0;
@@ -278,10 +289,16 @@ extern "C" gptq_status gptq_dequant_linear(const gptq_linear_args* args, int dev
   l.cluster = k_split((m + DEC_ROWS - 1) / DEC_ROWS, d.chunks);
   l.device = device;
   l.stream = st;
+  l.chunks = (d.chunks + l.cluster - 1) / l.cluster;
+  l.local = lay_out_locally(T, a.W.perm != nullptr, l.chunks) ? T : 0;
+  d.X = X;
+  d.ldx = ldx;
+  d.perm = a.W.perm;
   CUtensorMap cmap;
   const gptq_status s = encode_codes(&cmap, a.W, 64);
   if (s != GPTQ_OK) return s;
-  CK(launch_pdl(fragment_kernel, dim3(d.chunks, d.tiles), dim3(128), 0, 1, st, X, ldx, T, l.unit, a.W.perm,
+  if (!l.local)
+    CK(launch_pdl(fragment_kernel, dim3(d.chunks, d.tiles), dim3(128), 0, 1, st, X, ldx, T, l.unit, a.W.perm,
                 reinterpret_cast<uint4*>(ws + 256), d.status));
   CK(by_bits(a.W.qp.bits, [&](auto b) { return launch_linear_decode<decltype(b)::value>(l, cmap, d); }));
   return GPTQ_OK;
@@ -448,11 +465,25 @@ extern "C" gptq_status gptq_dequant_moe(const gptq_moe_args* args, int device, v
                 ROUTER_CLUSTER, st, r));
 
   const int gg = group_width(a.gate_up), gd = group_width(a.down);
-  CK(launch_pdl(moe_fragment_kernel, dim3(static_cast<unsigned>(H / 128), lay.max_tiles), dim3(128), 0, 1, st, r.X, a.ld_x,
-                r.H, std::min(gg, 128), a.gate_up.perm, r.plan, a.top_k, reinterpret_cast<uint4*>(ws + lay.x)));
+  DecodeLaunch l;
+  l.bf16 = bf;
+  l.nt = moe_nt(a.T);
+  l.device = device;
+  l.stream = st;
+  l.unit = std::min(gg, 128);
+  l.cluster = k_split(I / 64 * std::min<int64_t>(a.E, pairs), r.H / 128);
+  l.chunks = (r.H / 128 + l.cluster - 1) / l.cluster;
+  l.local = lay_out_locally(a.T, a.gate_up.perm != nullptr, l.chunks) ? r.T : 0;
+  if (!l.local)
+    CK(launch_pdl(moe_fragment_kernel, dim3(static_cast<unsigned>(H / 128), lay.max_tiles), dim3(128), 0, 1, st, r.X,
+                  a.ld_x, r.H, std::min(gg, 128), a.gate_up.perm, r.plan, a.top_k,
+                  reinterpret_cast<uint4*>(ws + lay.x)));
 
   MoeArgs m;
   m.x = ws + lay.x;
+  m.X = r.X;
+  m.ldx = a.ld_x;
+  m.perm = a.gate_up.perm;
   m.plan = r.plan;
   m.T = r.T;
   m.E = r.E;
@@ -475,16 +506,10 @@ extern "C" gptq_status gptq_dequant_moe(const gptq_moe_args* args, int device, v
   m.ld_res = a.ld_res;
   m.ldy = a.ld_y;
   m.Y = static_cast<uint16_t*>(a.Y);
-  DecodeLaunch l;
-  l.bf16 = bf;
-  l.nt = moe_nt(a.T);
-  l.device = device;
-  l.stream = st;
-  l.unit = std::min(gg, 128);
-  l.cluster = k_split(I / 64 * std::min<int64_t>(a.E, pairs), m.H / 128);
   CK(by_bits(a.gate_up.qp.bits,
              [&](auto b) { return launch_moe_gate_up<decltype(b)::value>(l, gmap, m, lay.max_segments); }));
   l.unit = m.dn_unit;
+  l.local = 0;
   l.cluster = k_split(m.H / DEC_ROWS, static_cast<int>(std::min<int64_t>(a.E, pairs)) * (m.I / 128));
   CK(by_bits(a.down.qp.bits, [&](auto b) { return launch_moe_down<decltype(b)::value>(l, dmap, m); }));
   return GPTQ_OK;

@@ -90,6 +90,16 @@ __device__ __forceinline__ uint32_t fma2_f16(uint32_t a, uint32_t b, uint32_t c)
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// Wait of a whole warp: one lane polls, so that the warp stays converged (the MMAs and tensor-memory
+// loads that follow are warp-wide instructions; lanes that each leave a polling loop on their own
+// need not run together afterwards), then the barrier's completion is made known to the others.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int lane) {
+  int ok = 1;
+  if (lane == 0) ok = mbar_wait_bounded(bar, parity, abort_flag) ? 1 : 0;
+  __syncwarp();
+  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+
 template <bool BF>
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                           uint32_t b0, uint32_t b1) {
@@ -354,14 +364,30 @@ struct Segment {
   const uint8_t* x;     // fragment order, [chunk][tiles][FRAG_BYTES]
 };
 
-template <int BITS, bool BF, int GU, int NT>
+// XL: the activations of the block's chunks are laid out in shared memory by its own consumer warps
+// before the loop (few tokens: no launch of its own, no copies in the ring); NT is 1 then.
+template <int BITS, bool BF, int GU, int NT, bool XL>
 struct Ring {
   using Raw = RawChunk<BITS, GU>;
   static constexpr int UNITS = Raw::UNITS, BLOCKS = Raw::BLOCKS;
-  static constexpr int STAGES = dec_stages(BITS, NT), STAGE = dec_stage_bytes(BITS, NT), CODES = dec_code_bytes(BITS);
+  static constexpr int STAGES = dec_stages(BITS, XL ? 0 : NT), STAGE = dec_stage_bytes(BITS, XL ? 0 : NT),
+                       CODES = dec_code_bytes(BITS);
+  static_assert(!XL || NT == 1, "local activations: one tile");
 
   uint32_t base, full, empty;  // shared-memory addresses: stages, barriers
   volatile int* abort_flag;
+
+  // Position in the ring: stage and the parity of its use.
+  struct Cursor {
+    int s = 0;
+    uint32_t ph = 0;
+    __device__ __forceinline__ void next() {
+      if (++s == STAGES) {
+        s = 0;
+        ph ^= 1u;
+      }
+    }
+  };
 
   __device__ __forceinline__ void init(uint32_t smem_base, uint64_t* bars, int* flag) {
     base = smem_base;
@@ -384,12 +410,13 @@ struct Ring {
     const int s = it % STAGES;
     if (!mbar_wait_bounded(empty + 8 * s, (static_cast<uint32_t>(it / STAGES) & 1u) ^ 1u, abort_flag)) return false;
     const uint32_t fb = full + 8 * s, st = base + s * STAGE;
-    mbar_arrive_expect_tx(fb, static_cast<uint32_t>(CODES + g.tiles * FRAG_BYTES));
+    mbar_arrive_expect_tx(fb, static_cast<uint32_t>(CODES + (XL ? 0 : g.tiles * FRAG_BYTES)));
     tma_load_2d(st, map, fb, c * (4 * BITS), g.row_a);
     tma_load_2d(st + CODES / 2, map, fb, c * (4 * BITS), g.row_b);
     return true;
   }
   __device__ __forceinline__ void acts(const Segment& g, int c, int it) const {
+    if (XL) return;
     const int s = it % STAGES;
     bulk_load(base + s * STAGE + CODES, g.x + static_cast<size_t>(c) * g.tiles * FRAG_BYTES,
               static_cast<uint32_t>(g.tiles * FRAG_BYTES), full + 8 * s);
@@ -400,79 +427,120 @@ struct Ring {
       mbar_wait_drain(full + 8 * (i % STAGES), static_cast<uint32_t>(i / STAGES) & 1u);
   }
 
-  // Consumer warp: its rows' scales and zero-points (rows g and g + 8 of its 16).
-  const float *scale_a, *scale_b;
-  ptrdiff_t zoff;  // zeros - scales (elements)
-  GroupIndex gi;
+  // Local activations: pieces [chunk][block][token][quad position] of 16 bytes.
+  uint32_t xs;   // shared-memory address
+  int xtok;      // tokens in them, 1 .. 8
+  template <typename RowOf>
+  __device__ __forceinline__ void lay_out(uint4* dst, int c0, int c1, int tokens, const int32_t* perm, RowOf&& row_of) {
+    xs = smem_u32(dst);
+    xtok = tokens;
+    const int pieces = (c1 - c0) * 16 * tokens;
+    for (int i = threadIdx.x; i < pieces; i += DEC_WARPS * 32) {
+      const int q = i & 3, n = (i >> 2) % tokens, ck = (i >> 2) / tokens;
+      dst[i] = frag_gather(row_of(n), perm, (c0 + (ck >> 2)) * 128 + frag_column(GU, ck & 3, q));
+    }
+    asm volatile("bar.sync 1, %0;" ::"n"(DEC_WARPS * 32) : "memory");  // the consumer warps
+  }
 
-  struct Params {
-    float s[2][UNITS], z[2][UNITS];
-  };
-  __device__ __forceinline__ void fetch(Params& p, int c) const {
+  // Consumer warp.  A lane fetches one of the four parameter rows of its quad's two weight rows:
+  // q = 0 scales of row a, 1 its zero-points, 2 and 3 those of row b; four consecutive units at a
+  // time, one window ahead (a window of a row is mostly one 32-byte sector); shuffles spread them.
+  const float* param;
+  GroupIndex gi;
+  // `left` units remain from unit `u0` of chunk c0 on.
+  __device__ __forceinline__ void window(float (&v)[4], int c0, int u0, int left) const {
+    if (UNITS > 1 || gi.div == 1) {
+      const float* at = param + c0 * UNITS + u0;
 #pragma unroll
-    for (int u = 0; u < UNITS; ++u) {
-      const int g = group_of<GU>(gi, c, u);
-      p.s[0][u] = __ldg(scale_a + g);
-      p.z[0][u] = __ldg(scale_a + zoff + g);
-      p.s[1][u] = __ldg(scale_b + g);
-      p.z[1][u] = __ldg(scale_b + zoff + g);
+      for (int j = 0; j < 4; ++j)
+        if (j < left) v[j] = __ldg(at + j);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j < left) v[j] = __ldg(param + group_of<GU>(gi, c0 + u0 + j, 0));
     }
   }
 
-  // acc[t] += the warp's 16 rows x tile t over chunks [c0, c1); offa, offb: byte offsets of the
-  // lane's two rows in a stage.  `it` as in the producer.  False when a wait ran out.
-  __device__ __forceinline__ bool consume(int c0, int c1, int tiles, uint32_t offa, uint32_t offb, int q, int lane,
-                                          int& it, float (&acc)[NT][4]) const {
-    Params next;
-    if (c0 < c1) fetch(next, c0);
-    for (int c = c0; c < c1; ++c, ++it) {
-      const Params pr = next;
-      if (c + 1 < c1) fetch(next, c + 1);
-      const int s = it % STAGES;
-      // (all lanes leave together: the MMAs below need the whole warp)
-      if (!__all_sync(0xffffffffu,
-                      mbar_wait_bounded(full + 8 * s, static_cast<uint32_t>(it / STAGES) & 1u, abort_flag)))
-        return false;
-      const uint32_t st = base + s * STAGE;
-      Raw ra, rb;
-      ra.load(st + offa, q);
-      rb.load(st + offb, q);
+  // acc[t] += the warp's 16 rows x tile t over chunks [c0, c1), TL tiles; offa, offb: byte offsets
+  // of the lane's two rows in a stage.  False when a wait ran out.
+  template <int TL>
+  __device__ __forceinline__ bool consume(int c0, int c1, uint32_t offa, uint32_t offb, int lane, Cursor& cur,
+                                          float (&acc)[NT][4]) const {
+    constexpr int PER = 4 / UNITS;  // chunks of a window
+    const int q = lane & 3, src = lane & 28;
+    uint32_t xat = XL ? xs + static_cast<uint32_t>((min(lane >> 2, xtok - 1) * 4 + q) * 16) : 0u;
+    const uint32_t xstep = XL ? static_cast<uint32_t>(xtok * 64) : 0u;
+    int left = (c1 - c0) * UNITS, u0 = 0;
+    float next[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    window(next, c0, 0, left);
+    while (left > 0) {
+      float now[4];
 #pragma unroll
-      for (int u = 0; u < UNITS; ++u) {
-        float sum[NT][4];
+      for (int j = 0; j < 4; ++j) now[j] = next[j];
+      u0 += 4;
+      window(next, c0, u0, left - 4);
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+      for (int jj = 0; jj < PER; ++jj) {
+        if (jj * UNITS < left) {
+          if (!warp_wait(full + 8 * cur.s, cur.ph, abort_flag, lane)) return false;
+          const uint32_t st = base + cur.s * STAGE;
+          Raw ra, rb;
+          ra.load(st + offa, q);
+          rb.load(st + offb, q);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) sum[t][j] = 0.0f;
-        const ZeroTerm za = zero_term<BITS, BF>(pr.z[0][u]), zb = zero_term<BITS, BF>(pr.z[1][u]);
+          for (int u = 0; u < UNITS; ++u) {
+            float sum[TL][4];
 #pragma unroll
-        for (int b = 0; b < BLOCKS; ++b) {
-          uint32_t pa[4], pb[4], v, v1;
-          ra.block(u, b, q, v, v1);
-          unpack8<BITS, BF>(v, v1, za, pa);
-          rb.block(u, b, q, v, v1);
-          unpack8<BITS, BF>(v, v1, zb, pb);
+            for (int t = 0; t < TL; ++t)
 #pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            if (t < tiles) {
-              const uint4 x = lds128(st + CODES + t * FRAG_BYTES + (u * BLOCKS + b) * 512 + lane * 16);
-              mma_16816<BF>(sum[t], pa[0], pb[0], pa[1], pb[1], x.x, x.y);
-              mma_16816<BF>(sum[t], pa[2], pb[2], pa[3], pb[3], x.z, x.w);
+              for (int j = 0; j < 4; ++j) sum[t][j] = 0.0f;
+            const float pv = now[(jj * UNITS + u) % 4];
+            const float s_a = __shfl_sync(0xffffffffu, pv, src), s_b = __shfl_sync(0xffffffffu, pv, src | 2);
+            const ZeroTerm za = zero_term<BITS, BF>(__shfl_sync(0xffffffffu, pv, src | 1)),
+                           zb = zero_term<BITS, BF>(__shfl_sync(0xffffffffu, pv, src | 3));
+#pragma unroll
+            for (int b = 0; b < BLOCKS; ++b) {
+              uint32_t pa[4], pb[4], v, v1;
+              ra.block(u, b, q, v, v1);
+              unpack8<BITS, BF>(v, v1, za, pa);
+              rb.block(u, b, q, v, v1);
+              unpack8<BITS, BF>(v, v1, zb, pb);
+#pragma unroll
+              for (int t = 0; t < TL; ++t) {
+                const uint4 x = lds128(XL ? xat : st + CODES + t * FRAG_BYTES + (u * BLOCKS + b) * 512 + lane * 16);
+                mma_16816<BF>(sum[t], pa[0], pb[0], pa[1], pb[1], x.x, x.y);
+                mma_16816<BF>(sum[t], pa[2], pb[2], pa[3], pb[3], x.z, x.w);
+              }
+              if (XL) xat += xstep;
+            }
+#pragma unroll
+            for (int t = 0; t < TL; ++t) {
+              acc[t][0] = fmaf(s_a, sum[t][0], acc[t][0]);
+              acc[t][1] = fmaf(s_a, sum[t][1], acc[t][1]);
+              acc[t][2] = fmaf(s_b, sum[t][2], acc[t][2]);
+              acc[t][3] = fmaf(s_b, sum[t][3], acc[t][3]);
             }
           }
-        }
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          acc[t][0] = fmaf(pr.s[0][u], sum[t][0], acc[t][0]);
-          acc[t][1] = fmaf(pr.s[0][u], sum[t][1], acc[t][1]);
-          acc[t][2] = fmaf(pr.s[1][u], sum[t][2], acc[t][2]);
-          acc[t][3] = fmaf(pr.s[1][u], sum[t][3], acc[t][3]);
+          // The stage's loads have to be done, not only issued, before it is given back: with 16 warps'
+          // loads queued, the copy that refills it was seen to overtake them where only the arrival
+          // stood here (run-to-run differences; none with the fence, which costs 1 %).
+          __threadfence_block();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(empty + 8 * cur.s);
+          cur.next();
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(empty + 8 * s);
+      left -= 4;
     }
     return true;
+  }
+  // The same for a number of tiles known at run time (1 .. NT): loops without conditions inside.
+  __device__ __forceinline__ bool consume_tiles(int tiles, int c0, int c1, uint32_t offa, uint32_t offb, int lane,
+                                                Cursor& cur, float (&acc)[NT][4]) const {
+    if (NT == 1 || tiles == 1) return consume<1>(c0, c1, offa, offb, lane, cur, acc);
+    if (NT == 2 || tiles == 2) return consume<(NT < 2 ? NT : 2)>(c0, c1, offa, offb, lane, cur, acc);
+    if (tiles == 3) return consume<(NT < 3 ? NT : 3)>(c0, c1, offa, offb, lane, cur, acc);
+    return consume<NT>(c0, c1, offa, offb, lane, cur, acc);
   }
 };
 
@@ -499,9 +567,13 @@ __device__ __forceinline__ float ld_dsmem_f(uint32_t addr) {
 // the linear layer for few tokens
 // ------------------------------------------------------------------------------------------
 constexpr int DEC_MAX_TILES = 4;
+constexpr int DEC_LOCAL_BYTES = 32 * 1024;  // local activations of a block at most
 
 struct LinearDecodeArgs {
-  const uint8_t* x;  // fragment order, [chunk][tiles][FRAG_BYTES]
+  const uint8_t* x;  // fragment order, [chunk][tiles][FRAG_BYTES] (not with local activations)
+  const uint16_t* X;  // local activations: the caller's [T x n], and its order
+  int64_t ldx;
+  const int32_t* perm;
   const float *scales, *zeros;
   int T, tiles, m, chunks, G;
   GroupIndex gi;
@@ -513,7 +585,7 @@ struct LinearDecodeArgs {
   int* status;
 };
 
-template <int BITS, bool BF, int GU, int NT>
+template <int BITS, bool BF, int GU, int NT, bool XL>
 __global__ void __launch_bounds__(DEC_THREADS)
     linear_decode_kernel(const __grid_constant__ CUtensorMap codes_map, const LinearDecodeArgs p) {
   extern __shared__ uint8_t dec_smem_raw[];
@@ -524,7 +596,7 @@ __global__ void __launch_bounds__(DEC_THREADS)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   const int cs = static_cast<int>(cluster_nctarank()), rank = static_cast<int>(cluster_ctarank());
   const int row0 = static_cast<int>(blockIdx.x) / cs * DEC_ROWS;
-  Ring<BITS, BF, GU, NT> r;
+  Ring<BITS, BF, GU, NT, XL> r;
   r.init(smem_u32(dec_smem), bars, &abort_flag);
   Segment sg;
   sg.row_a = row0;
@@ -533,17 +605,20 @@ __global__ void __launch_bounds__(DEC_THREADS)
   sg.c1 = p.chunks * (rank + 1) / cs;
   sg.tiles = p.tiles;
   sg.x = p.x;
-  bool ok = true;
+  if (XL) {
+    griddep_wait();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
+  }
   if (warp == DEC_WARPS) {
     if (lane == 0) {
+      const int n = sg.c1 - sg.c0, ahead = min(Ring<BITS, BF, GU, NT, XL>::STAGES, n);
+      int it = 0;
       // the launch before this one laid out x and had waited for all earlier work: the weights can
       // be read before it ends, x cannot
-      const int ahead = min(Ring<BITS, BF, GU, NT>::STAGES, sg.c1 - sg.c0);
-      int it = 0;
       for (; it < ahead; ++it) r.codes(&codes_map, sg, sg.c0 + it, it);
-      griddep_wait();
+      if (!XL) griddep_wait();
       for (int i = 0; i < ahead; ++i) r.acts(sg, sg.c0 + i, i);
-      for (; it < sg.c1 - sg.c0; ++it) {
+      for (; it < n; ++it) {
         if (!r.codes(&codes_map, sg, sg.c0 + it, it)) break;
         r.acts(sg, sg.c0 + it, it);
       }
@@ -556,14 +631,16 @@ __global__ void __launch_bounds__(DEC_THREADS)
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[t][j] = 0.0f;
-    const int ra = warp * 16 + g, rb = ra + 8;  // rows past m repeat the last one's parameters, unstored
-    r.scale_a = p.scales + static_cast<size_t>(min(row0 + ra, p.m - 1)) * p.G;
-    r.scale_b = p.scales + static_cast<size_t>(min(row0 + rb, p.m - 1)) * p.G;
-    r.zoff = p.zeros - p.scales;
+    const int ra = warp * 16 + g, rb = ra + 8;
+    // (rows past m repeat the last one's parameters, unstored)
+    r.param = ((q & 1) ? p.zeros : p.scales) + static_cast<size_t>(min(row0 + ((q & 2) ? rb : ra), p.m - 1)) * p.G;
     r.gi = p.gi;
-    int it = 0;
-    ok = r.consume(sg.c0, sg.c1, sg.tiles, ra * (16 * BITS), rb * (16 * BITS), q, lane, it, acc);
-    griddep_wait();  // (the residual and the outputs are touched from here on)
+    if (XL)
+      r.lay_out(reinterpret_cast<uint4*>(dec_smem + dec_ring_bytes(BITS, 0) - 128), sg.c0, sg.c1, p.T, p.perm,
+                [&](int n) { return p.X + n * p.ldx; });
+    typename Ring<BITS, BF, GU, NT, XL>::Cursor cur;
+    r.template consume<NT>(sg.c0, sg.c1, ra * (16 * BITS), rb * (16 * BITS), lane, cur, acc);
+    if (!XL) griddep_wait();  // (the residual and the outputs are touched from here on)
 #pragma unroll
     for (int t = 0; t < NT; ++t)
       red[(warp * NT + t) * 32 + lane] = make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
@@ -632,6 +709,9 @@ struct MoePlan {
 
 struct MoeArgs {
   const uint8_t* x;  // fragment order: segment s at tile0[s] * (H / 128) * FRAG_BYTES, [chunk][tiles][FRAG_BYTES]
+  const uint16_t* X;  // local activations: the caller's [T x H], and the experts' orders
+  int64_t ldx;
+  const int32_t* perm;
   MoePlan plan;
   int T, E, top_k, H, I;
   const float *gu_scales, *gu_zeros, *dn_scales, *dn_zeros;
@@ -649,7 +729,7 @@ struct MoeArgs {
 // product).  Grid (I / 64 * cluster, segments): a block's stage holds 64 gate rows and the same 64
 // up rows; a warp takes eight of each as rows 0-7 and 8-15 of its MMA, so both halves of an h value
 // end up in one lane.
-template <int BITS, bool BF, int GU, int NT>
+template <int BITS, bool BF, int GU, int NT, bool XL>
 __global__ void __launch_bounds__(DEC_THREADS)
     moe_gate_up_kernel(const __grid_constant__ CUtensorMap codes_map, const MoeArgs p) {
   extern __shared__ uint8_t dec_smem_raw[];
@@ -659,7 +739,7 @@ __global__ void __launch_bounds__(DEC_THREADS)
   uint8_t* dec_smem = align128(dec_smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   const int cs = static_cast<int>(cluster_nctarank()), rank = static_cast<int>(cluster_ctarank());
-  Ring<BITS, BF, GU, NT> r;
+  Ring<BITS, BF, GU, NT, XL> r;
   r.init(smem_u32(dec_smem), bars, &abort_flag);
   griddep_wait();
   griddep_launch_dependents();
@@ -691,12 +771,14 @@ __global__ void __launch_bounds__(DEC_THREADS)
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[t][j] = 0.0f;
     const int ra = warp * 8 + g;
-    r.scale_a = p.gu_scales + static_cast<size_t>(sg.row_a + ra) * p.gu_G;
-    r.scale_b = p.gu_scales + static_cast<size_t>(sg.row_b + ra) * p.gu_G;
-    r.zoff = p.gu_zeros - p.gu_scales;
+    r.param = ((q & 1) ? p.gu_zeros : p.gu_scales) + static_cast<size_t>(((q & 2) ? sg.row_b : sg.row_a) + ra) * p.gu_G;
     r.gi = p.gu_gi;
-    int it = 0;
-    r.consume(sg.c0, sg.c1, sg.tiles, ra * (16 * BITS), (ra + 64) * (16 * BITS), q, lane, it, acc);
+    if (XL)
+      r.lay_out(reinterpret_cast<uint4*>(dec_smem + dec_ring_bytes(BITS, 0) - 128), sg.c0, sg.c1, count,
+                p.perm ? p.perm + static_cast<size_t>(e) * p.H : nullptr,
+                [&](int n) { return p.X + p.plan.pair[p.plan.begin[seg] + n] / p.top_k * p.ldx; });
+    typename Ring<BITS, BF, GU, NT, XL>::Cursor cur;
+    r.consume_tiles(sg.tiles, sg.c0, sg.c1, ra * (16 * BITS), (ra + 64) * (16 * BITS), lane, cur, acc);
 #pragma unroll
     for (int t = 0; t < NT; ++t)
       red[(warp * NT + t) * 32 + lane] = make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
@@ -747,7 +829,7 @@ __global__ void __launch_bounds__(DEC_THREADS)
   const int row0 = static_cast<int>(blockIdx.x) / cs * DEC_ROWS;
   float* ysum = reinterpret_cast<float*>(dec_smem + dec_ring_bytes(BITS, NT) - 128);
   for (int i = threadIdx.x; i < p.T * DEC_ROWS; i += DEC_THREADS) ysum[i] = 0.0f;
-  Ring<BITS, BF, GU, NT> r;
+  Ring<BITS, BF, GU, NT, false> r;
   r.init(smem_u32(dec_smem), bars, &abort_flag);
   griddep_wait();
   griddep_launch_dependents();
@@ -785,8 +867,7 @@ __global__ void __launch_bounds__(DEC_THREADS)
       r.drain(it);
     }
   } else {
-    int it = 0;
-    r.zoff = p.dn_zeros - p.dn_scales;
+    typename Ring<BITS, BF, GU, NT, false>::Cursor cur;
     r.gi = p.dn_gi;
     const int ra = warp * 16 + g, rb = ra + 8;
     for (int w = w0; w < w1;) {
@@ -798,9 +879,8 @@ __global__ void __launch_bounds__(DEC_THREADS)
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[t][j] = 0.0f;
-      r.scale_a = p.dn_scales + static_cast<size_t>(sg.row_a + ra) * p.dn_G;
-      r.scale_b = p.dn_scales + static_cast<size_t>(sg.row_a + rb) * p.dn_G;
-      if (!r.consume(sg.c0, sg.c1, sg.tiles, ra * (16 * BITS), rb * (16 * BITS), q, lane, it, acc)) break;
+      r.param = ((q & 1) ? p.dn_zeros : p.dn_scales) + static_cast<size_t>(sg.row_a + ((q & 2) ? rb : ra)) * p.dn_G;
+      if (!r.consume_tiles(sg.tiles, sg.c0, sg.c1, ra * (16 * BITS), rb * (16 * BITS), lane, cur, acc)) break;
       const int begin = p.plan.begin[seg], count = p.plan.count[seg];
 #pragma unroll
       for (int t = 0; t < NT; ++t)
@@ -841,6 +921,8 @@ struct DecodeLaunch {
   bool bf16;
   int unit;      // 32, 64 or 128
   int nt;        // tiles a block holds sums for: 1, 2 or 4
+  int local;     // tokens whose activations the blocks lay out themselves (nt = 1), 0: none
+  int chunks;    // chunks of a block at most (local)
   int cluster;   // blocks that split k
   int device;
   cudaStream_t stream;

@@ -5,25 +5,27 @@
 namespace gptq {
 
 namespace {
-template <bool BF, int GU, int NT>
+template <bool BF, int GU, int NT, bool XL>
 struct Of {
+  static int smem(const DecodeLaunch& l) {
+    return XL ? dec_ring_bytes(PACKED_BITS, 0) + l.local * l.chunks * 256 : dec_ring_bytes(PACKED_BITS, NT);
+  }
+  static constexpr int smem_limit = XL ? dec_ring_bytes(PACKED_BITS, 0) + DEC_LOCAL_BYTES : dec_ring_bytes(PACKED_BITS, NT);
   static cudaError_t linear(const DecodeLaunch& l, const CUtensorMap& codes, const LinearDecodeArgs& a) {
     static std::atomic<uint64_t> done{0};
-    const auto kernel = linear_decode_kernel<PACKED_BITS, BF, GU, NT>;
-    const int smem = dec_ring_bytes(PACKED_BITS, NT);
-    const cudaError_t e = raise_smem_limit(done, l.device, kernel, smem);
+    const auto kernel = linear_decode_kernel<PACKED_BITS, BF, GU, NT, XL>;
+    const cudaError_t e = raise_smem_limit(done, l.device, kernel, smem_limit);
     if (e != cudaSuccess) return e;
     const dim3 grid(static_cast<unsigned>((a.m + DEC_ROWS - 1) / DEC_ROWS * l.cluster));
-    return launch_pdl(kernel, grid, dim3(DEC_THREADS), smem, l.cluster, l.stream, codes, a);
+    return launch_pdl(kernel, grid, dim3(DEC_THREADS), smem(l), l.cluster, l.stream, codes, a);
   }
   static cudaError_t gate_up(const DecodeLaunch& l, const CUtensorMap& codes, const MoeArgs& a, int segments) {
     static std::atomic<uint64_t> done{0};
-    const auto kernel = moe_gate_up_kernel<PACKED_BITS, BF, GU, NT>;
-    const int smem = dec_ring_bytes(PACKED_BITS, NT);
-    const cudaError_t e = raise_smem_limit(done, l.device, kernel, smem);
+    const auto kernel = moe_gate_up_kernel<PACKED_BITS, BF, GU, NT, XL>;
+    const cudaError_t e = raise_smem_limit(done, l.device, kernel, smem_limit);
     if (e != cudaSuccess) return e;
     const dim3 grid(static_cast<unsigned>(a.I / 64 * l.cluster), static_cast<unsigned>(segments));
-    return launch_pdl(kernel, grid, dim3(DEC_THREADS), smem, l.cluster, l.stream, codes, a);
+    return launch_pdl(kernel, grid, dim3(DEC_THREADS), smem(l), l.cluster, l.stream, codes, a);
   }
   static cudaError_t down(const DecodeLaunch& l, const CUtensorMap& codes, const MoeArgs& a) {
     static std::atomic<uint64_t> done{0};
@@ -39,9 +41,10 @@ struct Of {
 
 template <bool BF, int GU, typename F>
 cudaError_t by_tiles(const DecodeLaunch& l, F&& f) {
-  if (l.nt == 1) return f(Of<BF, GU, 1>());
-  if (l.nt == 2) return f(Of<BF, GU, 2>());
-  return f(Of<BF, GU, 4>());
+  if (l.local) return f(Of<BF, GU, 1, true>());
+  if (l.nt == 1) return f(Of<BF, GU, 1, false>());
+  if (l.nt == 2) return f(Of<BF, GU, 2, false>());
+  return f(Of<BF, GU, 4, false>());
 }
 template <bool BF, typename F>
 cudaError_t by_unit(const DecodeLaunch& l, F&& f) {

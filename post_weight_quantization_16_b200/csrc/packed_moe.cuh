@@ -87,6 +87,7 @@ __global__ void __launch_bounds__(ROUTER_WARPS * 32) moe_router_kernel(const Rou
   __shared__ int begins[MOE_MAX_E];
   __shared__ int slots[MOE_MAX_E];
   __shared__ int tiles[MOE_MAX_E];
+  __shared__ int chosen_ids[MOE_MAX_T * MOE_MAX_TOPK];
   griddep_wait();
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
@@ -203,10 +204,12 @@ __global__ void __launch_bounds__(ROUTER_WARPS * 32) moe_router_kernel(const Rou
   if (rank != 0) return;
 
   const int pairs = p.T * p.top_k;
+  for (int i = threadIdx.x; i < pairs; i += ROUTER_WARPS * 32) chosen_ids[i] = __ldcg(p.ids + i);
+  __syncthreads();
   for (int e = warp; e < p.E; e += ROUTER_WARPS) {
     int n = 0;
     for (int i = lane; i < (pairs + 31) / 32 * 32; i += 32)
-      n += __popc(__ballot_sync(0xffffffffu, i < pairs && __ldcg(p.ids + i) == e));
+      n += __popc(__ballot_sync(0xffffffffu, i < pairs && chosen_ids[i] == e));
     if (lane == 0) counts[e] = n;
   }
   __syncthreads();
@@ -248,7 +251,7 @@ __global__ void __launch_bounds__(ROUTER_WARPS * 32) moe_router_kernel(const Rou
     if (n == 0) continue;
     int at = begins[e];
     for (int i = lane; i < (pairs + 31) / 32 * 32; i += 32) {
-      const bool mine = i < pairs && __ldcg(p.ids + i) == e;
+      const bool mine = i < pairs && chosen_ids[i] == e;
       const unsigned m = __ballot_sync(0xffffffffu, mine);
       if (mine) {
         const int o = at + __popc(m & ((1u << lane) - 1u));
