@@ -15,7 +15,8 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libgptq.so")
 OBJ = os.path.join(HERE, "_build")
 SOURCES = ["gptq_api.cu", "packed_api.cu", "packed_decode_b2.cu", "packed_decode_b3.cu", "packed_decode_b4.cu",
-           "packed_decode_b8.cu", "packed_tc_b2.cu", "packed_tc_b3.cu", "packed_tc_b4.cu", "packed_tc_b8.cu"]
+           "packed_decode_b8.cu", "packed_tc_b2.cu", "packed_tc_b3.cu", "packed_tc_b4.cu", "packed_tc_b8.cu",
+           "packed_pair_b2.cu", "packed_pair_b3.cu", "packed_pair_b4.cu", "packed_pair_b8.cu"]
 NVCC_FLAGS = ["-std=c++17", "-O3", "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo",
               "-Xcompiler", "-fPIC"]
 

@@ -7,6 +7,7 @@
 #include "packed_decode.cuh"
 #include "packed_grad.cuh"
 #include "packed_moe.cuh"
+#include "packed_pair.cuh"
 #include "packed_tc.cuh"
 
 using namespace gptq;
@@ -74,6 +75,8 @@ int k_split(int64_t tiles, int chunks) {
 
 // Tokens up to which the warp-level kernel runs; beyond, tcgen05.
 constexpr int kDecodeTokens = 16;
+// Tokens up to which one block's 128-row tile runs; beyond, CTA pairs with 256-token tiles.
+constexpr int kSingleTokens = 128;
 
 // Tokens that the decode kernels lay out themselves, chunk range by chunk range, instead of a launch
 // of its own before them: every block of 128 rows repeats the layout, which is cheap for plain
@@ -142,16 +145,27 @@ gptq_status linear_many_tokens(const gptq_linear_args& a, const uint16_t* X, int
   d.status = static_cast<int*>(a.workspace);
   CUtensorMap cmap, xmap;
   gptq_status s = encode_codes(&cmap, a.W, TC_BM);
-  if (s == GPTQ_OK) s = encode_act(&xmap, a.dtype, X, n, T, ldx, d.tn);
+  if (s == GPTQ_OK) s = encode_act(&xmap, a.dtype, X, n, T, ldx, std::min(d.tn, 128));
   if (s != GPTQ_OK) return s;
   TcLaunch l;
   l.bf16 = a.dtype == GPTQ_BF16;
   l.unit = std::min(g, 128);
+  l.sms = kSms;
+  l.device = device;
+  l.stream = st;
+  if (T > kSingleTokens) {
+    PairArgs p = {};
+    p.tiles_m = (m + 255) / 256;
+    p.tiles_t = (T + PR_TN - 1) / PR_TN;
+    p.chunks = p.steps = d.chunks;
+    p.lin = d;
+    CK(by_bits(a.W.qp.bits,
+               [&](auto b) { return launch_packed_pair<decltype(b)::value>(l, false, cmap, xmap, xmap, p); }));
+    return GPTQ_OK;
+  }
   const int64_t tiles = static_cast<int64_t>((m + TC_BM - 1) / TC_BM) * ((T + d.tn - 1) / d.tn);
   l.cluster = 1;
   while (l.cluster < 8 && tiles * l.cluster * 2 <= kSms && d.chunks >= 4 * l.cluster) l.cluster *= 2;
-  l.device = device;
-  l.stream = st;
   CK(by_bits(a.W.qp.bits, [&](auto b) { return launch_linear_tc<decltype(b)::value>(l, cmap, xmap, d); }));
   return GPTQ_OK;
 }
@@ -378,18 +392,42 @@ extern "C" gptq_status gptq_dequant_linear_backward(const gptq_linear_grad_args*
   d.status = reinterpret_cast<int*>(ws);
   CUtensorMap cmap, hmap, lmap;
   gptq_status s = encode_codes(&cmap, a.W, TC_BM);
-  if (s == GPTQ_OK) s = encode_act(&hmap, GPTQ_FP16, hi, m, T, ldz, d.tn);
-  if (s == GPTQ_OK) s = encode_act(&lmap, GPTQ_FP16, lo, m, T, ldz, d.tn);
+  const bool pair = T > kSingleTokens;
+  if (s == GPTQ_OK) s = encode_act(&hmap, GPTQ_FP16, hi, m, T, ldz, pair ? 128 : d.tn);
+  if (s == GPTQ_OK) s = encode_act(&lmap, GPTQ_FP16, lo, m, T, ldz, pair ? 128 : d.tn);
   if (s != GPTQ_OK) return s;
   TcLaunch l;
   l.bf16 = bf;
   l.unit = std::min(g, 128);
-  const int64_t tiles = static_cast<int64_t>(n / 128) * ((T + d.tn - 1) / d.tn);
-  l.cluster = 1;
-  while (l.cluster < 8 && tiles * l.cluster * 2 <= kSms && d.row_chunks >= 4 * l.cluster) l.cluster *= 2;
+  l.sms = kSms;
   l.device = device;
   l.stream = st;
-  CK(by_bits(a.W.qp.bits, [&](auto b) { return launch_linear_bwd_tc<decltype(b)::value>(l, cmap, hmap, lmap, d); }));
+  if (pair) {
+    PairArgs p = {};
+    p.tiles_m = (n + 255) / 256;
+    p.tiles_t = (T + PR_TN - 1) / PR_TN;
+    p.chunks = d.row_chunks;
+    p.steps = d.parts * d.row_chunks;
+    p.lin.T = T;
+    p.lin.m = m;
+    p.lin.G = d.G;
+    p.lin.gi = d.gi;
+    p.lin.scales = d.scales;
+    p.lin.zeros = d.zeros;
+    p.lin.status = d.status;
+    p.token_scale = d.token_scale;
+    p.dX = d.dX;
+    p.lddx = d.lddx;
+    p.n = n;
+    p.dx_vec = d.vec;
+    CK(by_bits(a.W.qp.bits,
+               [&](auto b) { return launch_packed_pair<decltype(b)::value>(l, true, cmap, hmap, lmap, p); }));
+  } else {
+    const int64_t tiles = static_cast<int64_t>(n / 128) * ((T + d.tn - 1) / d.tn);
+    l.cluster = 1;
+    while (l.cluster < 8 && tiles * l.cluster * 2 <= kSms && d.row_chunks >= 4 * l.cluster) l.cluster *= 2;
+    CK(by_bits(a.W.qp.bits, [&](auto b) { return launch_linear_bwd_tc<decltype(b)::value>(l, cmap, hmap, lmap, d); }));
+  }
   if (a.W.perm) {
     static std::atomic<uint64_t> done{0};
     CK(raise_smem_limit(done, device, unpermute_kernel, static_cast<int>(kPackedMaxN) * 2));

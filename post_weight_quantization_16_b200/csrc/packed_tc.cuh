@@ -31,7 +31,7 @@ constexpr int TC_THREADS = 18 * 32;
 constexpr int TC_SMEM_BUDGET = 224 * 1024;
 constexpr int TC_MAX_TN = 128;
 
-__host__ __device__ inline int tc_code_bytes(int bits) { return TC_BM * TC_BK * bits / 8; }
+__host__ __device__ constexpr int tc_code_bytes(int bits) { return TC_BM * TC_BK * bits / 8; }
 __host__ __device__ inline int tc_stage_bytes(int tn, int bits) { return tc_code_bytes(bits) + tn * 256; }
 __host__ __device__ inline int tc_stages(int tn, int bits) {
   const int s = (TC_SMEM_BUDGET - 2048 - TC_NA * TC_A_BYTES) / tc_stage_bytes(tn, bits);
@@ -690,6 +690,7 @@ __global__ void __launch_bounds__(BW_THREADS, 1)
 struct TcLaunch {
   bool bf16;
   int unit;     // 32, 64 or 128
+  int sms;
   int cluster;  // blocks that split k
   int device;
   cudaStream_t stream;
