@@ -268,10 +268,13 @@ extern "C" gptq_status gptq_dequant_linear(const gptq_linear_args* args, int dev
   int64_t ldx = a.ld_x;
   if (T > kDecodeTokens) {
     if (a.W.perm) {
+      static std::atomic<uint64_t> done{0};
+      CK(raise_smem_limit(done, device, gather_x_kernel, static_cast<int>(kPackedMaxN) * 2));
       uint16_t* xs = reinterpret_cast<uint16_t*>(ws + 256);
-      for (int t0 = 0; t0 < T; t0 += 65535)
-        CK(launch_pdl(gather_x_kernel, dim3((n + 1023) / 1024, std::min(65535, T - t0)), dim3(256), 0, 1, st,
-                      X + static_cast<size_t>(t0) * ldx, ldx, n, a.W.perm, xs + static_cast<size_t>(t0) * n));
+      // rows of a block: as many as 64 KB hold, while the blocks still fill the GPU
+      const int rows = std::max(1, std::min(32768 / n, T / (4 * kSms)));
+      CK(launch_pdl(gather_x_kernel, dim3((T + rows - 1) / rows), dim3(512), static_cast<size_t>(rows) * n * 2, 1, st, X,
+                    ldx, T, n, a.W.perm, rows, xs));
       X = xs;
       ldx = n;
     }
@@ -353,9 +356,10 @@ extern "C" gptq_status gptq_dequant_linear_backward(const gptq_linear_grad_args*
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   const uint16_t* dY = static_cast<const uint16_t*>(a.dY);
   const uint16_t* Z = a.act == GPTQ_ACT_NONE ? nullptr : static_cast<const uint16_t*>(a.preact);
+  const int vec4 = a.ld_dy % 4 == 0 && aligned_to(dY, 8) && (!Z || (m % 4 == 0 && aligned_to(Z, 8)));
   if (a.dbias)
-    CK(launch_pdl(bf ? dbias_kernel<true> : dbias_kernel<false>, dim3((m + 127) / 128 * DBIAS_CLUSTER), dim3(256), 0,
-                  DBIAS_CLUSTER, st, dY, a.ld_dy, Z, T, m, a.act, a.dbias));
+    CK(launch_pdl(bf ? dbias_kernel<true> : dbias_kernel<false>, dim3((m + 127) / 128 * DBIAS_CLUSTER),
+                  dim3(DBIAS_WARPS * 32), 0, DBIAS_CLUSTER, st, dY, a.ld_dy, Z, T, m, a.act, vec4, a.dbias));
   if (!a.dX) return GPTQ_OK;
   // dY is the operand itself when it is fp16, nothing is to be multiplied and TMA can read it
   const bool direct = aligned16(dY) && a.ld_dy % 8 == 0;
@@ -366,8 +370,8 @@ extern "C" gptq_status gptq_dequant_linear_backward(const gptq_linear_grad_args*
     uint16_t* h = reinterpret_cast<uint16_t*>(ws + lay.hi);
     uint16_t* o = lay.parts == 2 ? reinterpret_cast<uint16_t*>(ws + lay.lo) : nullptr;
     ldz = lay.ldz;
-    CK(launch_pdl(bf ? act_grad_kernel<true> : act_grad_kernel<false>, dim3(T), dim3(256), 0, 1, st, dY, a.ld_dy, Z, m,
-                  a.act, h, o, ldz, reinterpret_cast<float*>(ws + lay.scale)));
+    CK(launch_pdl(bf ? act_grad_kernel<true> : act_grad_kernel<false>, dim3(T), dim3(512), 0, 1, st, dY, a.ld_dy, Z, m,
+                  a.act, vec4, h, o, ldz, reinterpret_cast<float*>(ws + lay.scale)));
     hi = h;
     lo = o ? o : h;
   }

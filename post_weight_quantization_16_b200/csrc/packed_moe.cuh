@@ -7,17 +7,29 @@
 
 namespace gptq {
 
-// out[t][k] = X[t][perm[k]] in rows of n.  Grid (n / 1024 rounded up, tokens); four columns a thread.
-__global__ void __launch_bounds__(256) gather_x_kernel(const uint16_t* __restrict__ X, int64_t ldx, int n,
-                                                       const int32_t* __restrict__ perm, uint16_t* __restrict__ out) {
+// out[t][k] = X[t][perm[k]] in rows of n.  A block takes GATHER_ROWS tokens; each row passes through
+// shared memory, so that global reads and writes are whole lines and the order is read once a block.
+// Grid (tokens / GATHER_ROWS rounded up), dynamic shared memory GATHER_ROWS * n * 2 bytes.
+__global__ void __launch_bounds__(512) gather_x_kernel(const uint16_t* __restrict__ X, int64_t ldx, int T, int n,
+                                                       const int32_t* __restrict__ perm, int rows,
+                                                       uint16_t* __restrict__ out) {
+  extern __shared__ __align__(16) uint16_t gather_rows[];
   griddep_wait();
   griddep_launch_dependents();
-  const int k = (blockIdx.x * 256 + threadIdx.x) * 4;
-  if (k >= n) return;
-  const uint16_t* src = X + static_cast<size_t>(blockIdx.y) * ldx;
-  const int4 i = *reinterpret_cast<const int4*>(perm + k);
-  const ushort4 v = make_ushort4(src[i.x], src[i.y], src[i.z], src[i.w]);
-  *reinterpret_cast<ushort4*>(out + static_cast<size_t>(blockIdx.y) * n + k) = v;
+  const int t0 = blockIdx.x * rows, cnt = min(rows, T - t0);
+  for (int r = 0; r < cnt; ++r) {
+    const uint4* src = reinterpret_cast<const uint4*>(X + static_cast<size_t>(t0 + r) * ldx);
+    for (int k = threadIdx.x; k < n / 8; k += 512) reinterpret_cast<uint4*>(gather_rows + r * n)[k] = src[k];
+  }
+  __syncthreads();
+  for (int k = threadIdx.x * 4; k < n; k += 2048) {
+    const int4 i = *reinterpret_cast<const int4*>(perm + k);
+    for (int r = 0; r < cnt; ++r) {
+      const uint16_t* row = gather_rows + r * n;
+      *reinterpret_cast<ushort4*>(out + static_cast<size_t>(t0 + r) * n + k) =
+          make_ushort4(row[i.x], row[i.y], row[i.z], row[i.w]);
+    }
+  }
 }
 
 // Few tokens in fragment order, [chunk][tiles][FRAG_BYTES], for units of gu columns.  Grid (chunks,

@@ -11,8 +11,12 @@
 //                 the even block's barrier)
 //   warp 3        codes by TMA (each block its own)
 //   warp 1        tensor-memory allocation; in the even block MMA issue for the pair
-//   warps 4-7     unpack, one thread per weight row
-//   warps 8-15    drain and epilogue: lane = tensor-memory lane, each warp 128 of the 256 tokens
+//   warps 4-11    unpack: two groups of four warps, each its half of every chunk
+//   warps 12-19   drain and epilogue: lane = tensor-memory lane, each warp 128 of the 256 tokens
+// Operands move in steps of 64 along k.  Handing a step from the MMA back to the unpack warps and
+// forward again takes about 2700 cycles (measured with empty unpack warps), against the 512 cycles
+// of its MMAs: six steps of each operand are in flight (with two 128-wide ones the 70B-shaped layer
+// took 3.7 ms).
 // Tensor memory holds two accumulators of 256 columns.  Forward: they alternate by group unit, and
 // the sums live in the drain warps' registers (128 each, hence the register split), whose epilogue
 // overlaps the producers' next tile.  Gradient: they alternate by tile, so that a tile's epilogue
@@ -23,20 +27,21 @@
 
 namespace gptq {
 
-constexpr int PR_THREADS = 512;
+constexpr int PR_THREADS = 640;
 constexpr int PR_TN = 256;                     // tokens of a tile
-constexpr int PR_NA = 2;                       // unpacked operand tiles in flight
-constexpr int PR_SX = 3;                       // activation stages
-constexpr int PR_X_BYTES = 128 * 256;          // a block's half of a stage: 128 tokens x 128 values
+constexpr int PR_A_BYTES = 128 * 128;          // an unpacked step: 128 x 64 values
+constexpr int PR_X_BYTES = 128 * 128;          // a block's half of a step's activations: 128 tokens x 64 values
 constexpr int PR_EPI_BYTES = 8 * 2048;         // per drain warp: 16 tokens x 32 rows of sums
-// Register split (setmaxnreg): 128 * (40 + 96 + 184 + 184) = 64512 of the 65536 that 512 threads of 128 start with.
-constexpr int PR_REGS_MISC = 40, PR_REGS_UNPACK = 96, PR_REGS_DRAIN = 184;
-static_assert(PR_REGS_MISC + PR_REGS_UNPACK + 2 * PR_REGS_DRAIN <= 4 * 128, "register split");
+// Register split (setmaxnreg): 128 * (32 + 2 * 56 + 2 * 168) = 61440, what 640 threads of 96 start with.
+constexpr int PR_REGS_MISC = 32, PR_REGS_UNPACK = 56, PR_REGS_DRAIN = 168;
+static_assert(PR_REGS_MISC + 2 * PR_REGS_UNPACK + 2 * PR_REGS_DRAIN <= 5 * 96, "register split");
 
-__host__ __device__ constexpr int pr_code_stages(int bits) { return bits == 8 ? 2 : 4; }
+__host__ __device__ constexpr int pr_steps(int bits) { return bits == 8 ? 4 : 6; }  // steps in flight (even)
+constexpr int PR_SC = 2;                                                         // code chunks in flight
 __host__ __device__ constexpr int pr_smem_bytes(int bits) {
-  return 1024 + PR_NA * TC_A_BYTES + PR_SX * PR_X_BYTES + pr_code_stages(bits) * tc_code_bytes(bits) + PR_EPI_BYTES + 512;
+  return 1024 + pr_steps(bits) * (PR_A_BYTES + PR_X_BYTES) + PR_SC * tc_code_bytes(bits) + PR_EPI_BYTES + 512;
 }
+static_assert(pr_smem_bytes(4) <= 227 * 1024 && pr_smem_bytes(8) <= 227 * 1024, "shared memory");
 
 struct PairArgs {
   int tiles_m, tiles_t;  // tiles of 256 rows (forward) or columns (gradient), and of 256 tokens
@@ -55,6 +60,11 @@ __device__ __forceinline__ void regs_dec() {
 template <int REGS>
 __device__ __forceinline__ void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+// Arrival on a barrier of the pair's even block.  (A release at cluster scope would also wait for the
+// warp's loads of the next step's parameters: with it the gradient's kernel ran 590 us, not 430.)
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 // Waits of a whole warp on a barrier that the peer block arrives on too.
 __device__ __forceinline__ bool warp_wait_cl(uint32_t bar, uint32_t parity, volatile int* abort_flag, int lane) {
@@ -81,16 +91,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PR_THREADS, 1)
     packed_pair_kernel(const __grid_constant__ CUtensorMap codes_map, const __grid_constant__ CUtensorMap x_map,
                        const __grid_constant__ CUtensorMap xlo_map, const PairArgs p) {
   constexpr int UNITS = 128 / GU;
-  constexpr int SC = pr_code_stages(BITS), CODES = tc_code_bytes(BITS);
+  constexpr int SC = PR_SC, NS = pr_steps(BITS), CODES = tc_code_bytes(BITS);
   extern __shared__ uint8_t pr_smem_raw[];
   const uint32_t raw_s = smem_u32(pr_smem_raw);
   uint8_t* smem = pr_smem_raw + (((raw_s + 1023u) & ~1023u) - raw_s);
   const uint32_t sbase = smem_u32(smem);
-  const uint32_t a_base = sbase, x_base = a_base + PR_NA * TC_A_BYTES, c_base = x_base + PR_SX * PR_X_BYTES,
+  const uint32_t a_base = sbase, x_base = a_base + NS * PR_A_BYTES, c_base = x_base + NS * PR_X_BYTES,
                  e_base = c_base + SC * CODES;
-  const uint32_t bar_xfull = e_base + PR_EPI_BYTES, bar_xempty = bar_xfull + 8 * PR_SX, bar_cfull = bar_xempty + 8 * PR_SX,
-                 bar_cempty = bar_cfull + 8 * SC, bar_afull = bar_cempty + 8 * SC, bar_aempty = bar_afull + 8 * PR_NA,
-                 bar_tfull = bar_aempty + 8 * PR_NA, bar_tempty = bar_tfull + 16, bar_drain = bar_tempty + 16;
+  const uint32_t bar_full = e_base + PR_EPI_BYTES, bar_empty = bar_full + 8 * NS, bar_cfull = bar_empty + 8 * NS,
+                 bar_cempty = bar_cfull + 8 * SC, bar_tfull = bar_cempty + 8 * SC, bar_tempty = bar_tfull + 16,
+                 bar_drain = bar_tempty + 16;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + (bar_drain + 8 - sbase));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -101,17 +111,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PR_THREADS, 1)
   const int ntiles = p.tiles_m * p.tiles_t;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < PR_SX; ++s) {
-      mbar_init(bar_xfull + 8 * s, 1);  // even block: one expect_tx arrival, the pair's bytes
-      mbar_init(bar_xempty + 8 * s, 1);
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(bar_full + 8 * s, 9);  // even block: the pair's activations (one arrival and their bytes) and
+      mbar_init(bar_empty + 8 * s, 1);  // a group of unpack warps of each block
     }
     for (int s = 0; s < SC; ++s) {
       mbar_init(bar_cfull + 8 * s, 1);
-      mbar_init(bar_cempty + 8 * s, 4);
-    }
-    for (int j = 0; j < PR_NA; ++j) {
-      mbar_init(bar_afull + 8 * j, 8);  // even block: the unpack warps of both
-      mbar_init(bar_aempty + 8 * j, 1);
+      mbar_init(bar_cempty + 8 * s, 8);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(bar_tfull + 8 * b, 1);
@@ -142,23 +148,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PR_THREADS, 1)
     regs_dec<PR_REGS_MISC>();
     if (warp == 0 && lane == 0) {
       // ---------------- activations ----------------
-      const uint32_t lead_full = mapa_shared(bar_xfull, 0);
-      RingPos<PR_SX> r;
+      const uint32_t lead_full = mapa_shared(bar_full, 0);
+      RingPos<NS> r;
       int issued = 0;
       bool ok = true;
       for (int tile = cluster; tile < ntiles && ok; tile += clusters) {
         const int t0 = tile / p.tiles_m * PR_TN + 128 * static_cast<int>(rank);
-        for (int i = 0; i < p.steps; ++i) {
-          if (!mbar_wait_bounded_cl(bar_xempty + 8 * r.s, r.ph ^ 1u, abort_flag)) {
+        for (int i = 0; i < 2 * p.steps; ++i) {
+          if (!mbar_wait_bounded_cl(bar_empty + 8 * r.s, r.ph ^ 1u, abort_flag)) {
             ok = false;
             break;
           }
-          if (leader) mbar_arrive_expect_tx(bar_xfull + 8 * r.s, 2 * PR_X_BYTES);
-          const uint32_t fb = lead_full + 8 * r.s, st = x_base + r.s * PR_X_BYTES;
-          const CUtensorMap* map = (BWD && i >= p.chunks) ? &xlo_map : &x_map;
-          const int k = ((BWD && i >= p.chunks) ? i - p.chunks : i) * 128;
-          tma_load_2d_pair(st, map, fb, k, t0);
-          tma_load_2d_pair(st + PR_X_BYTES / 2, map, fb, k + 64, t0);
+          if (leader) mbar_arrive_expect_tx(bar_full + 8 * r.s, 2 * PR_X_BYTES);
+          const bool low = BWD && i >= 2 * p.chunks;
+          tma_load_2d_pair(x_base + r.s * PR_X_BYTES, low ? &xlo_map : &x_map, lead_full + 8 * r.s,
+                           (low ? i - 2 * p.chunks : i) * 64, t0);
           r.next();
           ++issued;
         }
@@ -166,8 +170,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PR_THREADS, 1)
       // no copy of the pair may be in flight when either block leaves (the odd block is held by the
       // closing cluster barrier until the even one has seen its last stages complete)
       if (leader)
-        for (int i = max(0, issued - PR_SX); i < issued; ++i)
-          mbar_wait_drain(bar_xfull + 8 * (i % PR_SX), static_cast<uint32_t>(i / PR_SX) & 1u);
+        for (int i = max(0, issued - NS); i < issued; ++i)
+          mbar_wait_drain(bar_full + 8 * (i % NS), static_cast<uint32_t>(i / NS) & 1u);
     } else if (warp == 3 && lane == 0) {
       // ---------------- codes ----------------
       RingPos<SC> r;
@@ -194,49 +198,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PR_THREADS, 1)
       // ---------------- MMA for the pair ----------------
       const uint32_t fmt = (BF && !BWD) ? 1u : 0u;
       const uint32_t idesc = idesc_make(fmt, fmt, BWD ? 1u : 0u, 0u, 256, PR_TN);
-      RingPos<PR_SX> x;
-      RingPos<PR_NA> a;
+      RingPos<NS> x;
       RingPos<2> t;
       bool ok = true;
       for (int tile = cluster; tile < ntiles && ok; tile += clusters) {
-        for (int i = 0; i < p.steps && ok; ++i) {
-          if (!mbar_wait_bounded_cl(bar_xfull + 8 * x.s, x.ph, abort_flag) ||
-              !mbar_wait_bounded_cl(bar_afull + 8 * a.s, a.ph, abort_flag)) {
+        for (int i = 0; i < 2 * p.steps && ok; ++i) {
+          if (!mbar_wait_bounded_cl(bar_full + 8 * x.s, x.ph, abort_flag)) {
             ok = false;
             break;
           }
-          const uint32_t a_t = a_base + a.s * TC_A_BYTES, x_t = x_base + x.s * PR_X_BYTES;
+          const uint32_t a_t = a_base + x.s * PR_A_BYTES, x_t = x_base + x.s * PR_X_BYTES;
+          constexpr int SUB = (!BWD && GU == 32) ? 2 : 1;  // accumulation units of a step
 #pragma unroll
-          for (int u = 0; u < (BWD ? 1 : UNITS); ++u) {
-            if (!BWD || i == 0) {
-              if (!mbar_wait_bounded_cl(bar_tempty + 8 * t.s, t.ph ^ 1u, abort_flag)) {
-                ok = false;
-                break;
-              }
+          for (int u = 0; u < SUB; ++u) {
+            // a unit starts with this step's MMAs (u = 0), and ends with them
+            const bool first = BWD ? i == 0 : (GU < 128 || (i & 1) == 0);
+            const bool last = BWD ? i == 2 * p.steps - 1 : (GU < 128 || (i & 1) == 1);
+            if (first && !mbar_wait_bounded_cl(bar_tempty + 8 * t.s, t.ph ^ 1u, abort_flag)) {
+              ok = false;
+              break;
             }
             tc_fence_after();
             const uint32_t d = tmem_base + static_cast<uint32_t>(t.s * PR_TN);
-            constexpr int STEPS16 = BWD ? 8 : GU / 16;
 #pragma unroll
-            for (int k = 0; k < STEPS16; ++k) {
-              const int kk = u * STEPS16 + k;
-              // forward: K-major, atoms of 64 columns; gradient: MN-major, 16 rows = two 8-row atoms
-              const uint64_t ad = BWD ? sdesc_sw128(a_t + kk * 2048, TC_ATOM, 1024)
-                                      : sdesc_sw128(a_t + (kk >> 2) * TC_ATOM + (kk & 3) * 32, 16, 1024);
-              const uint64_t bd = sdesc_sw128(x_t + (kk >> 2) * (PR_X_BYTES / 2) + (kk & 3) * 32, 16, 1024);
-              umma_f16_pair(d, ad, bd, idesc, (BWD ? (i > 0 || k > 0) : k > 0) ? 1u : 0u);
+            for (int k = 0; k < 4 / SUB; ++k) {
+              const int kk = u * (4 / SUB) + k;
+              // forward: K-major; gradient: MN-major, 16 rows = two 8-row atoms, 64-column halves 8 KB apart
+              const uint64_t ad = BWD ? sdesc_sw128(a_t + kk * 2048, PR_A_BYTES / 2, 1024)
+                                      : sdesc_sw128(a_t + kk * 32, 16, 1024);
+              umma_f16_pair(d, ad, sdesc_sw128(x_t + kk * 32, 16, 1024), idesc, (first && k == 0) ? 0u : 1u);
             }
-            if (BWD || u == UNITS - 1) {
-              umma_commit_pair_mc(bar_xempty + 8 * x.s, 0x3);
-              umma_commit_pair_mc(bar_aempty + 8 * a.s, 0x3);
-            }
-            if (!BWD || i == p.steps - 1) {
+            if (u == SUB - 1) umma_commit_pair_mc(bar_empty + 8 * x.s, 0x3);
+            if (last) {
               umma_commit_pair_mc(bar_tfull + 8 * t.s, 0x3);
               t.next();
             }
           }
           x.next();
-          a.next();
         }
       }
       if (!ok) {  // MMAs may still be running: wait for them before tensor memory is released
@@ -244,82 +242,89 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PR_THREADS, 1)
         mbar_wait_drain(bar_drain, 0);
       }
     }
-  } else if (warp < 8) {
-    // ---------------- unpack: one thread per row of the tile ----------------
+  } else if (warp < 12) {
+    // ---------------- unpack ----------------
+    // Forward: group 0 takes columns 0-63 of every chunk, group 1 columns 64-127, a thread one row.
+    // Gradient: group 0 takes rows 0-63 of every chunk, group 1 rows 64-127, two threads per row.
     regs_dec<PR_REGS_UNPACK>();
-    const int r = threadIdx.x - 128, r7 = r & 7;
-    const uint32_t lead_afull = mapa_shared(bar_afull, 0);
+    const int d = threadIdx.x & 127, grp = (warp - 4) >> 2;
+    const int r = BWD ? grp * 64 + (d >> 1) : d, h = BWD ? d & 1 : grp, r7 = r & 7;
+    const uint32_t lead_full = mapa_shared(bar_full, 0);
+    const uint32_t dst0 = a_base + (BWD ? h * (PR_A_BYTES / 2) + (r & 63) * 128 : r * 128);
+    constexpr int ZN = GU == 32 ? 2 : 1;  // groups of a half row
     RingPos<SC> c;
-    RingPos<PR_NA> a;
+    int as = grp;  // slot of this group's next step
+    uint32_t aph = 0;
     bool ok = true;
     for (int tile = cluster; tile < ntiles && ok; tile += clusters) {
       const int mt = tile % p.tiles_m * 2 + static_cast<int>(rank);
       // row of W and its groups: forward row mt * 128 + r in chunk i; gradient row i * 128 + r in chunk mt
-      float ns[UNITS], nz[UNITS];
+      float ns[ZN], nz[ZN];
       auto load_sz = [&](int i) {
         const int gr = (BWD ? i : mt) * 128 + r;
         const bool in = gr < p.lin.m;
         const size_t row = static_cast<size_t>(min(gr, p.lin.m - 1)) * p.lin.G;
         const int kc = BWD ? min(mt, p.n / 128 - 1) : i;
 #pragma unroll
-        for (int u = 0; u < UNITS; ++u) {
-          const size_t at = row + group_of<GU>(p.lin.gi, kc, u);
-          nz[u] = in ? __ldg(p.lin.zeros + at) : 0.0f;
-          if (BWD) ns[u] = in ? __ldg(p.lin.scales + at) : 0.0f;  // rows past m: zero weights
+        for (int j = 0; j < ZN; ++j) {
+          const size_t at = row + group_of<GU>(p.lin.gi, kc, GU == 128 ? 0 : GU == 64 ? h : 2 * h + j);
+          nz[j] = in ? __ldg(p.lin.zeros + at) : 0.0f;
+          if (BWD) ns[j] = in ? __ldg(p.lin.scales + at) : 0.0f;  // rows past m: zero weights
         }
       };
       load_sz(0);
       for (int i = 0; i < p.steps; ++i) {
-        float cs[UNITS], cz[UNITS];
+        float cs[ZN], cz[ZN];
 #pragma unroll
-        for (int u = 0; u < UNITS; ++u) {
-          cz[u] = nz[u];
-          cs[u] = BWD ? ns[u] : 0.0f;
+        for (int j = 0; j < ZN; ++j) {
+          cz[j] = nz[j];
+          cs[j] = BWD ? ns[j] : 0.0f;
         }
         if (i + 1 < p.steps) load_sz((BWD && i + 1 >= p.chunks) ? i + 1 - p.chunks : i + 1);
         if (!warp_wait(bar_cfull + 8 * c.s, c.ph, abort_flag, lane) ||
-            !warp_wait_cl(bar_aempty + 8 * a.s, a.ph ^ 1u, abort_flag, lane)) {
+            !warp_wait_cl(bar_empty + 8 * as, aph ^ 1u, abort_flag, lane)) {
           ok = false;
           break;
         }
+        uint32_t w[2 * BITS];
+        load_half_row<BITS>(smem + (c_base - sbase) + c.s * CODES, r, h, w);
+        const uint32_t dst = dst0 + as * PR_A_BYTES;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t w[2 * BITS];
-          load_half_row<BITS>(smem + (c_base - sbase) + c.s * CODES, r, h, w);
-          const uint32_t dst = a_base + a.s * TC_A_BYTES + h * TC_ATOM + r * 128;
-#pragma unroll
-          for (int b = 0; b < 8; ++b) {
-            const int u = GU == 128 ? 0 : GU == 64 ? h : 2 * h + (b >> 2);
-            uint32_t v, v1, q[4];
-            half_row_block<BITS>(w, b, v, v1);
-            if (BWD) {
-              dequant8<BITS>(v, v1, make_float2(-8388608.0f - cz[u], -8388608.0f - cz[u]), make_float2(cs[u], cs[u]), q);
-              st_shared_v4(dst + ((b ^ r7) << 4), q[0], q[1], q[2], q[3]);
-            } else {
-              unpack8<BITS, BF>(v, v1, zero_term<BITS, BF>(cz[u]), q);
-              // pairs (i, i + 4) -> columns in order
-              st_shared_v4(dst + ((b ^ r7) << 4), __byte_perm(q[0], q[1], 0x5410), __byte_perm(q[2], q[3], 0x5410),
-                           __byte_perm(q[0], q[1], 0x7632), __byte_perm(q[2], q[3], 0x7632));
-            }
+        for (int b = 0; b < 8; ++b) {
+          const int j = GU == 32 ? b >> 2 : 0;
+          uint32_t v, v1, q[4];
+          half_row_block<BITS>(w, b, v, v1);
+          if (BWD) {
+            dequant8<BITS>(v, v1, make_float2(-8388608.0f - cz[j], -8388608.0f - cz[j]), make_float2(cs[j], cs[j]), q);
+            st_shared_v4(dst + ((b ^ r7) << 4), q[0], q[1], q[2], q[3]);
+          } else {
+            unpack8<BITS, BF>(v, v1, zero_term<BITS, BF>(cz[j]), q);
+            // pairs (i, i + 4) -> columns in order
+            st_shared_v4(dst + ((b ^ r7) << 4), __byte_perm(q[0], q[1], 0x5410), __byte_perm(q[2], q[3], 0x5410),
+                         __byte_perm(q[0], q[1], 0x7632), __byte_perm(q[2], q[3], 0x7632));
           }
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(bar_cempty + 8 * c.s);
-          mbar_arrive_cluster(lead_afull + 8 * a.s);
+          mbar_arrive_remote(lead_full + 8 * as);
         }
         c.next();
-        a.next();
+        as += 2;
+        if (as >= NS) {
+          as = grp;
+          aph ^= 1u;
+        }
       }
     }
   } else {
     // ---------------- drain and epilogue ----------------
     regs_inc<PR_REGS_DRAIN>();
-    const int qd = warp & 3, half = (warp - 8) >> 2;
+    const int qd = warp & 3, half = (warp - 12) >> 2;
     const uint32_t lead_tempty = mapa_shared(bar_tempty, 0);
     const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(qd * 32) << 16) + static_cast<uint32_t>(half * 128);
-    float* stage = reinterpret_cast<float*>(smem + (e_base - sbase)) + (warp - 8) * 512;  // [16 tokens][32 rows]
+    float* stage = reinterpret_cast<float*>(smem + (e_base - sbase)) + (warp - 12) * 512;  // [16 tokens][32 rows]
     RingPos<2> t;
     bool ok = true;
     for (int tile = cluster; tile < ntiles && ok; tile += clusters) {
@@ -370,7 +375,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PR_THREADS, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(lead_tempty + 8 * t.s);
+        if (lane == 0) mbar_arrive_remote(lead_tempty + 8 * t.s);
         t.next();
       } else {
         float acc[128];
@@ -387,18 +392,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PR_THREADS, 1)
           }
           tc_fence_after();
           const uint32_t at = lane_base + static_cast<uint32_t>(t.s * PR_TN);
-          uint32_t v[2][16];
-          tmem_ld_32x32b_x16(at, v[0]);
 #pragma unroll
           for (int cc = 0; cc < 8; ++cc) {
+            uint32_t v[16];
+            tmem_ld_32x32b_x16(at + cc * 16, v);
             tmem_ld_wait();
-            if (cc + 1 < 8) tmem_ld_32x32b_x16(at + (cc + 1) * 16, v[(cc + 1) & 1]);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) acc[cc * 16 + j] = fmaf(sc, __uint_as_float(v[cc & 1][j]), acc[cc * 16 + j]);
+            for (int j = 0; j < 16; ++j) acc[cc * 16 + j] = fmaf(sc, __uint_as_float(v[j]), acc[cc * 16 + j]);
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(lead_tempty + 8 * t.s);
+          if (lane == 0) mbar_arrive_remote(lead_tempty + 8 * t.s);
           t.next();
         }
         if (ok) {
