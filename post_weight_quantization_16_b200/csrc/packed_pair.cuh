@@ -31,15 +31,15 @@ constexpr int PR_THREADS = 640;
 constexpr int PR_TN = 256;                     // tokens of a tile
 constexpr int PR_A_BYTES = 128 * 128;          // an unpacked step: 128 x 64 values
 constexpr int PR_X_BYTES = 128 * 128;          // a block's half of a step's activations: 128 tokens x 64 values
-constexpr int PR_EPI_BYTES = 8 * 2048;         // per drain warp: 16 tokens x 32 rows of sums
+constexpr int PR_EPI_BYTES = 8 * 1024;         // per drain warp: 8 tokens x 32 rows of sums
 // Register split (setmaxnreg): 128 * (32 + 2 * 56 + 2 * 168) = 61440, what 640 threads of 96 start with.
 constexpr int PR_REGS_MISC = 32, PR_REGS_UNPACK = 56, PR_REGS_DRAIN = 168;
 static_assert(PR_REGS_MISC + 2 * PR_REGS_UNPACK + 2 * PR_REGS_DRAIN <= 5 * 96, "register split");
 
 __host__ __device__ constexpr int pr_steps(int bits) { return bits == 8 ? 4 : 6; }  // steps in flight (even)
-constexpr int PR_SC = 2;                                                         // code chunks in flight
+__host__ __device__ constexpr int pr_code_chunks(int bits) { return bits == 8 ? 4 : 3; }  // code chunks in flight
 __host__ __device__ constexpr int pr_smem_bytes(int bits) {
-  return 1024 + pr_steps(bits) * (PR_A_BYTES + PR_X_BYTES) + PR_SC * tc_code_bytes(bits) + PR_EPI_BYTES + 512;
+  return 1024 + pr_steps(bits) * (PR_A_BYTES + PR_X_BYTES) + pr_code_chunks(bits) * tc_code_bytes(bits) + PR_EPI_BYTES + 512;
 }
 static_assert(pr_smem_bytes(4) <= 227 * 1024 && pr_smem_bytes(8) <= 227 * 1024, "shared memory");
 
@@ -91,7 +91,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PR_THREADS, 1)
     packed_pair_kernel(const __grid_constant__ CUtensorMap codes_map, const __grid_constant__ CUtensorMap x_map,
                        const __grid_constant__ CUtensorMap xlo_map, const PairArgs p) {
   constexpr int UNITS = 128 / GU;
-  constexpr int SC = PR_SC, NS = pr_steps(BITS), CODES = tc_code_bytes(BITS);
+  constexpr int SC = pr_code_chunks(BITS), NS = pr_steps(BITS), CODES = tc_code_bytes(BITS);
   extern __shared__ uint8_t pr_smem_raw[];
   const uint32_t raw_s = smem_u32(pr_smem_raw);
   uint8_t* smem = pr_smem_raw + (((raw_s + 1023u) & ~1023u) - raw_s);
@@ -198,43 +198,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PR_THREADS, 1)
       // ---------------- MMA for the pair ----------------
       const uint32_t fmt = (BF && !BWD) ? 1u : 0u;
       const uint32_t idesc = idesc_make(fmt, fmt, BWD ? 1u : 0u, 0u, 256, PR_TN);
+      // This thread shares its scheduler with unpack and drain warps, so its instructions are few:
+      // descriptors are those of step 0 plus the slot's and the 16-wide slice's offsets.
+      // Forward: K-major; gradient: MN-major, 16 rows = two 8-row atoms, 64-column halves 8 KB apart.
+      const uint64_t ad0 = BWD ? sdesc_sw128(a_base, PR_A_BYTES / 2, 1024) : sdesc_sw128(a_base, 16, 1024);
+      const uint64_t bd0 = sdesc_sw128(x_base, 16, 1024);
+      constexpr uint32_t A_SLICE = (BWD ? 2048 : 32) >> 4, B_SLICE = 32 >> 4;
+      constexpr int SUB = (!BWD && GU == 32) ? 2 : 1;  // accumulation units of a step
       RingPos<NS> x;
       RingPos<2> t;
       bool ok = true;
       for (int tile = cluster; tile < ntiles && ok; tile += clusters) {
-        for (int i = 0; i < 2 * p.steps && ok; ++i) {
-          if (!mbar_wait_bounded_cl(bar_full + 8 * x.s, x.ph, abort_flag)) {
-            ok = false;
-            break;
-          }
-          const uint32_t a_t = a_base + x.s * PR_A_BYTES, x_t = x_base + x.s * PR_X_BYTES;
-          constexpr int SUB = (!BWD && GU == 32) ? 2 : 1;  // accumulation units of a step
+        for (int i = 0; i < p.steps && ok; ++i) {
 #pragma unroll
-          for (int u = 0; u < SUB; ++u) {
-            // a unit starts with this step's MMAs (u = 0), and ends with them
-            const bool first = BWD ? i == 0 : (GU < 128 || (i & 1) == 0);
-            const bool last = BWD ? i == 2 * p.steps - 1 : (GU < 128 || (i & 1) == 1);
-            if (first && !mbar_wait_bounded_cl(bar_tempty + 8 * t.s, t.ph ^ 1u, abort_flag)) {
+          for (int h = 0; h < 2; ++h) {
+            if (!mbar_wait_bounded_cl(bar_full + 8 * x.s, x.ph, abort_flag)) {
               ok = false;
               break;
             }
-            tc_fence_after();
-            const uint32_t d = tmem_base + static_cast<uint32_t>(t.s * PR_TN);
+            const uint64_t ad = ad0 + static_cast<uint32_t>(x.s * (PR_A_BYTES >> 4)),
+                           bd = bd0 + static_cast<uint32_t>(x.s * (PR_X_BYTES >> 4));
 #pragma unroll
-            for (int k = 0; k < 4 / SUB; ++k) {
-              const int kk = u * (4 / SUB) + k;
-              // forward: K-major; gradient: MN-major, 16 rows = two 8-row atoms, 64-column halves 8 KB apart
-              const uint64_t ad = BWD ? sdesc_sw128(a_t + kk * 2048, PR_A_BYTES / 2, 1024)
-                                      : sdesc_sw128(a_t + kk * 32, 16, 1024);
-              umma_f16_pair(d, ad, sdesc_sw128(x_t + kk * 32, 16, 1024), idesc, (first && k == 0) ? 0u : 1u);
+            for (int u = 0; u < SUB; ++u) {
+              // a unit starts and ends with this step's MMAs: gradient, the whole tile is one unit
+              const bool first = BWD ? (h == 0 && i == 0) : (GU < 128 || h == 0);
+              const bool last = BWD ? (h == 1 && i == p.steps - 1) : (GU < 128 || h == 1);
+              if (first && !mbar_wait_bounded_cl(bar_tempty + 8 * t.s, t.ph ^ 1u, abort_flag)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              const uint32_t d = tmem_base + static_cast<uint32_t>(t.s * PR_TN);
+#pragma unroll
+              for (int k = 0; k < 4 / SUB; ++k) {
+                const uint32_t kk = u * (4 / SUB) + k;
+                umma_f16_pair(d, ad + kk * A_SLICE, bd + kk * B_SLICE, idesc, (first && k == 0) ? 0u : 1u);
+              }
+              if (u == SUB - 1) umma_commit_pair_mc(bar_empty + 8 * x.s, 0x3);
+              if (last) {
+                umma_commit_pair_mc(bar_tfull + 8 * t.s, 0x3);
+                t.next();
+              }
             }
-            if (u == SUB - 1) umma_commit_pair_mc(bar_empty + 8 * x.s, 0x3);
-            if (last) {
-              umma_commit_pair_mc(bar_tfull + 8 * t.s, 0x3);
-              t.next();
-            }
+            if (!ok) break;
+            x.next();
           }
-          x.next();
         }
       }
       if (!ok) {  // MMAs may still be running: wait for them before tensor memory is released
@@ -324,36 +332,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PR_THREADS, 1)
     const int qd = warp & 3, half = (warp - 12) >> 2;
     const uint32_t lead_tempty = mapa_shared(bar_tempty, 0);
     const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(qd * 32) << 16) + static_cast<uint32_t>(half * 128);
-    float* stage = reinterpret_cast<float*>(smem + (e_base - sbase)) + (warp - 12) * 512;  // [16 tokens][32 rows]
+    float* stage = reinterpret_cast<float*>(smem + (e_base - sbase)) + (warp - 12) * 256;  // [8 tokens][32 rows]
     RingPos<2> t;
     bool ok = true;
     for (int tile = cluster; tile < ntiles && ok; tile += clusters) {
       const int mt = tile % p.tiles_m * 2 + static_cast<int>(rank);
       const int row0 = mt * 128 + qd * 32;                       // rows of Y, or columns of dX
       const int tok0 = tile / p.tiles_m * PR_TN + half * 128;
-      // 16 tokens of the sums, from the staging buffer: lane = 4 rows of every fourth token
-      auto write16 = [&](int j0) {
+      // Eight tokens from the staging buffer to rows of `out` (f32: fp32, else 16 bits), + res: a lane
+      // writes four rows of two tokens.  Little code: the callers unroll it over the registers.
+      const int row = row0 + 4 * (lane & 7), tl = lane >> 3, rows = BWD ? p.n : p.lin.m;
+      const bool whole = (BWD ? p.dx_vec : p.lin.vec) && row + 4 <= rows;
+      auto put8 = [&](int j0, void* out, int64_t ld, bool f32, const uint16_t* res) {
         __syncwarp();
-#pragma unroll 1
-        for (int k = 0; k < 4; ++k) {
-          const int tl = k * 4 + (lane >> 3), tok = tok0 + j0 + tl, row = row0 + 4 * (lane & 7);
-          const float4 v = *reinterpret_cast<const float4*>(stage + tl * 32 + 4 * (lane & 7));
-          if (BWD) {
-            if (tok < p.lin.T && row < p.n) {
-              const float s = p.token_scale ? p.token_scale[tok] : 1.0f;
-              uint16_t* d = p.dX + static_cast<size_t>(tok) * p.lddx + row;
-              const uint32_t lo = pack2<BF>(v.x * s, v.y * s), hi = pack2<BF>(v.z * s, v.w * s);
-              if (p.dx_vec) {
-                *reinterpret_cast<uint2*>(d) = make_uint2(lo, hi);
-              } else {
-                d[0] = static_cast<uint16_t>(lo);
-                d[1] = static_cast<uint16_t>(lo >> 16);
-                d[2] = static_cast<uint16_t>(hi);
-                d[3] = static_cast<uint16_t>(hi >> 16);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int t = tok0 + j0 + 4 * k + tl;
+          if (t < p.lin.T && row < rows) {
+            const float4 v = *reinterpret_cast<const float4*>(stage + (4 * k + tl) * 32 + 4 * (lane & 7));
+            float z[4] = {v.x, v.y, v.z, v.w};
+            const size_t at = static_cast<size_t>(t) * ld + row;
+            if (whole) {
+              if (res) {
+                const ushort4 r = *reinterpret_cast<const ushort4*>(res + static_cast<size_t>(t) * p.lin.ld_res + row);
+                z[0] += h2f<BF>(r.x);
+                z[1] += h2f<BF>(r.y);
+                z[2] += h2f<BF>(r.z);
+                z[3] += h2f<BF>(r.w);
+              }
+              if (f32)
+                *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = make_float4(z[0], z[1], z[2], z[3]);
+              else
+                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) =
+                    make_uint2(pack2<BF>(z[0], z[1]), pack2<BF>(z[2], z[3]));
+            } else {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                if (row + j < rows) {
+                  if (res) z[j] += h2f<BF>(res[static_cast<size_t>(t) * p.lin.ld_res + row + j]);
+                  if (f32)
+                    static_cast<float*>(out)[at + j] = z[j];
+                  else
+                    static_cast<uint16_t*>(out)[at + j] = f2h<BF>(z[j]);
+                }
               }
             }
-          } else if (tok < p.lin.T && row < p.lin.m) {
-            linear_epilogue4<BF>(p.lin, tok, row, v);
           }
         }
         __syncwarp();
@@ -370,8 +393,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PR_THREADS, 1)
           tmem_ld_32x32b_x16(lane_base + static_cast<uint32_t>(t.s * PR_TN + cc * 16), v);
           tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < 16; ++j) stage[j * 32 + lane] = __uint_as_float(v[j]);
-          write16(cc * 16);
+          for (int g = 0; g < 2; ++g) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const int t = tok0 + cc * 16 + 8 * g + j;
+              const float ts = p.token_scale && t < p.lin.T ? __ldg(p.token_scale + t) : 1.0f;
+              stage[j * 32 + lane] = __uint_as_float(v[8 * g + j]) * ts;
+            }
+            put8(cc * 16 + 8 * g, p.dX, p.lddx, false, nullptr);
+          }
         }
         tc_fence_before();
         __syncwarp();
@@ -406,11 +436,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PR_THREADS, 1)
           t.next();
         }
         if (ok) {
+          if (p.lin.bias) {
+            const float bias = h2f<BF>(p.lin.bias[min(row0 + lane, p.lin.m - 1)]);
 #pragma unroll
-          for (int cc = 0; cc < 8; ++cc) {
+            for (int j = 0; j < 128; ++j) acc[j] += bias;
+          }
+          if (p.lin.preact) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) stage[j * 32 + lane] = acc[cc * 16 + j];
-            write16(cc * 16);
+            for (int cc = 0; cc < 16; ++cc) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) stage[j * 32 + lane] = acc[cc * 8 + j];
+              put8(cc * 8, p.lin.preact, p.lin.m, false, nullptr);
+            }
+          }
+          if (p.lin.act == ACT_RELU) {
+#pragma unroll
+            for (int j = 0; j < 128; ++j) acc[j] = acc[j] > 0.0f ? acc[j] : 0.0f;
+          } else if (p.lin.act == ACT_SILU) {
+#pragma unroll
+            for (int j = 0; j < 128; ++j) acc[j] = silu_fast(acc[j]);
+          } else if (p.lin.act == ACT_GELU) {
+#pragma unroll
+            for (int j = 0; j < 128; ++j) acc[j] = gelu_fast(acc[j]);
+          }
+#pragma unroll
+          for (int cc = 0; cc < 16; ++cc) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) stage[j * 32 + lane] = acc[cc * 8 + j];
+            put8(cc * 8, p.lin.Y, p.lin.ldy, p.lin.y_fp32 != 0, p.lin.residual);
           }
         }
       }
