@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 
 import torch
 
@@ -48,33 +49,12 @@ class KernelStat(ctypes.Structure):
                 ("flops", ctypes.c_double), ("bytes", ctypes.c_double)]
 
 
-class PackedLayer(ctypes.Structure):
-    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("zeros", ctypes.c_void_p),
-                ("perm", ctypes.c_void_p), ("m", ctypes.c_int64), ("n", ctypes.c_int64), ("qp", QParams)]
-
-
-class LinearArgs(ctypes.Structure):
-    _fields_ = [("X", ctypes.c_void_p), ("T", ctypes.c_int64), ("ld_x", ctypes.c_int64), ("dtype", ctypes.c_int),
-                ("W", PackedLayer), ("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p),
-                ("ld_res", ctypes.c_int64), ("act", ctypes.c_int), ("Y", ctypes.c_void_p), ("ld_y", ctypes.c_int64),
-                ("y_fp32", ctypes.c_int), ("preact", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
-                ("workspace_bytes", ctypes.c_size_t)]
-
-
-class LinearGradArgs(ctypes.Structure):
-    _fields_ = [("dY", ctypes.c_void_p), ("T", ctypes.c_int64), ("ld_dy", ctypes.c_int64), ("dtype", ctypes.c_int),
-                ("W", PackedLayer), ("act", ctypes.c_int), ("preact", ctypes.c_void_p), ("dX", ctypes.c_void_p),
-                ("ld_dx", ctypes.c_int64), ("dbias", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
-                ("workspace_bytes", ctypes.c_size_t)]
-
-
-class MoeArgs(ctypes.Structure):
-    _fields_ = [("X", ctypes.c_void_p), ("T", ctypes.c_int64), ("ld_x", ctypes.c_int64), ("dtype", ctypes.c_int),
-                ("router", ctypes.c_void_p), ("E", ctypes.c_int64), ("top_k", ctypes.c_int),
-                ("renormalize", ctypes.c_int), ("act", ctypes.c_int), ("gate_up", PackedLayer), ("down", PackedLayer),
-                ("residual", ctypes.c_void_p), ("ld_res", ctypes.c_int64), ("Y", ctypes.c_void_p),
-                ("ld_y", ctypes.c_int64), ("ids_out", ctypes.c_void_p), ("weights_out", ctypes.c_void_p),
-                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+# Argument blocks of the calls on packed layers (the C structures of the same names), packed natively;
+# "0q" pads to the alignment of the nested structure's end.
+_PACKED = "PPPPqqiii0q"                                                    # gptq_packed
+_LINEAR_ARGS = struct.Struct("@Pqqi0q" + _PACKED + "PPqiPqiPPN")           # gptq_linear_args
+_LINEAR_GRAD_ARGS = struct.Struct("@Pqqi0q" + _PACKED + "iPPqPPN")         # gptq_linear_grad_args
+_MOE_ARGS = struct.Struct("@PqqiPqiii0q" + _PACKED + _PACKED + "PqPqPPPN")  # gptq_moe_args
 
 
 ACT_NONE, ACT_RELU, ACT_GELU, ACT_SILU = range(4)
@@ -107,14 +87,14 @@ _SIGS = {
                                            QParams, _P, _P, ctypes.c_size_t, ctypes.c_int, _P]),
     "gptq_dequant_matmul_check": (ctypes.c_int, [_P, ctypes.c_int, _P]),
     "gptq_dequant_linear_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int]),
-    "gptq_dequant_linear": (ctypes.c_int, [ctypes.POINTER(LinearArgs), ctypes.c_int, _P]),
+    "gptq_dequant_linear": (ctypes.c_int, [ctypes.c_char_p, ctypes.c_int, _P]),
     "gptq_dequant_linear_backward_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64,
                                                                        ctypes.c_int64, ctypes.c_int, ctypes.c_int,
                                                                        ctypes.c_int]),
-    "gptq_dequant_linear_backward": (ctypes.c_int, [ctypes.POINTER(LinearGradArgs), ctypes.c_int, _P]),
+    "gptq_dequant_linear_backward": (ctypes.c_int, [ctypes.c_char_p, ctypes.c_int, _P]),
     "gptq_dequant_moe_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int,
                                                            ctypes.c_int64, ctypes.c_int64]),
-    "gptq_dequant_moe": (ctypes.c_int, [ctypes.POINTER(MoeArgs), ctypes.c_int, _P]),
+    "gptq_dequant_moe": (ctypes.c_int, [ctypes.c_char_p, ctypes.c_int, _P]),
     "gptq_quantize_layers": (ctypes.c_int, [ctypes.POINTER(LayerJob), ctypes.c_int, ctypes.c_int, _P]),
     "gptq_pipeline_create": (ctypes.c_int, [ctypes.POINTER(_P), ctypes.POINTER(ctypes.c_int64),
                                             ctypes.POINTER(ctypes.c_int64), ctypes.c_int, ctypes.c_int, _P]),
@@ -347,73 +327,84 @@ def dequant_matmul(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, z
     return out
 
 
-def _packed(codes, scales, zeros, perm, bits: int, group_size: int, dev: torch.device, experts: int = 0) -> PackedLayer:
-    """The C description of a packed layer (of `experts` stacked ones), its tensors checked."""
+def _packed(codes, scales, zeros, perm, bits: int, group_size: int, index: int, experts: int = 0) -> tuple:
+    """Fields of gptq_packed for a packed layer (`experts`: that many stacked ones), its tensors checked."""
     lead = (experts,) if experts else ()
-    if codes.dim() != 2 + len(lead) or tuple(codes.shape[:-2]) != lead:
-        raise ValueError(f"codes must be {'[E, m, words]' if lead else '[m, words]'}, got {tuple(codes.shape)}")
-    m, words = codes.shape[-2:]
-    if bits not in (2, 3, 4, 8) or words * 32 % bits:
+    shape = codes.shape
+    if len(shape) != 2 + len(lead) or (experts and shape[0] != experts):
+        raise ValueError(f"codes must be {'[E, m, words]' if lead else '[m, words]'}, got {tuple(shape)}")
+    m, words = shape[-2], shape[-1]
+    n, rest = divmod(words * 32, bits) if bits in (2, 3, 4, 8) else (0, 1)
+    if rest or n == 0:
         raise ValueError(f"bits must be 2, 3, 4 or 8 and fit the rows of codes, got {bits}")
-    n = words * 32 // bits
     g = n if group_size == -1 else group_size
     if g < 32 or n % g:
         raise ValueError(f"group_size {group_size} does not divide {n} columns")
     want = (*lead, m, n // g)
-    for name, t, dt, shape in (("codes", codes, torch.int32, codes.shape), ("scales", scales, torch.float32, want),
-                               ("zeros", zeros, torch.float32, want), ("perm", perm, torch.int32, (*lead, n))):
-        if t is None and name == "perm":
-            continue
-        if t.dtype != dt or t.shape != shape or not t.is_contiguous() or t.device != dev:
-            raise ValueError(f"{name} must be a contiguous {dt} {tuple(shape)} tensor on {dev}")
-    return PackedLayer(codes.data_ptr(), scales.data_ptr(), zeros.data_ptr(), None if perm is None else perm.data_ptr(),
-                       m, n, QParams(bits, group_size, 0))
+    for name, t, dt, sh in (("codes", codes, torch.int32, shape), ("scales", scales, torch.float32, want),
+                            ("zeros", zeros, torch.float32, want)):
+        if t.dtype is not dt or t.shape != sh or t.get_device() != index or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dt} {tuple(sh)} tensor on cuda:{index}")
+    p = None
+    if perm is not None:
+        if perm.dtype is not torch.int32 or perm.shape != (*lead, n) or perm.get_device() != index \
+                or not perm.is_contiguous():
+            raise ValueError(f"perm must be a contiguous torch.int32 {(*lead, n)} tensor on cuda:{index}")
+        p = perm.data_ptr()
+    return codes.data_ptr(), scales.data_ptr(), zeros.data_ptr(), p or 0, m, n, bits, group_size, 0
 
 
-def _rows(name: str, t: torch.Tensor | None, shape: tuple, dtype: torch.dtype, dev: torch.device):
+def _rows(name: str, t: torch.Tensor | None, rows: int, cols: int, dtype: torch.dtype, index: int) -> tuple:
     """(pointer, row stride) of an optional row-major matrix with unit column stride."""
     if t is None:
-        return None, 0
-    if t.dtype != dtype or t.shape != shape or t.device != dev or (t.stride(1) != 1 and shape[1] > 1):
-        raise ValueError(f"{name} must be a {dtype} {tuple(shape)} tensor with unit column stride on {dev}")
-    return t.data_ptr(), t.stride(0) if shape[0] > 1 else max(t.stride(0), shape[1])
+        return 0, 0
+    if t.dtype is not dtype or t.shape != (rows, cols) or t.get_device() != index or (t.stride(1) != 1 and cols > 1):
+        raise ValueError(f"{name} must be a {dtype} {(rows, cols)} tensor with unit column stride on cuda:{index}")
+    return t.data_ptr(), (t.stride(0) if rows > 1 else cols)
 
 
-def _activations(name: str, X: torch.Tensor, n: int):
+def _activations(name: str, X: torch.Tensor, n: int) -> tuple:
     """Checks of the left operand: (pointer, tokens, row stride, dtype code)."""
-    if X.dim() != 2 or X.shape[1] != n or X.dtype not in _DTYPES or not X.is_cuda or (X.stride(1) != 1 and n > 1):
+    shape = X.shape
+    if len(shape) != 2 or shape[1] != n or X.dtype not in _DTYPES or not X.is_cuda or (X.stride(1) != 1 and n > 1):
         raise ValueError(f"{name} must be an fp16 or bf16 [T, {n}] device tensor with unit column stride")
-    ld = X.stride(0) if X.shape[0] > 1 else n
-    if ld % 8 or ld < n or X.data_ptr() % 16:
+    T = shape[0]
+    ld, at = (X.stride(0) if T > 1 else n), X.data_ptr()
+    if ld % 8 or ld < n or at % 16:
         raise ValueError(f"{name} needs a 16-byte aligned base and a row stride that is a multiple of 8 elements "
                          "and no smaller than a row")
-    return X.data_ptr(), X.shape[0], ld, _DTYPES[X.dtype]
+    return at, T, ld, _DTYPES[X.dtype]
 
 
-class _on:
-    """Allocations and launches of a call on `stream` (None: the device's current stream)."""
+# The current stream's handle without building a Stream object, where torch offers it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
-    def __init__(self, dev: torch.device, stream: torch.cuda.Stream | None):
-        current = torch.cuda.current_stream(dev)
-        self.handle = (current if stream is None else stream).cuda_stream
-        self.ctx = None if self.handle == current.cuda_stream else torch.cuda.stream(stream)
+
+class _On:
+    """Allocations and launches of a call on a stream that is not the current one."""
+
+    def __init__(self, stream: torch.cuda.Stream):
+        self.ctx = torch.cuda.stream(stream)
+        self.handle = stream.cuda_stream
 
     def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
+        self.ctx.__enter__()
         return self.handle
 
     def __exit__(self, *a):
-        if self.ctx is not None:
-            self.ctx.__exit__(*a)
+        self.ctx.__exit__(*a)
 
 
-def _workspace(need: int, workspace: torch.Tensor | None, dev: torch.device) -> torch.Tensor:
+def _workspace(need: int, workspace: torch.Tensor | None, like: torch.Tensor) -> torch.Tensor:
+    """The caller's workspace, checked, or a new one of `need` bytes on the device of `like`."""
+    if need == 0:
+        raise GPTQError(ERR_ARG, "workspace size")
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=dev)
-    if workspace.dtype != torch.uint8 or workspace.device != dev or not workspace.is_contiguous() \
+        return like.new_empty(need, dtype=torch.uint8)
+    if workspace.dtype != torch.uint8 or workspace.device != like.device or not workspace.is_contiguous() \
             or workspace.numel() < need:
-        raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {need} bytes on {dev}")
+        raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {need} bytes on {like.device}")
     return workspace
 
 
@@ -428,31 +419,42 @@ def dequant_linear(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, z
     residual [T, m] in X's type; act one of ACT_NONE, ACT_RELU, ACT_GELU, ACT_SILU.  Returns Y [T, m]
     in X's type (or fp32 with out_dtype=torch.float32), and with want_preact also Z, the value the
     activation was applied to, which dequant_linear_backward takes.  `out` may be `residual`.
-    Asynchronous on `stream`; capturable into a graph when out and workspace are given or the
-    capture owns the allocations."""
-    dev = X.device
-    W = _packed(codes, scales, zeros, perm, bits, group_size, dev)
-    m, n = W.m, W.n
+    Asynchronous on `stream` (default: the device's current one; another stream's allocations are made
+    on it); can be captured into a graph."""
+    if stream is not None and stream.cuda_stream != _raw_stream(X.get_device()):
+        with _On(stream):
+            return dequant_linear(X, codes, scales, zeros, perm, bits, group_size, bias, act, residual, out_dtype,
+                                  want_preact, out, workspace)
+    index = X.get_device()
+    W = _packed(codes, scales, zeros, perm, bits, group_size, index)
+    m, n = W[4], W[5]
     x_ptr, T, ldx, dt = _activations("X", X, n)
-    if out_dtype not in (None, X.dtype, torch.float32):
+    xt = X.dtype
+    b_ptr = 0
+    if bias is not None:
+        if bias.dtype is not xt or bias.shape != (m,) or bias.get_device() != index or not bias.is_contiguous():
+            raise ValueError(f"bias must be a contiguous {xt} [{m}] tensor on cuda:{index}")
+        b_ptr = bias.data_ptr()
+    r_ptr, ldr = _rows("residual", residual, T, m, xt, index)
+    if out_dtype is None or out_dtype is xt:
+        y_type, f32 = xt, 0
+    elif out_dtype is torch.float32:
+        y_type, f32 = out_dtype, 1
+    else:
         raise ValueError("out_dtype must be X's type or torch.float32")
-    if bias is not None and (bias.dtype != X.dtype or bias.shape != (m,) or not bias.is_contiguous()
-                             or bias.device != dev):
-        raise ValueError(f"bias must be a contiguous {X.dtype} [{m}] tensor on {dev}")
-    r_ptr, ldr = _rows("residual", residual, (T, m), X.dtype, dev)
-    y_type = X.dtype if out_dtype is None else out_dtype
-    with _on(dev, stream) as handle:
-        if out is None:
-            out = torch.empty((T, m), dtype=y_type, device=dev)
-        y_ptr, ldy = _rows("out", out, (T, m), y_type, dev)
-        z = torch.empty((T, m), dtype=X.dtype, device=dev) if want_preact else None
-        need = int(lib().gptq_dequant_linear_workspace_bytes(T, n, int(perm is not None)))
-        if need == 0:
-            raise GPTQError(ERR_ARG, "gptq_dequant_linear_workspace_bytes")
-        ws = _workspace(need, workspace, dev)
-        a = LinearArgs(x_ptr, T, ldx, dt, W, None if bias is None else bias.data_ptr(), r_ptr, ldr, int(act), y_ptr, ldy,
-                       int(y_type == torch.float32), None if z is None else z.data_ptr(), ws.data_ptr(), ws.numel())
-        _check(lib().gptq_dequant_linear(ctypes.byref(a), dev.index, handle), "gptq_dequant_linear")
+    if out is None:
+        out = X.new_empty((T, m), dtype=y_type) if f32 else X.new_empty((T, m))
+        y_ptr, ldy = out.data_ptr(), m
+    else:
+        y_ptr, ldy = _rows("out", out, T, m, y_type, index)
+    z = X.new_empty((T, m)) if want_preact else None
+    L = lib()
+    ws = _workspace(L.gptq_dequant_linear_workspace_bytes(T, n, perm is not None), workspace, X)
+    a = _LINEAR_ARGS.pack(x_ptr, T, ldx, dt, *W, b_ptr, r_ptr, ldr, act, y_ptr, ldy, f32, 0 if z is None else z.data_ptr(),
+                          ws.data_ptr(), ws.numel())
+    st = L.gptq_dequant_linear(a, index, _raw_stream(index))
+    if st != OK:
+        raise GPTQError(st, "gptq_dequant_linear")
     return (out, z) if want_preact else out
 
 
@@ -465,35 +467,36 @@ def dequant_linear_backward(dY: torch.Tensor, codes: torch.Tensor, scales: torch
     [T, m]; preact: the Z that dequant_linear(want_preact=True) gave (needed unless act is ACT_NONE).
     Returns dX [T, n] in dY's type, or (dX, dbias) with want_dbias (dbias fp32 [m]; dX is None with
     want_dx=False).  The residual's gradient is dY itself.  Asynchronous on `stream`."""
-    dev = dY.device
-    W = _packed(codes, scales, zeros, perm, bits, group_size, dev)
-    m, n = W.m, W.n
+    if stream is not None and stream.cuda_stream != _raw_stream(dY.get_device()):
+        with _On(stream):
+            return dequant_linear_backward(dY, codes, scales, zeros, perm, bits, group_size, act, preact, want_dx,
+                                           want_dbias, out, workspace)
+    index = dY.get_device()
+    W = _packed(codes, scales, zeros, perm, bits, group_size, index)
+    m, n = W[4], W[5]
     if dY.dim() != 2 or dY.shape[1] != m or dY.dtype not in _DTYPES or not dY.is_cuda:
         raise ValueError(f"dY must be an fp16 or bf16 [T, {m}] device tensor")
-    T = dY.shape[0]
-    dy_ptr, ld_dy = _rows("dY", dY, (T, m), dY.dtype, dev)
-    z_ptr = None
+    T, t = dY.shape[0], dY.dtype
+    dy_ptr, ld_dy = _rows("dY", dY, T, m, t, index)
+    z_ptr = 0
     if act != ACT_NONE:
-        if preact is None or preact.dtype != dY.dtype or preact.shape != (T, m) or not preact.is_contiguous() \
-                or preact.device != dev:
-            raise ValueError(f"preact must be a contiguous {dY.dtype} [{T}, {m}] tensor on {dev}")
+        if preact is None or preact.dtype is not t or preact.shape != (T, m) or not preact.is_contiguous() \
+                or preact.get_device() != index:
+            raise ValueError(f"preact must be a contiguous {t} [{T}, {m}] tensor on cuda:{index}")
         z_ptr = preact.data_ptr()
     if not (want_dx or want_dbias):
         raise ValueError("nothing to compute: want_dx and want_dbias are both off")
-    dt = _DTYPES[dY.dtype]
-    with _on(dev, stream) as handle:
-        dx = None
-        if want_dx:
-            dx = torch.empty((T, n), dtype=dY.dtype, device=dev) if out is None else out
-        dx_ptr, ld_dx = _rows("out", dx, (T, n), dY.dtype, dev)
-        db = torch.empty(m, dtype=torch.float32, device=dev) if want_dbias else None
-        need = int(lib().gptq_dequant_linear_backward_workspace_bytes(T, m, n, int(perm is not None), dt, int(act)))
-        if need == 0:
-            raise GPTQError(ERR_ARG, "gptq_dequant_linear_backward_workspace_bytes")
-        ws = _workspace(need, workspace, dev)
-        a = LinearGradArgs(dy_ptr, T, ld_dy, dt, W, int(act), z_ptr, dx_ptr, ld_dx, None if db is None else db.data_ptr(),
-                           ws.data_ptr(), ws.numel())
-        _check(lib().gptq_dequant_linear_backward(ctypes.byref(a), dev.index, handle), "gptq_dequant_linear_backward")
+    dt = _DTYPES[t]
+    dx = (dY.new_empty((T, n)) if out is None else out) if want_dx else None
+    dx_ptr, ld_dx = _rows("out", dx, T, n, t, index)
+    db = dY.new_empty(m, dtype=torch.float32) if want_dbias else None
+    L = lib()
+    ws = _workspace(L.gptq_dequant_linear_backward_workspace_bytes(T, m, n, perm is not None, dt, act), workspace, dY)
+    a = _LINEAR_GRAD_ARGS.pack(dy_ptr, T, ld_dy, dt, *W, act, z_ptr, dx_ptr, ld_dx, 0 if db is None else db.data_ptr(),
+                               ws.data_ptr(), ws.numel())
+    st = L.gptq_dequant_linear_backward(a, index, _raw_stream(index))
+    if st != OK:
+        raise GPTQError(st, "gptq_dequant_linear_backward")
     return (dx, db) if want_dbias else dx
 
 
@@ -508,32 +511,35 @@ def dequant_moe(X: torch.Tensor, router: torch.Tensor, gate_up: tuple, down: tup
     act-order of each expert's gate and up, or None (stack_experts builds these from quantized
     layers).  Returns Y [T, H], the chosen experts [T, top_k] (int32, by descending probability) and
     their weights [T, top_k] (fp32).  Asynchronous on `stream`."""
-    dev = X.device
+    if stream is not None and stream.cuda_stream != _raw_stream(X.get_device()):
+        with _On(stream):
+            return dequant_moe(X, router, gate_up, down, perm, bits, group_size, top_k, renormalize, act, residual,
+                               down_group_size, out, workspace)
+    index = X.get_device()
     E = router.shape[0] if router.dim() == 2 else 0
     if E == 0:
         raise ValueError("router must be [E, H] with at least one expert")
-    gu = _packed(*gate_up, perm, bits, group_size, dev, E)
-    dn = _packed(*down, None, bits, group_size if down_group_size is None else down_group_size, dev, E)
-    H, I = gu.n, dn.n
-    if gu.m != 2 * I or dn.m != H:
-        raise ValueError(f"gate_up [E, {gu.m}, {H} columns] and down [E, {dn.m}, {I} columns] do not fit together")
+    gu = _packed(*gate_up, perm, bits, group_size, index, E)
+    dn = _packed(*down, None, bits, group_size if down_group_size is None else down_group_size, index, E)
+    H, I = gu[5], dn[5]
+    if gu[4] != 2 * I or dn[4] != H:
+        raise ValueError(f"gate_up [E, {gu[4]}, {H} columns] and down [E, {dn[4]}, {I} columns] do not fit together")
     x_ptr, T, ldx, dt = _activations("X", X, H)
-    if router.dtype != X.dtype or router.shape[1] != H or not router.is_contiguous() or router.device != dev:
-        raise ValueError(f"router must be a contiguous {X.dtype} [E, {H}] tensor on {dev}")
-    r_ptr, ldr = _rows("residual", residual, (T, H), X.dtype, dev)
-    with _on(dev, stream) as handle:
-        if out is None:
-            out = torch.empty((T, H), dtype=X.dtype, device=dev)
-        y_ptr, ldy = _rows("out", out, (T, H), X.dtype, dev)
-        ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
-        weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
-        need = int(lib().gptq_dequant_moe_workspace_bytes(T, E, top_k, H, I))
-        if need == 0:
-            raise GPTQError(ERR_ARG, "gptq_dequant_moe_workspace_bytes")
-        ws = _workspace(need, workspace, dev)
-        a = MoeArgs(x_ptr, T, ldx, dt, router.data_ptr(), E, int(top_k), int(bool(renormalize)), int(act), gu, dn, r_ptr,
-                    ldr, y_ptr, ldy, ids.data_ptr(), weights.data_ptr(), ws.data_ptr(), ws.numel())
-        _check(lib().gptq_dequant_moe(ctypes.byref(a), dev.index, handle), "gptq_dequant_moe")
+    if router.dtype is not X.dtype or router.shape[1] != H or not router.is_contiguous() or router.get_device() != index:
+        raise ValueError(f"router must be a contiguous {X.dtype} [E, {H}] tensor on cuda:{index}")
+    r_ptr, ldr = _rows("residual", residual, T, H, X.dtype, index)
+    if out is None:
+        out = X.new_empty((T, H))
+    y_ptr, ldy = _rows("out", out, T, H, X.dtype, index)
+    ids = X.new_empty((T, top_k), dtype=torch.int32)
+    weights = X.new_empty((T, top_k), dtype=torch.float32)
+    L = lib()
+    ws = _workspace(L.gptq_dequant_moe_workspace_bytes(T, E, top_k, H, I), workspace, X)
+    a = _MOE_ARGS.pack(x_ptr, T, ldx, dt, router.data_ptr(), E, top_k, renormalize, act, *gu, *dn, r_ptr, ldr, y_ptr, ldy,
+                       ids.data_ptr(), weights.data_ptr(), ws.data_ptr(), ws.numel())
+    st = L.gptq_dequant_moe(a, index, _raw_stream(index))
+    if st != OK:
+        raise GPTQError(st, "gptq_dequant_moe")
     return out, ids, weights
 
 
