@@ -119,6 +119,22 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
   return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 
+// The same with all lanes testing the barrier together and one decision for the warp: no branch by lane.
+__device__ __forceinline__ bool warp_wait_uniform(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  uint64_t t0 = 0;
+  for (uint32_t i = 1;; ++i) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if ((i & 255u) == 0) {
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      const bool late = now - t0 > kWaitLimitNs;
+      if (__any_sync(0xffffffffu, late)) *abort_flag = 1;
+      if (__any_sync(0xffffffffu, late || *abort_flag)) return false;
+    }
+  }
+}
+
 template <bool BF>
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                           uint32_t b0, uint32_t b1) {
@@ -132,6 +148,22 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The same with a zero addend (the first product of a sum).
+template <bool BF>
+__device__ __forceinline__ void mma_16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                uint32_t b0, uint32_t b1) {
+  if (BF)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 // ------------------------------------------------------------------------------------------
@@ -501,7 +533,7 @@ struct Ring {
 #pragma unroll
       for (int jj = 0; jj < PER; ++jj) {
         if (jj * UNITS < left) {
-          if (!warp_wait(full + 8 * cur.s, cur.ph, abort_flag, lane)) return false;
+          if (!warp_wait_uniform(full + 8 * cur.s, cur.ph, abort_flag)) return false;
           const uint32_t st = base + cur.s * STAGE;
           Raw ra, rb;
           ra.load(st + offa, q);
@@ -509,10 +541,6 @@ struct Ring {
 #pragma unroll
           for (int u = 0; u < UNITS; ++u) {
             float sum[TL][4];
-#pragma unroll
-            for (int t = 0; t < TL; ++t)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) sum[t][j] = 0.0f;
             const float pv = now[(jj * UNITS + u) % 4];
             const float s_a = __shfl_sync(0xffffffffu, pv, src), s_b = __shfl_sync(0xffffffffu, pv, src | 2);
             const ZeroTerm za = zero_term<BITS, BF>(__shfl_sync(0xffffffffu, pv, src | 1)),
@@ -527,7 +555,10 @@ struct Ring {
 #pragma unroll
               for (int t = 0; t < TL; ++t) {
                 const uint4 x = lds128(XL ? xat : st + CODES + t * FRAG_BYTES + (u * BLOCKS + b) * 512 + lane * 16);
-                mma_16816<BF>(sum[t], pa[0], pb[0], pa[1], pb[1], x.x, x.y);
+                if (b == 0)
+                  mma_16816_first<BF>(sum[t], pa[0], pb[0], pa[1], pb[1], x.x, x.y);
+                else
+                  mma_16816<BF>(sum[t], pa[0], pb[0], pa[1], pb[1], x.x, x.y);
                 mma_16816<BF>(sum[t], pa[2], pb[2], pa[3], pb[3], x.z, x.w);
               }
               if (XL) xat += xstep;
@@ -543,7 +574,7 @@ struct Ring {
           // The stage's loads have to be done, not only issued, before it is given back: with 16 warps'
           // loads queued, the copy that refills it was seen to overtake them where only the arrival
           // stood here (run-to-run differences; none with the fence, which costs 1 %).
-          __threadfence_block();
+          asm volatile("fence.acq_rel.cta;" ::: "memory");
           __syncwarp();
           if (lane == 0) mbar_arrive(empty + 8 * cur.s);
           cur.next();
