@@ -86,8 +86,8 @@ struct RouterArgs {
   int* status;
 };
 
-// One cluster.  (1) Logits: tiles of 16 experts x 8 tokens go round the blocks, a tile's 16 warps
-// split H; products of 16-bit values are exact in fp32, 128 columns are summed on the tensor cores
+// One cluster.  (1) Logits: tiles of 16 experts x 8 tokens go round the blocks, two at a time; a
+// tile's eight warps split H; products of 16-bit values are exact in fp32, 128 columns are summed on the tensor cores
 // and the partial sums of those in fp64, so the order of the choices is that of the 64-bit logits
 // but for logits that agree to about 1e-7.  (2) Softmax and top-k: a warp per token, in fp64; equal
 // values go to the lower expert; a NaN logit is chosen last (its weights are NaN).  (3) The lists:
@@ -106,23 +106,31 @@ __global__ void __launch_bounds__(ROUTER_WARPS * 32) moe_router_kernel(const Rou
   const int rank = static_cast<int>(cluster_ctarank());
   if (rank == 0 && threadIdx.x == 0) *p.status = 0;
   const int et = (p.E + 15) / 16, tt = (p.T + 7) / 8, blocks = p.H / 32;
-  for (int tile = rank; tile < et * tt; tile += ROUTER_CLUSTER) {
+  constexpr int KW = ROUTER_WARPS / 2;  // warps of a tile
+  const int half = warp / KW, kw = warp % KW;
+  for (int first = rank * 2; first < et * tt; first += ROUTER_CLUSTER * 2) {
+    const int tile = min(first + half, et * tt - 1);  // (an odd last tile is computed twice, alike)
     const int e0 = (tile % et) * 16, t0 = (tile / et) * 8;
     const uint16_t* ra = p.R + static_cast<size_t>(min(e0 + g, p.E - 1)) * p.H + q * 8;
     const uint16_t* rb = p.R + static_cast<size_t>(min(e0 + g + 8, p.E - 1)) * p.H + q * 8;
     const uint16_t* x = p.X + static_cast<size_t>(min(t0 + g, p.T - 1)) * p.ldx + q * 8;
     double acc[4] = {0.0, 0.0, 0.0, 0.0};
-    const int b0 = blocks * warp / ROUTER_WARPS, b1 = blocks * (warp + 1) / ROUTER_WARPS;
+    const int b0 = blocks * kw / KW, b1 = blocks * (kw + 1) / KW;
     for (int b = b0; b < b1; b += 4) {
+      uint4 va[4], vb[4], vx[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int at = min(b + j, b1 - 1) * 32;
+        va[j] = *reinterpret_cast<const uint4*>(ra + at);
+        vb[j] = *reinterpret_cast<const uint4*>(rb + at);
+        vx[j] = *reinterpret_cast<const uint4*>(x + at);
+      }
       float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         if (b + j < b1) {
-          const uint4 va = *reinterpret_cast<const uint4*>(ra + (b + j) * 32);
-          const uint4 vb = *reinterpret_cast<const uint4*>(rb + (b + j) * 32);
-          const uint4 vx = *reinterpret_cast<const uint4*>(x + (b + j) * 32);
-          mma_16816<BF>(d, va.x, vb.x, va.y, vb.y, vx.x, vx.y);
-          mma_16816<BF>(d, va.z, vb.z, va.w, vb.w, vx.z, vx.w);
+          mma_16816<BF>(d, va[j].x, vb[j].x, va[j].y, vb[j].y, vx[j].x, vx[j].y);
+          mma_16816<BF>(d, va[j].z, vb[j].z, va[j].w, vb[j].w, vx[j].z, vx[j].w);
         }
       }
 #pragma unroll
@@ -131,81 +139,74 @@ __global__ void __launch_bounds__(ROUTER_WARPS * 32) moe_router_kernel(const Rou
 #pragma unroll
     for (int j = 0; j < 4; ++j) red[warp][lane * 4 + j] = acc[j];
     __syncthreads();
-    if (threadIdx.x < 128) {
+    if (threadIdx.x < 256) {
+      const int hh = threadIdx.x >> 7, i = threadIdx.x & 127;
+      const int mine = first + hh;
       double v = 0.0;
 #pragma unroll
-      for (int w = 0; w < ROUTER_WARPS; ++w) v += red[w][threadIdx.x];
-      const int l = threadIdx.x >> 2, j = threadIdx.x & 3;
-      const int e = e0 + (l >> 2) + 8 * (j >> 1), t = t0 + 2 * (l & 3) + (j & 1);
-      if (e < p.E && t < p.T) p.logits[static_cast<size_t>(t) * p.E + e] = v;
+      for (int w = 0; w < KW; ++w) v += red[hh * KW + w][i];
+      const int l = i >> 2, j = i & 3;
+      const int e = (mine % et) * 16 + (l >> 2) + 8 * (j >> 1), t = (mine / et) * 8 + 2 * (l & 3) + (j & 1);
+      if (mine < et * tt && e < p.E && t < p.T) p.logits[static_cast<size_t>(t) * p.E + e] = v;
     }
     __syncthreads();
   }
   cluster_sync();  // the logits are written
 
   constexpr int PER = MOE_MAX_E / 32;
+  const int per = (p.E + 31) / 32;
   for (int t = rank * ROUTER_WARPS + warp; t < p.T; t += ROUTER_CLUSTER * ROUTER_WARPS) {
-    double v[PER];
-    double best_all = -INFINITY;
+    // logits as keys whose unsigned order is theirs; a NaN comes after every number, a place past E
+    // is never taken (key 0)
+    double v[PER], best = -INFINITY;
+    unsigned long long key[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const int e = lane + 32 * i;
-      v[i] = e < p.E ? __ldcg(p.logits + static_cast<size_t>(t) * p.E + e) : -INFINITY;
-      best_all = fmax(best_all, v[i]);
+      key[i] = 0;
+      v[i] = 0.0;
+      if (i < per && lane + 32 * i < p.E) {
+        v[i] = __ldcg(p.logits + static_cast<size_t>(t) * p.E + lane + 32 * i);
+        const unsigned long long u = static_cast<unsigned long long>(__double_as_longlong(v[i] + 0.0));
+        key[i] = v[i] != v[i] ? 1ull : ((u >> 63) ? ~u : (u | 0x8000000000000000ull));
+        best = fmax(best, v[i]);
+      }
     }
 #pragma unroll
-    for (int o = 16; o; o >>= 1) best_all = fmax(best_all, __shfl_xor_sync(0xffffffffu, best_all, o));
+    for (int o = 16; o; o >>= 1) best = fmax(best, __shfl_xor_sync(0xffffffffu, best, o));
     double sum = 0.0;
 #pragma unroll
     for (int i = 0; i < PER; ++i)
-      if (lane + 32 * i < p.E) sum += exp(v[i] - best_all);
+      if (i < per && lane + 32 * i < p.E) sum += exp(v[i] - best);
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    unsigned used = 0;
     int my_id = 0;
-    double my_p = 0.0, chosen = 0.0;
     for (int k = 0; k < p.top_k; ++k) {
-      double bv = 0.0;
-      int bi = 1 << 30;  // none yet
-      bool bn = true;    // the best so far is a NaN (or none)
+      unsigned long long bk = 0;
+      unsigned bi = 0xffffffffu;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const int e = lane + 32 * i;
-        if (e < p.E && !((used >> i) & 1u)) {
-          const bool isn = v[i] != v[i];
-          const bool better = bi == (1 << 30) || (bn && !isn) || (!bn && !isn && v[i] > bv);
-          if (better) {
-            bv = v[i];
-            bi = e;
-            bn = isn;
-          }
+      for (int i = 0; i < PER; ++i)
+        if (i < per && key[i] > bk) {  // (equal keys: the lower expert stands first)
+          bk = key[i];
+          bi = lane + 32 * i;
         }
-      }
+      const unsigned hi = __reduce_max_sync(0xffffffffu, static_cast<unsigned>(bk >> 32));
+      const bool top = static_cast<unsigned>(bk >> 32) == hi;
+      const unsigned lo = __reduce_max_sync(0xffffffffu, top ? static_cast<unsigned>(bk) : 0u);
+      const unsigned id = __reduce_min_sync(0xffffffffu, top && static_cast<unsigned>(bk) == lo ? bi : 0xffffffffu);
 #pragma unroll
-      for (int o = 16; o; o >>= 1) {
-        const double ov = __shfl_xor_sync(0xffffffffu, bv, o);
-        const int oi = __shfl_xor_sync(0xffffffffu, bi, o);
-        const bool on = __shfl_xor_sync(0xffffffffu, static_cast<int>(bn), o) != 0;
-        const bool none = bi == (1 << 30), onone = oi == (1 << 30);
-        const bool take = !onone && (none || (bn && !on) ||
-                                     (bn == on && ((!bn && ov > bv) || ((bn || ov == bv) && oi < bi))));
-        if (take) {
-          bv = ov;
-          bi = oi;
-          bn = on;
-        }
-      }
-      const double pk = exp(bv - best_all) / sum;
-      if ((bi & 31) == lane) used |= 1u << (bi >> 5);
-      if (lane == k) {
-        my_id = bi;
-        my_p = pk;
-      }
-      chosen += pk;
+      for (int i = 0; i < PER; ++i)
+        if (static_cast<unsigned>(lane + 32 * i) == id) key[i] = 0;
+      if (lane == k) my_id = static_cast<int>(id);
     }
+    // (top_k <= E: every round finds an expert)
+    double mine = 0.0;
+    if (lane < p.top_k) mine = exp(__ldcg(p.logits + static_cast<size_t>(t) * p.E + my_id) - best) / sum;
+    double chosen = mine;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) chosen += __shfl_xor_sync(0xffffffffu, chosen, o);
     if (lane < p.top_k) {
       const size_t o = static_cast<size_t>(t) * p.top_k + lane;
-      const float w = static_cast<float>(p.renorm ? my_p / chosen : my_p);
+      const float w = static_cast<float>(p.renorm ? mine / chosen : mine);
       p.ids[o] = my_id;
       p.weights[o] = w;
       if (p.ids_out) p.ids_out[o] = my_id;
