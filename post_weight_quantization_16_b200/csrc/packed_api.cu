@@ -117,6 +117,18 @@ gptq_status encode_act(CUtensorMap* map, int dtype, const void* base, int64_t co
                     base, cols, rows, ld, 64, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// Blocks of a cluster that split a reduction of `chunks` chunks when `tiles` tiles leave SMs idle.
+int tc_cluster(int64_t tiles, int chunks) {
+  int cs = 1;
+  while (cs < 8 && tiles * (cs + 1) <= kSms && chunks >= 2 * (cs + 1)) ++cs;
+  return cs;
+}
+// Whether CTA pairs (one 256 x 256 tile per two SMs) serve a product of `rows` x T outputs: they need
+// tiles for most SM pairs.
+bool use_pairs(int64_t rows, int64_t T) {
+  return T > kSingleTokens && ((rows + 255) / 256) * ((T + PR_TN - 1) / PR_TN) >= kSms / 4;
+}
+
 // The linear layer on tcgen05: X in sweep order.
 gptq_status linear_many_tokens(const gptq_linear_args& a, const uint16_t* X, int64_t ldx, int device,
                                cudaStream_t st) {
@@ -145,7 +157,7 @@ gptq_status linear_many_tokens(const gptq_linear_args& a, const uint16_t* X, int
   d.status = static_cast<int*>(a.workspace);
   CUtensorMap cmap, xmap;
   gptq_status s = encode_codes(&cmap, a.W, TC_BM);
-  if (s == GPTQ_OK) s = encode_act(&xmap, a.dtype, X, n, T, ldx, std::min(d.tn, 128));
+  if (s == GPTQ_OK) s = encode_act(&xmap, a.dtype, X, n, T, ldx, d.tn);
   if (s != GPTQ_OK) return s;
   TcLaunch l;
   l.bf16 = a.dtype == GPTQ_BF16;
@@ -153,7 +165,7 @@ gptq_status linear_many_tokens(const gptq_linear_args& a, const uint16_t* X, int
   l.sms = kSms;
   l.device = device;
   l.stream = st;
-  if (T > kSingleTokens) {
+  if (use_pairs(m, T)) {
     PairArgs p = {};
     p.tiles_m = (m + 255) / 256;
     p.tiles_t = (T + PR_TN - 1) / PR_TN;
@@ -163,10 +175,10 @@ gptq_status linear_many_tokens(const gptq_linear_args& a, const uint16_t* X, int
                [&](auto b) { return launch_packed_pair<decltype(b)::value>(l, false, cmap, xmap, xmap, p); }));
     return GPTQ_OK;
   }
-  const int64_t tiles = static_cast<int64_t>((m + TC_BM - 1) / TC_BM) * ((T + d.tn - 1) / d.tn);
-  l.cluster = 1;
-  while (l.cluster < 8 && tiles * l.cluster * 2 <= kSms && d.chunks >= 4 * l.cluster) l.cluster *= 2;
-  CK(by_bits(a.W.qp.bits, [&](auto b) { return launch_linear_tc<decltype(b)::value>(l, cmap, xmap, d); }));
+  l.cluster = tc_cluster(static_cast<int64_t>((m + TC_BM - 1) / TC_BM) * ((T + d.tn - 1) / d.tn), d.chunks);
+  CK(by_bits(a.W.qp.bits, [&](auto b) {
+    return launch_packed_tc<decltype(b)::value>(l, false, cmap, xmap, xmap, d, GradOut{}, 1);
+  }));
   return GPTQ_OK;
 }
 
@@ -375,30 +387,28 @@ extern "C" gptq_status gptq_dequant_linear_backward(const gptq_linear_grad_args*
     hi = h;
     lo = o ? o : h;
   }
-  LinearBwdArgs d;
+  LinearTcArgs d = {};
   const int g = group_width(a.W);
   d.T = T;
   d.m = m;
-  d.n = n;
+  d.chunks = (m + 127) / 128;
   d.G = n / g;
   d.gi = group_index(g);
-  d.parts = std::max(1, lay.parts);
-  d.tn = T <= 32 ? 32 : T <= 64 ? 64 : T <= 128 ? 128 : 256;
-  while (d.tn > 32 && bw_stages(d.tn, a.W.qp.bits, d.parts) < 2) d.tn /= 2;
-  d.row_chunks = (m + 127) / 128;
+  d.tn = T <= 32 ? 32 : T <= 64 ? 64 : TC_MAX_TN;
   d.scales = a.W.scales;
   d.zeros = a.W.zeros;
-  d.token_scale = lay.parts >= 1 ? reinterpret_cast<const float*>(ws + lay.scale) : nullptr;
-  d.dX = a.W.perm ? reinterpret_cast<uint16_t*>(ws + lay.dx) : static_cast<uint16_t*>(a.dX);
-  d.lddx = a.W.perm ? n : a.ld_dx;
-  d.bf16_out = bf ? 1 : 0;
-  d.vec = d.lddx % 4 == 0 && aligned_to(d.dX, 8);
   d.status = reinterpret_cast<int*>(ws);
+  GradOut go;
+  go.token_scale = lay.parts >= 1 ? reinterpret_cast<const float*>(ws + lay.scale) : nullptr;
+  go.dX = a.W.perm ? reinterpret_cast<uint16_t*>(ws + lay.dx) : static_cast<uint16_t*>(a.dX);
+  go.lddx = a.W.perm ? n : a.ld_dx;
+  go.n = n;
+  go.vec = go.lddx % 4 == 0 && aligned_to(go.dX, 8);
+  const int parts = std::max(1, lay.parts);
   CUtensorMap cmap, hmap, lmap;
   gptq_status s = encode_codes(&cmap, a.W, TC_BM);
-  const bool pair = T > kSingleTokens;
-  if (s == GPTQ_OK) s = encode_act(&hmap, GPTQ_FP16, hi, m, T, ldz, pair ? 128 : d.tn);
-  if (s == GPTQ_OK) s = encode_act(&lmap, GPTQ_FP16, lo, m, T, ldz, pair ? 128 : d.tn);
+  if (s == GPTQ_OK) s = encode_act(&hmap, GPTQ_FP16, hi, m, T, ldz, d.tn);
+  if (s == GPTQ_OK) s = encode_act(&lmap, GPTQ_FP16, lo, m, T, ldz, d.tn);
   if (s != GPTQ_OK) return s;
   TcLaunch l;
   l.bf16 = bf;
@@ -406,37 +416,26 @@ extern "C" gptq_status gptq_dequant_linear_backward(const gptq_linear_grad_args*
   l.sms = kSms;
   l.device = device;
   l.stream = st;
-  if (pair) {
+  if (use_pairs(n, T)) {
     PairArgs p = {};
     p.tiles_m = (n + 255) / 256;
     p.tiles_t = (T + PR_TN - 1) / PR_TN;
-    p.chunks = d.row_chunks;
-    p.steps = d.parts * d.row_chunks;
-    p.lin.T = T;
-    p.lin.m = m;
-    p.lin.G = d.G;
-    p.lin.gi = d.gi;
-    p.lin.scales = d.scales;
-    p.lin.zeros = d.zeros;
-    p.lin.status = d.status;
-    p.token_scale = d.token_scale;
-    p.dX = d.dX;
-    p.lddx = d.lddx;
-    p.n = n;
-    p.dx_vec = d.vec;
+    p.chunks = d.chunks;
+    p.steps = parts * d.chunks;
+    p.lin = d;
+    p.go = go;
     CK(by_bits(a.W.qp.bits,
                [&](auto b) { return launch_packed_pair<decltype(b)::value>(l, true, cmap, hmap, lmap, p); }));
   } else {
-    const int64_t tiles = static_cast<int64_t>(n / 128) * ((T + d.tn - 1) / d.tn);
-    l.cluster = 1;
-    while (l.cluster < 8 && tiles * l.cluster * 2 <= kSms && d.row_chunks >= 4 * l.cluster) l.cluster *= 2;
-    CK(by_bits(a.W.qp.bits, [&](auto b) { return launch_linear_bwd_tc<decltype(b)::value>(l, cmap, hmap, lmap, d); }));
+    l.cluster = tc_cluster(static_cast<int64_t>(n / 128) * ((T + d.tn - 1) / d.tn), d.chunks);
+    CK(by_bits(a.W.qp.bits,
+               [&](auto b) { return launch_packed_tc<decltype(b)::value>(l, true, cmap, hmap, lmap, d, go, parts); }));
   }
   if (a.W.perm) {
     static std::atomic<uint64_t> done{0};
     CK(raise_smem_limit(done, device, unpermute_kernel, static_cast<int>(kPackedMaxN) * 2));
     CK(launch_pdl(unpermute_kernel, dim3(T), dim3(256), static_cast<size_t>(n) * 2, 1, st,
-                  static_cast<const uint16_t*>(d.dX), n, a.W.perm, static_cast<uint16_t*>(a.dX), a.ld_dx));
+                  static_cast<const uint16_t*>(go.dX), n, a.W.perm, static_cast<uint16_t*>(a.dX), a.ld_dx));
   }
   return GPTQ_OK;
 }

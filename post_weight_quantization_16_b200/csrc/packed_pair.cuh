@@ -47,20 +47,9 @@ struct PairArgs {
   int tiles_m, tiles_t;  // tiles of 256 rows (forward) or columns (gradient), and of 256 tokens
   int chunks, steps;     // 128-wide chunks of the reduction; steps = chunks, or 2 chunks with a low part
   LinearTcArgs lin;      // forward: everything; gradient: T, m, G, gi, scales, zeros, status
-  const float* token_scale;  // gradient: [T] or null
-  uint16_t* dX;
-  int64_t lddx;
-  int n, dx_vec;
+  GradOut go;            // gradient
 };
 
-template <int REGS>
-__device__ __forceinline__ void regs_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
-}
-template <int REGS>
-__device__ __forceinline__ void regs_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
-}
 // Arrival on a barrier of the pair's even block.  (A release at cluster scope would also wait for the
 // warp's loads of the next step's parameters: with it the gradient's kernel ran 590 us, not 430.)
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
@@ -272,7 +261,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PR_THREADS, 1)
         const int gr = (BWD ? i : mt) * 128 + r;
         const bool in = gr < p.lin.m;
         const size_t row = static_cast<size_t>(min(gr, p.lin.m - 1)) * p.lin.G;
-        const int kc = BWD ? min(mt, p.n / 128 - 1) : i;
+        const int kc = BWD ? min(mt, p.go.n / 128 - 1) : i;
 #pragma unroll
         for (int j = 0; j < ZN; ++j) {
           const size_t at = row + group_of<GU>(p.lin.gi, kc, GU == 128 ? 0 : GU == 64 ? h : 2 * h + j);
@@ -341,8 +330,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PR_THREADS, 1)
       const int tok0 = tile / p.tiles_m * PR_TN + half * 128;
       // Eight tokens from the staging buffer to rows of `out` (f32: fp32, else 16 bits), + res: a lane
       // writes four rows of two tokens.  Little code: the callers unroll it over the registers.
-      const int row = row0 + 4 * (lane & 7), tl = lane >> 3, rows = BWD ? p.n : p.lin.m;
-      const bool whole = (BWD ? p.dx_vec : p.lin.vec) && row + 4 <= rows;
+      const int row = row0 + 4 * (lane & 7), tl = lane >> 3, rows = BWD ? p.go.n : p.lin.m;
+      const bool whole = (BWD ? p.go.vec : p.lin.vec) && row + 4 <= rows;
       auto put8 = [&](int j0, void* out, int64_t ld, bool f32, const uint16_t* res) {
         __syncwarp();
 #pragma unroll
@@ -397,10 +386,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PR_THREADS, 1)
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               const int t = tok0 + cc * 16 + 8 * g + j;
-              const float ts = p.token_scale && t < p.lin.T ? __ldg(p.token_scale + t) : 1.0f;
+              const float ts = p.go.token_scale && t < p.lin.T ? __ldg(p.go.token_scale + t) : 1.0f;
               stage[j * 32 + lane] = __uint_as_float(v[8 * g + j]) * ts;
             }
-            put8(cc * 16 + 8 * g, p.dX, p.lddx, false, nullptr);
+            put8(cc * 16 + 8 * g, p.go.dX, p.go.lddx, false, nullptr);
           }
         }
         tc_fence_before();

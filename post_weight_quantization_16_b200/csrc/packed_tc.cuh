@@ -1,5 +1,6 @@
-// packed_tc.cuh — products of packed weights with many tokens on the sm_100a tensor cores
-// (tcgen05): the linear layer (linear_tc_kernel) and its gradient (linear_bwd_tc_kernel).
+// packed_tc.cuh — products of packed weights with 17 to 128 tokens on the sm_100a tensor cores
+// (tcgen05), and with more where the CTA-pair kernel would leave SMs idle: the linear layer
+// (BWD = false) and its gradient (BWD = true).
 //
 // Forward, one block = 128 weight rows (the MMA's M) x TN tokens (its N) over a range of k:
 //     y[t][r] = sum over groups G of  s[r][G] * ( sum over k in G of (u[r][k] - z[r][G]) x[t][k] )
@@ -7,15 +8,29 @@
 // of two tensor-memory buffers and drained into fp32 registers with one fused multiply-add by the
 // row's scale.  So weights are never rounded to 16 bits, and no sum on the tensor cores is longer
 // than 128 terms (their accumulation truncates; the registers' additions round to nearest).
-//   warp 0       TMA producer (one lane): packed codes (no swizzle) and activations (128-byte swizzle)
-//   warp 1       tensor-memory allocation and MMA issue (one lane)
-//   warps 2-9    unpack codes into the swizzled K-major operand tile (two threads per row)
-//   warps 10-17  drain: lane = weight row, each warp half of the tokens
-// Cost of a 128-column chunk at TN = 128: the MMAs take 512 cycles; unpacking issues about 16384 x 2
-// / 128 = 256 cycles of the four schedulers, the drain 128 and its tensor-memory loads: all
-// three overlap.  The blocks of a cluster split k when there are few tiles; their sums meet over
+//   warp 0        activations by TMA (128-byte swizzle)
+//   warp 3        codes by TMA (no swizzle)
+//   warp 1        tensor-memory allocation and MMA issue (one lane)
+//   warps 4-11    unpack codes into the swizzled operand tile: two groups of four warps, each its half
+//                 of every chunk
+//   warps 12-19   drain: lane = weight row, each warp half of the tokens
+// Operands move in steps of 64 along k through a ring deep enough to hide the hand-over between the
+// unpack warps and the MMA (about 2700 cycles there and back).  Cost of a 128-column chunk at TN =
+// 128: the MMAs take 512 cycles, unpacking about 320 of the integer pipes, the drain 128: all three
+// overlap.  The blocks of a cluster split k when there are few tiles; their sums meet over
 // distributed shared memory in a fixed order, in the epilogue that also adds the bias, applies the
-// activation and adds the residual: one launch, no workspace, deterministic.
+// activation and adds the residual: one launch, deterministic.
+//
+// Gradient: dX[t][perm[k]] = scale_t * sum over rows r of W16[r][k] * dz[t][r],
+//     W16 = fp16( fp32(u - z) * s ),   dz[t][r] = dY[t][r] act'(Z[t][r]) / scale_t  in fp16
+// The sum runs over the rows, across which the scale varies, so the weights enter as their fp16
+// values (the library's dequantized weight) and both operands are fp16 whatever the type of the
+// activations: bf16 operands would lose three more bits of each.  scale_t is a power of two per
+// token that puts the token's largest dY at 2^13 or above, so the range of bf16 gradients fits.
+// With fp16 activations and a smooth act' the rounding of dz would be as large as that of dX
+// itself: dz then comes as a sum of two fp16 values and the rows are gone through twice.  A block
+// owns 128 columns of W: its operand is read transposed (MN-major) straight from the row-wise
+// unpacked tile, and everything accumulates in one tensor-memory buffer.
 #pragma once
 
 #include "packed_decode.cuh"
@@ -24,22 +39,21 @@ namespace gptq {
 
 constexpr int TC_BM = 128;                    // weight rows of a block
 constexpr int TC_BK = 128;                    // columns of a chunk (two 64-column swizzle atoms)
-constexpr int TC_ATOM = TC_BM * 128;          // 16 KB: 128 rows x 64 sixteen-bit values
-constexpr int TC_A_BYTES = 2 * TC_ATOM;
-constexpr int TC_NA = 2;                      // unpacked tiles in flight
-constexpr int TC_THREADS = 18 * 32;
-constexpr int TC_SMEM_BUDGET = 224 * 1024;
+constexpr int TC_THREADS = 20 * 32;
 constexpr int TC_MAX_TN = 128;
+constexpr int TC_STEP_A = 128 * 128;          // an unpacked step: 128 x 64 values
+constexpr int TC_STEPS_MAX = 8;
+// Register split (setmaxnreg): 128 * (48 + 2 * 72 + 2 * 144) = 61440, what 640 threads of 96 start with.
+constexpr int TC_REGS_MISC = 48, TC_REGS_UNPACK = 72, TC_REGS_DRAIN = 144;
+static_assert(TC_REGS_MISC + 2 * TC_REGS_UNPACK + 2 * TC_REGS_DRAIN <= 5 * 96, "register split");
 
 __host__ __device__ constexpr int tc_code_bytes(int bits) { return TC_BM * TC_BK * bits / 8; }
-__host__ __device__ inline int tc_stage_bytes(int tn, int bits) { return tc_code_bytes(bits) + tn * 256; }
-__host__ __device__ inline int tc_stages(int tn, int bits) {
-  const int s = (TC_SMEM_BUDGET - 2048 - TC_NA * TC_A_BYTES) / tc_stage_bytes(tn, bits);
-  return s > 8 ? 8 : s;
+__host__ __device__ constexpr int tc_code_chunks(int bits) { return bits == 8 ? 2 : 3; }  // in flight
+__host__ __device__ constexpr int tc_steps(int tn) { return tn == 128 ? 6 : TC_STEPS_MAX; }  // in flight (even)
+__host__ __device__ constexpr int tc_smem_bytes(int tn, int bits) {
+  return 1024 + tc_steps(tn) * (TC_STEP_A + tn * 128) + tc_code_chunks(bits) * tc_code_bytes(bits) + 512;
 }
-__host__ __device__ inline int tc_smem_bytes(int tn, int bits) {
-  return 2048 + TC_NA * TC_A_BYTES + tc_stages(tn, bits) * tc_stage_bytes(tn, bits);
-}
+static_assert(tc_smem_bytes(128, 8) <= 227 * 1024 && tc_smem_bytes(128, 4) <= 227 * 1024, "shared memory");
 
 struct LinearTcArgs {
   int T, m, chunks, G, tn;
@@ -174,272 +188,6 @@ __device__ __forceinline__ void linear_epilogue4(const LinearTcArgs& p, int tok,
   }
 }
 
-template <int BITS, bool BF, int GU>
-__global__ void __launch_bounds__(TC_THREADS, 1)
-    linear_tc_kernel(const __grid_constant__ CUtensorMap codes_map, const __grid_constant__ CUtensorMap x_map,
-                     const LinearTcArgs p) {
-  constexpr int UNITS = 128 / GU;
-  extern __shared__ uint8_t tc_smem_raw[];
-  const uint32_t raw_s = smem_u32(tc_smem_raw);
-  uint8_t* smem = tc_smem_raw + (((raw_s + 1023u) & ~1023u) - raw_s);
-  const uint32_t sbase = smem_u32(smem);
-  const int tn = p.tn;
-  const int stages = tc_stages(tn, BITS);
-  const int stage_bytes = tc_stage_bytes(tn, BITS);
-  const uint32_t a_base = sbase;
-  const uint32_t st_base = sbase + TC_NA * TC_A_BYTES;  // stages: X atom 0 | X atom 1 | codes
-  const uint32_t bar = st_base + stages * stage_bytes;
-  const uint32_t bar_full = bar, bar_empty = bar + 64, bar_afull = bar + 128, bar_aempty = bar_afull + 8 * TC_NA,
-                 bar_tfull = bar_aempty + 8 * TC_NA, bar_tempty = bar_tfull + 16, bar_drain = bar_tempty + 16;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + (bar_drain + 8 - sbase));
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int cs = static_cast<int>(cluster_nctarank()), rank = static_cast<int>(cluster_ctarank());
-  const int m0 = static_cast<int>(blockIdx.x) / cs * TC_BM;
-  const int t0 = static_cast<int>(blockIdx.y) * tn;
-  const int kt0 = p.chunks * rank / cs, nk = p.chunks * (rank + 1) / cs - kt0;
-  const uint32_t tmem_cols = static_cast<uint32_t>(2 * tn);
-
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < stages; ++s) {
-      mbar_init(bar_full + 8 * s, 1);
-      mbar_init(bar_empty + 8 * s, 1);
-    }
-    for (int j = 0; j < TC_NA; ++j) {
-      mbar_init(bar_afull + 8 * j, 8);
-      mbar_init(bar_aempty + 8 * j, 1);
-    }
-    for (int j = 0; j < 2; ++j) {
-      mbar_init(bar_tfull + 8 * j, 1);
-      mbar_init(bar_tempty + 8 * j, 8);
-    }
-    mbar_init(bar_drain, 1);
-    *abort_flag = 0;
-    fence_mbar_init();
-  }
-  if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_slot), tmem_cols);
-    tmem_relinquish();
-  }
-  if (warp == 0 && lane == 0) {
-    tma_prefetch_desc(&codes_map);
-    tma_prefetch_desc(&x_map);
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem_base = *tmem_slot;
-  griddep_wait();
-  griddep_launch_dependents();
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) atomicExch(p.status, 0);
-
-  if (warp == 0) {
-    if (lane == 0) {
-      const uint32_t tx = static_cast<uint32_t>(stage_bytes);
-      int issued = 0;
-      for (int i = 0; i < nk; ++i) {
-        const int s = i % stages;
-        if (!mbar_wait_bounded(bar_empty + 8 * s, (static_cast<uint32_t>(i / stages) & 1u) ^ 1u, abort_flag)) break;
-        const uint32_t fb = bar_full + 8 * s, st = st_base + s * stage_bytes;
-        mbar_arrive_expect_tx(fb, tx);
-        const int kt = kt0 + i;
-        tma_load_2d(st + tn * 256, &codes_map, fb, kt * (TC_BK * BITS / 32), m0);
-        tma_load_2d(st, &x_map, fb, kt * TC_BK, t0);
-        tma_load_2d(st + tn * 128, &x_map, fb, kt * TC_BK + 64, t0);
-        issued = i + 1;
-      }
-      for (int i = max(0, issued - stages); i < issued; ++i)
-        mbar_wait_drain(bar_full + 8 * (i % stages), static_cast<uint32_t>(i / stages) & 1u);
-    }
-  } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t idesc = idesc_make(BF ? 1u : 0u, BF ? 1u : 0u, 0u, 0u, TC_BM, static_cast<uint32_t>(tn));
-      bool ok = true;
-      for (int i = 0; i < nk && ok; ++i) {
-        const int s = i % stages, j = i % TC_NA;
-        if (!mbar_wait_bounded(bar_full + 8 * s, static_cast<uint32_t>(i / stages) & 1u, abort_flag) ||
-            !mbar_wait_bounded(bar_afull + 8 * j, static_cast<uint32_t>(i / TC_NA) & 1u, abort_flag)) {
-          ok = false;
-          break;
-        }
-        const uint32_t a_t = a_base + j * TC_A_BYTES, x_t = st_base + s * stage_bytes;
-#pragma unroll
-        for (int u = 0; u < UNITS; ++u) {
-          const int uc = i * UNITS + u, b = uc & 1;
-          if (!mbar_wait_bounded(bar_tempty + 8 * b, (static_cast<uint32_t>(uc >> 1) & 1u) ^ 1u, abort_flag)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-#pragma unroll
-          for (int k = 0; k < GU / 16; ++k) {
-            const int kk = u * (GU / 16) + k;  // 16-column step of the chunk: atom kk / 4
-            const uint64_t ad = sdesc_sw128(a_t + (kk >> 2) * TC_ATOM + (kk & 3) * 32, 16, 1024);
-            const uint64_t bd = sdesc_sw128(x_t + (kk >> 2) * (tn * 128) + (kk & 3) * 32, 16, 1024);
-            umma_f16(tmem_base + static_cast<uint32_t>(b * tn), ad, bd, idesc, k > 0 ? 1u : 0u);
-          }
-          umma_commit(bar_tfull + 8 * b);
-        }
-        if (!ok) break;
-        umma_commit(bar_empty + 8 * s);
-        umma_commit(bar_aempty + 8 * j);
-      }
-      if (!ok) {  // MMAs may still be running: wait for them before tensor memory is released
-        umma_commit(bar_drain);
-        mbar_wait_drain(bar_drain, 0);
-      }
-    }
-  } else if (warp < 10) {
-    // ---------------- unpack: two threads per row ----------------
-    const int d = threadIdx.x - 64, r = d >> 1, h = d & 1, r7 = r & 7;
-    const int gr = m0 + r;
-    constexpr int ZN = GU == 32 ? 2 : 1;  // zero-points of a half row
-    const float* zrow = p.zeros + static_cast<size_t>(min(gr, p.m - 1)) * p.G;
-    auto load_z = [&](int kt, float (&z)[ZN]) {
-#pragma unroll
-      for (int j = 0; j < ZN; ++j)
-        z[j] = gr < p.m ? __ldg(zrow + group_of<GU>(p.gi, kt, GU == 128 ? 0 : GU == 64 ? h : 2 * h + j)) : 0.0f;
-    };
-    float nz[ZN];
-    load_z(kt0, nz);
-    for (int i = 0; i < nk; ++i) {
-      ZeroTerm zt[ZN];
-#pragma unroll
-      for (int j = 0; j < ZN; ++j) zt[j] = zero_term<BITS, BF>(nz[j]);
-      if (i + 1 < nk) load_z(kt0 + i + 1, nz);
-      const int s = i % stages, j = i % TC_NA;
-      if (!warp_wait(bar_full + 8 * s, static_cast<uint32_t>(i / stages) & 1u, abort_flag, lane) ||
-          !warp_wait(bar_aempty + 8 * j, (static_cast<uint32_t>(i / TC_NA) & 1u) ^ 1u, abort_flag, lane))
-        break;
-      uint32_t w[2 * BITS];
-      load_half_row<BITS>(smem + (st_base - sbase) + s * stage_bytes + tn * 256, r, h, w);
-      const uint32_t dst = a_base + j * TC_A_BYTES + h * TC_ATOM + r * 128;
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        uint32_t v, v1, q[4];
-        half_row_block<BITS>(w, c, v, v1);
-        unpack8<BITS, BF>(v, v1, zt[GU == 32 ? c >> 2 : 0], q);
-        // pairs (i, i + 4) -> columns in order
-        st_shared_v4(dst + ((c ^ r7) << 4), __byte_perm(q[0], q[1], 0x5410), __byte_perm(q[2], q[3], 0x5410),
-                     __byte_perm(q[0], q[1], 0x7632), __byte_perm(q[2], q[3], 0x7632));
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar_afull + 8 * j);
-    }
-  } else {
-    // ---------------- drain ----------------
-    const int qd = warp & 3, half = (warp - 10) >> 2;
-    const int row = qd * 32 + lane, gr = m0 + row;
-    const int cols = tn / 2;  // tokens of this warp: 16, 32 or 64
-    const float* srow = p.scales + static_cast<size_t>(min(gr, p.m - 1)) * p.G;
-    float acc[64];
-#pragma unroll
-    for (int j = 0; j < 64; ++j) acc[j] = 0.0f;
-    const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(qd * 32) << 16) + static_cast<uint32_t>(half * cols);
-    float ns = nk > 0 ? __ldg(srow + group_of<GU>(p.gi, kt0, 0)) : 0.0f;
-    bool ok = true;
-    for (int uc = 0; uc < nk * UNITS; ++uc) {
-      const float sc = ns;
-      if (uc + 1 < nk * UNITS) ns = __ldg(srow + group_of<GU>(p.gi, kt0 + (uc + 1) / UNITS, (uc + 1) % UNITS));
-      const int b = uc & 1;
-      if (!warp_wait(bar_tfull + 8 * b, static_cast<uint32_t>(uc >> 1) & 1u, abort_flag, lane)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-#pragma unroll
-      for (int cc = 0; cc < 4; ++cc) {
-        if (cc * 16 < cols) {
-          uint32_t v[16];
-          tmem_ld_32x32b_x16(lane_base + static_cast<uint32_t>(b * tn + cc * 16), v);
-          tmem_ld_wait();
-#pragma unroll
-          for (int j = 0; j < 16; ++j) acc[cc * 16 + j] = fmaf(sc, __uint_as_float(v[j]), acc[cc * 16 + j]);
-        }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar_tempty + 8 * b);
-    }
-    // sums as [token][row] over the operand tiles (every MMA that read them has completed)
-    if (ok) {
-      float* sums = reinterpret_cast<float*>(smem);
-#pragma unroll
-      for (int j = 0; j < 64; ++j)
-        if (j < cols) sums[(half * cols + j) * TC_BM + row] = acc[j];
-    }
-  }
-
-  __syncthreads();
-  if (cs > 1) cluster_sync();
-  // tokens rank, rank + cs, ... of the tile: a warp takes a token, a lane four rows
-  if (!*abort_flag) {
-    for (int t = rank + cs * warp; t < tn; t += cs * (TC_THREADS / 32)) {
-      if (t0 + t >= p.T || m0 + 4 * lane >= p.m) continue;
-      const uint32_t at = sbase + static_cast<uint32_t>((t * TC_BM + 4 * lane) * 4);
-      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      for (int o = 0; o < cs; ++o) {
-        const float4 w = cs > 1 ? ld_dsmem_f4(mapa_shared(at, o)) : *reinterpret_cast<const float4*>(smem + (at - sbase));
-        v.x += w.x;
-        v.y += w.y;
-        v.z += w.z;
-        v.w += w.w;
-      }
-      linear_epilogue4<BF>(p, t0 + t, m0 + 4 * lane, v);
-    }
-  }
-  if (cs > 1) cluster_sync();  // no block leaves while its sums may still be read
-  if (threadIdx.x == 0 && *abort_flag) atomicOr(p.status, ST_TIMEOUT);
-  if (warp == 1) {
-    tc_fence_after();
-    tmem_dealloc(tmem_base, tmem_cols);
-  }
-}
-
-// ------------------------------------------------------------------------------------------
-// the gradient
-// ------------------------------------------------------------------------------------------
-//     dX[t][perm[k]] = scale_t * sum over rows r of W16[r][k] * dz[t][r],
-//     W16 = fp16( fp32(u - z) * s ),   dz[t][r] = dY[t][r] act'(Z[t][r]) / scale_t  in fp16
-// The sum runs over the rows, across which the scale varies, so the weights enter as their fp16
-// values (the library's dequantized weight) and both operands are fp16 whatever the type of the
-// activations: bf16 operands would lose three more bits of each.  scale_t is a power of two per
-// token that puts the token's largest dY at 2^13 or above, so the range of bf16 gradients fits.
-// With fp16 activations and a smooth act' the rounding of dz would be as large as that of dX
-// itself: dz then comes as a sum of two fp16 values (parts = 2) and each chunk takes two MMAs.
-//
-// One block = 128 columns of W (the MMA's M; the operand is read transposed, MN-major, straight
-// from the row-wise unpacked tile) x TN tokens, over a range of rows in chunks of 128.  Everything
-// accumulates in one tensor-memory buffer.  Roles as in the forward kernel, without a drain loop.
-constexpr int BW_THREADS = 10 * 32;
-constexpr int BW_MAX_TN = 256;
-
-__host__ __device__ inline int bw_stage_bytes(int tn, int bits, int parts) {
-  return tc_code_bytes(bits) + parts * tn * 256;
-}
-__host__ __device__ inline int bw_stages(int tn, int bits, int parts) {
-  const int s = (TC_SMEM_BUDGET - 2048 - TC_NA * TC_A_BYTES) / bw_stage_bytes(tn, bits, parts);
-  return s > 8 ? 8 : s;
-}
-__host__ __device__ inline int bw_smem_bytes(int tn, int bits, int parts) {
-  return 2048 + TC_NA * TC_A_BYTES + bw_stages(tn, bits, parts) * bw_stage_bytes(tn, bits, parts);
-}
-
-struct LinearBwdArgs {
-  int T, m, n, G, tn, parts;
-  int row_chunks;  // ceil(m / 128)
-  GroupIndex gi;
-  const float *scales, *zeros;
-  const float* token_scale;  // [T] or null (1)
-  uint16_t* dX;              // [T x n], sweep order
-  int64_t lddx;
-  int bf16_out;
-  int vec;  // dX allows 8-byte accesses
-  int* status;
-};
-
 // Eight codes -> their fp16 weights, adjacent pairs in order.  f + nzm is u - z exactly (2^23 + u
 // minus 2^23 + z), times s rounded to nearest in fp32, then to nearest fp16.
 template <int BITS>
@@ -467,54 +215,88 @@ __device__ __forceinline__ void dequant8(uint32_t v, uint32_t v1, float2 nzm, fl
   }
 }
 
-template <int BITS, int GU>
-__global__ void __launch_bounds__(BW_THREADS, 1)
-    linear_bwd_tc_kernel(const __grid_constant__ CUtensorMap codes_map, const __grid_constant__ CUtensorMap dz_map,
-                         const __grid_constant__ CUtensorMap dzlo_map, const LinearBwdArgs p) {
+template <int REGS>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+template <int REGS>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+// Position in a ring of n stages.
+struct RingAt {
+  int s = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next(int n) {
+    if (++s == n) {
+      s = 0;
+      ph ^= 1u;
+    }
+  }
+};
+
+struct GradOut {
+  const float* token_scale;  // [T] or null (1)
+  uint16_t* dX;              // [T x n], sweep order
+  int64_t lddx;
+  int n, vec;  // vec: dX allows 8-byte accesses
+};
+
+// Forward: lin holds everything, `chunks` are 128-column chunks of k.  Gradient: lin holds T, m, G,
+// gi, scales, zeros, tn and status; `chunks` are 128-row chunks, gone through `parts` times (dz, then
+// its low part).
+template <int BITS, bool BF, int GU, bool BWD>
+__global__ void __launch_bounds__(TC_THREADS, 1)
+    packed_tc_kernel(const __grid_constant__ CUtensorMap codes_map, const __grid_constant__ CUtensorMap x_map,
+                     const __grid_constant__ CUtensorMap xlo_map, const LinearTcArgs p, const GradOut go,
+                     const int parts) {
+  constexpr int UNITS = 128 / GU, SC = tc_code_chunks(BITS), CODES = tc_code_bytes(BITS);
   extern __shared__ uint8_t tc_smem_raw[];
   const uint32_t raw_s = smem_u32(tc_smem_raw);
   uint8_t* smem = tc_smem_raw + (((raw_s + 1023u) & ~1023u) - raw_s);
   const uint32_t sbase = smem_u32(smem);
-  const int tn = p.tn, parts = p.parts;
-  const int stages = bw_stages(tn, BITS, parts);
-  const int stage_bytes = bw_stage_bytes(tn, BITS, parts);
-  const uint32_t a_base = sbase;
-  const uint32_t st_base = sbase + TC_NA * TC_A_BYTES;  // stages: dz atoms | (low part's atoms) | codes
-  const int code_off = parts * tn * 256;
-  const uint32_t bar = st_base + stages * stage_bytes;
-  const uint32_t bar_full = bar, bar_empty = bar + 64, bar_afull = bar + 128, bar_aempty = bar_afull + 8 * TC_NA,
-                 bar_acc = bar_aempty + 8 * TC_NA, bar_drain = bar_acc + 8;
+  const int tn = p.tn, NS = tc_steps(tn), xb = tn * 128;
+  const uint32_t a_base = sbase, x_base = a_base + NS * TC_STEP_A, c_base = x_base + NS * xb,
+                 bar_full = c_base + SC * CODES, bar_empty = bar_full + 8 * TC_STEPS_MAX,
+                 bar_cfull = bar_empty + 8 * TC_STEPS_MAX, bar_cempty = bar_cfull + 8 * SC, bar_tfull = bar_cempty + 8 * SC,
+                 bar_tempty = bar_tfull + 16, bar_drain = bar_tempty + 16;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + (bar_drain + 8 - sbase));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cs = static_cast<int>(cluster_nctarank()), rank = static_cast<int>(cluster_ctarank());
-  const int kc = static_cast<int>(blockIdx.x) / cs;  // chunk of 128 columns
+  const int mt = static_cast<int>(blockIdx.x) / cs;  // tile of 128 rows of W, or of 128 columns (gradient)
   const int t0 = static_cast<int>(blockIdx.y) * tn;
-  const int rc0 = static_cast<int>(static_cast<int64_t>(p.row_chunks) * rank / cs);
-  const int nk = static_cast<int>(static_cast<int64_t>(p.row_chunks) * (rank + 1) / cs) - rc0;
+  // this block's part of the reduction, in chunks; the gradient's second part follows the first
+  const int ch0 = static_cast<int>(static_cast<int64_t>(p.chunks) * rank / cs);
+  const int nch = static_cast<int>(static_cast<int64_t>(p.chunks) * (rank + 1) / cs) - ch0;
+  const int nk = nch * parts;
+  const uint32_t tmem_cols = static_cast<uint32_t>(2 * tn);
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < stages; ++s) {
-      mbar_init(bar_full + 8 * s, 1);
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(bar_full + 8 * s, 5);  // the activations and a group of unpack warps
       mbar_init(bar_empty + 8 * s, 1);
     }
-    for (int j = 0; j < TC_NA; ++j) {
-      mbar_init(bar_afull + 8 * j, 8);
-      mbar_init(bar_aempty + 8 * j, 1);
+    for (int s = 0; s < SC; ++s) {
+      mbar_init(bar_cfull + 8 * s, 1);
+      mbar_init(bar_cempty + 8 * s, 8);
     }
-    mbar_init(bar_acc, 1);
+    for (int j = 0; j < 2; ++j) {
+      mbar_init(bar_tfull + 8 * j, 1);
+      mbar_init(bar_tempty + 8 * j, 8);
+    }
     mbar_init(bar_drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_slot), static_cast<uint32_t>(tn));
+    tmem_alloc(smem_u32(tmem_slot), tmem_cols);
     tmem_relinquish();
   }
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&codes_map);
-    tma_prefetch_desc(&dz_map);
+    tma_prefetch_desc(&x_map);
   }
   tc_fence_before();
   __syncthreads();
@@ -524,129 +306,209 @@ __global__ void __launch_bounds__(BW_THREADS, 1)
   griddep_launch_dependents();
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) atomicExch(p.status, 0);
 
-  if (warp == 0) {
-    if (lane == 0) {
+  if (warp < 4) {
+    regs_dec<TC_REGS_MISC>();
+    if (warp == 0 && lane == 0) {
+      // ---------------- activations ----------------
+      RingAt r;
+      int issued = 0;
+      for (int i = 0; i < 2 * nk; ++i) {
+        if (!mbar_wait_bounded(bar_empty + 8 * r.s, r.ph ^ 1u, abort_flag)) break;
+        const bool low = BWD && i >= 2 * nch;
+        mbar_arrive_expect_tx(bar_full + 8 * r.s, static_cast<uint32_t>(xb));
+        tma_load_2d(x_base + r.s * xb, low ? &xlo_map : &x_map, bar_full + 8 * r.s,
+                    ch0 * 128 + (low ? i - 2 * nch : i) * 64, t0);
+        r.next(NS);
+        ++issued;
+      }
+      for (int i = max(0, issued - NS); i < issued; ++i)
+        mbar_wait_drain(bar_full + 8 * (i % NS), static_cast<uint32_t>(i / NS) & 1u);
+    } else if (warp == 3 && lane == 0) {
+      // ---------------- codes ----------------
+      RingAt r;
       int issued = 0;
       for (int i = 0; i < nk; ++i) {
-        const int s = i % stages;
-        if (!mbar_wait_bounded(bar_empty + 8 * s, (static_cast<uint32_t>(i / stages) & 1u) ^ 1u, abort_flag)) break;
-        const uint32_t fb = bar_full + 8 * s, st = st_base + s * stage_bytes;
-        mbar_arrive_expect_tx(fb, static_cast<uint32_t>(stage_bytes));
-        const int r0 = (rc0 + i) * 128;
-        tma_load_2d(st + code_off, &codes_map, fb, kc * (TC_BK * BITS / 32), r0);
-        tma_load_2d(st, &dz_map, fb, r0, t0);
-        tma_load_2d(st + tn * 128, &dz_map, fb, r0 + 64, t0);
-        if (parts == 2) {
-          tma_load_2d(st + tn * 256, &dzlo_map, fb, r0, t0);
-          tma_load_2d(st + tn * 384, &dzlo_map, fb, r0 + 64, t0);
-        }
-        issued = i + 1;
+        if (!mbar_wait_bounded(bar_cempty + 8 * r.s, r.ph ^ 1u, abort_flag)) break;
+        const int c = ch0 + (BWD && i >= nch ? i - nch : i);
+        mbar_arrive_expect_tx(bar_cfull + 8 * r.s, CODES);
+        tma_load_2d(c_base + r.s * CODES, &codes_map, bar_cfull + 8 * r.s, (BWD ? mt : c) * (4 * BITS),
+                    (BWD ? c : mt) * 128);
+        r.next(SC);
+        ++issued;
       }
-      for (int i = max(0, issued - stages); i < issued; ++i)
-        mbar_wait_drain(bar_full + 8 * (i % stages), static_cast<uint32_t>(i / stages) & 1u);
-    }
-  } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t idesc = idesc_make(0u, 0u, 1u, 0u, TC_BM, static_cast<uint32_t>(tn));  // f16; A is MN-major
+      for (int i = max(0, issued - SC); i < issued; ++i)
+        mbar_wait_drain(bar_cfull + 8 * (i % SC), static_cast<uint32_t>(i / SC) & 1u);
+    } else if (warp == 1 && lane == 0) {
+      // ---------------- MMA ----------------
+      const uint32_t fmt = (BF && !BWD) ? 1u : 0u;
+      const uint32_t idesc = idesc_make(fmt, fmt, BWD ? 1u : 0u, 0u, TC_BM, static_cast<uint32_t>(tn));
+      // forward: K-major; gradient: MN-major, 16 rows = two 8-row atoms, 64-column halves 8 KB apart
+      const uint64_t ad0 = BWD ? sdesc_sw128(a_base, TC_STEP_A / 2, 1024) : sdesc_sw128(a_base, 16, 1024);
+      const uint64_t bd0 = sdesc_sw128(x_base, 16, 1024);
+      constexpr uint32_t A_SLICE = (BWD ? 2048 : 32) >> 4, B_SLICE = 32 >> 4;
+      constexpr int SUB = (!BWD && GU == 32) ? 2 : 1;  // accumulation units of a step
+      RingAt x, t;
       bool ok = true;
-      for (int i = 0; i < nk; ++i) {
-        const int s = i % stages, j = i % TC_NA;
-        if (!mbar_wait_bounded(bar_full + 8 * s, static_cast<uint32_t>(i / stages) & 1u, abort_flag) ||
-            !mbar_wait_bounded(bar_afull + 8 * j, static_cast<uint32_t>(i / TC_NA) & 1u, abort_flag)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t a_t = a_base + j * TC_A_BYTES, x_t = st_base + s * stage_bytes;
-        for (int part = 0; part < parts; ++part) {
+      for (int i = 0; i < nk && ok; ++i) {
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            // 16 rows = two 8-row swizzle atoms of 1024 bytes; the 64-column halves 16 KB apart
-            const uint64_t ad = sdesc_sw128(a_t + kk * 2048, TC_ATOM, 1024);
-            const uint64_t bd = sdesc_sw128(x_t + part * (tn * 256) + (kk >> 2) * (tn * 128) + (kk & 3) * 32, 16, 1024);
-            umma_f16(tmem_base, ad, bd, idesc, (i > 0 || part > 0 || kk > 0) ? 1u : 0u);
+        for (int h = 0; h < 2; ++h) {
+          if (!mbar_wait_bounded(bar_full + 8 * x.s, x.ph, abort_flag)) {
+            ok = false;
+            break;
           }
+          const uint64_t ad = ad0 + static_cast<uint32_t>(x.s * (TC_STEP_A >> 4)),
+                         bd = bd0 + static_cast<uint32_t>(x.s * (xb >> 4));
+#pragma unroll
+          for (int u = 0; u < SUB; ++u) {
+            const bool first = BWD ? (h == 0 && i == 0) : (GU < 128 || h == 0);
+            const bool last = BWD ? (h == 1 && i == nk - 1) : (GU < 128 || h == 1);
+            if (first && !mbar_wait_bounded(bar_tempty + 8 * t.s, t.ph ^ 1u, abort_flag)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t d = tmem_base + static_cast<uint32_t>(t.s * tn);
+#pragma unroll
+            for (int k = 0; k < 4 / SUB; ++k) {
+              const uint32_t kk = u * (4 / SUB) + k;
+              umma_f16(d, ad + kk * A_SLICE, bd + kk * B_SLICE, idesc, (first && k == 0) ? 0u : 1u);
+            }
+            if (u == SUB - 1) umma_commit(bar_empty + 8 * x.s);
+            if (last) {
+              umma_commit(bar_tfull + 8 * t.s);
+              t.next(2);
+            }
+          }
+          if (!ok) break;
+          x.next(NS);
         }
-        umma_commit(bar_empty + 8 * s);
-        umma_commit(bar_aempty + 8 * j);
       }
-      if (ok) {
-        umma_commit(bar_acc);
-      } else {
+      if (!ok) {  // MMAs may still be running: wait for them before tensor memory is released
         umma_commit(bar_drain);
         mbar_wait_drain(bar_drain, 0);
       }
     }
-  } else {
-    // ---------------- unpack: two threads per row of W, 64 columns each ----------------
-    const int d = threadIdx.x - 64, r = d >> 1, h = d & 1, r7 = r & 7;
-    constexpr int ZN = GU == 32 ? 2 : 1;
-    auto load_sz = [&](int rc, float (&s)[ZN], float (&z)[ZN]) {
-      const int gr = rc * 128 + r;
+  } else if (warp < 12) {
+    // ---------------- unpack ----------------
+    // Forward: group 0 takes columns 0-63 of every chunk, group 1 columns 64-127, a thread one row.
+    // Gradient: group 0 takes rows 0-63 of every chunk, group 1 rows 64-127, two threads per row.
+    regs_dec<TC_REGS_UNPACK>();
+    const int d = threadIdx.x & 127, grp = (warp - 4) >> 2;
+    const int r = BWD ? grp * 64 + (d >> 1) : d, h = BWD ? d & 1 : grp, r7 = r & 7;
+    const uint32_t dst0 = a_base + (BWD ? h * (TC_STEP_A / 2) + (r & 63) * 128 : r * 128);
+    constexpr int ZN = GU == 32 ? 2 : 1;  // groups of a half row
+    float ns[ZN], nz[ZN];
+    auto load_sz = [&](int i) {
+      const int c = ch0 + (BWD && i >= nch ? i - nch : i);
+      const int gr = (BWD ? c : mt) * 128 + r;
+      const bool in = gr < p.m;
+      const size_t row = static_cast<size_t>(min(gr, p.m - 1)) * p.G;
 #pragma unroll
       for (int j = 0; j < ZN; ++j) {
-        const size_t at = static_cast<size_t>(min(gr, p.m - 1)) * p.G +
-                          group_of<GU>(p.gi, kc, GU == 128 ? 0 : GU == 64 ? h : 2 * h + j);
-        s[j] = gr < p.m ? __ldg(p.scales + at) : 0.0f;  // rows past m: zero weights
-        z[j] = gr < p.m ? __ldg(p.zeros + at) : 0.0f;
+        const size_t at = row + group_of<GU>(p.gi, BWD ? mt : c, GU == 128 ? 0 : GU == 64 ? h : 2 * h + j);
+        nz[j] = in ? __ldg(p.zeros + at) : 0.0f;
+        if (BWD) ns[j] = in ? __ldg(p.scales + at) : 0.0f;  // rows past m: zero weights
       }
     };
-    float ns[ZN], nz[ZN];
-    if (nk > 0) load_sz(rc0, ns, nz);
-    bool ok = true;
+    RingAt c;
+    int as = grp;  // slot of this group's next step
+    uint32_t aph = 0;
+    if (nk > 0) load_sz(0);
     for (int i = 0; i < nk; ++i) {
-      float2 ss[ZN], nzm[ZN];
+      float cs_[ZN], cz[ZN];
 #pragma unroll
       for (int j = 0; j < ZN; ++j) {
-        ss[j] = make_float2(ns[j], ns[j]);
-        nzm[j] = make_float2(-8388608.0f - nz[j], -8388608.0f - nz[j]);
+        cz[j] = nz[j];
+        cs_[j] = BWD ? ns[j] : 0.0f;
       }
-      if (i + 1 < nk) load_sz(rc0 + i + 1, ns, nz);
-      const int s = i % stages, j = i % TC_NA;
-      if (!warp_wait(bar_full + 8 * s, static_cast<uint32_t>(i / stages) & 1u, abort_flag, lane) ||
-          !warp_wait(bar_aempty + 8 * j, (static_cast<uint32_t>(i / TC_NA) & 1u) ^ 1u, abort_flag, lane)) {
-        ok = false;
+      if (i + 1 < nk) load_sz(i + 1);
+      if (!warp_wait(bar_cfull + 8 * c.s, c.ph, abort_flag, lane) ||
+          !warp_wait(bar_empty + 8 * as, aph ^ 1u, abort_flag, lane))
         break;
-      }
       uint32_t w[2 * BITS];
-      load_half_row<BITS>(smem + (st_base - sbase) + s * stage_bytes + code_off, r, h, w);
-      const uint32_t dst = a_base + j * TC_A_BYTES + h * TC_ATOM + r * 128;
+      load_half_row<BITS>(smem + (c_base - sbase) + c.s * CODES, r, h, w);
+      const uint32_t dst = dst0 + as * TC_STEP_A;
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
+      for (int b = 0; b < 8; ++b) {
+        const int j = GU == 32 ? b >> 2 : 0;
         uint32_t v, v1, q[4];
-        half_row_block<BITS>(w, c, v, v1);
-        dequant8<BITS>(v, v1, nzm[GU == 32 ? c >> 2 : 0], ss[GU == 32 ? c >> 2 : 0], q);
-        st_shared_v4(dst + ((c ^ r7) << 4), q[0], q[1], q[2], q[3]);
+        half_row_block<BITS>(w, b, v, v1);
+        if (BWD) {
+          dequant8<BITS>(v, v1, make_float2(-8388608.0f - cz[j], -8388608.0f - cz[j]), make_float2(cs_[j], cs_[j]), q);
+          st_shared_v4(dst + ((b ^ r7) << 4), q[0], q[1], q[2], q[3]);
+        } else {
+          unpack8<BITS, BF>(v, v1, zero_term<BITS, BF>(cz[j]), q);
+          // pairs (i, i + 4) -> columns in order
+          st_shared_v4(dst + ((b ^ r7) << 4), __byte_perm(q[0], q[1], 0x5410), __byte_perm(q[2], q[3], 0x5410),
+                       __byte_perm(q[0], q[1], 0x7632), __byte_perm(q[2], q[3], 0x7632));
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar_afull + 8 * j);
+      if (lane == 0) {
+        mbar_arrive(bar_cempty + 8 * c.s);
+        mbar_arrive(bar_full + 8 * as);
+      }
+      c.next(SC);
+      as += 2;
+      if (as >= NS) {
+        as = grp;
+        aph ^= 1u;
+      }
     }
-    // accumulator -> [token][column] sums over the operand tiles
-    if (ok && nk > 0) ok = warp_wait(bar_acc, 0u, abort_flag, lane);
-    if (ok) {
-      tc_fence_after();
-      const int qd = warp & 3, half = (warp - 2) >> 2, col = qd * 32 + lane;
-      float* sums = reinterpret_cast<float*>(smem);
-      for (int cc = half; cc < tn / 16; cc += 2) {
-        uint32_t v[16];
-        if (nk > 0) {
-          tmem_ld_32x32b_x16(tmem_base + (static_cast<uint32_t>(qd * 32) << 16) + static_cast<uint32_t>(cc * 16), v);
-          tmem_ld_wait();
-        }
+  } else {
+    // ---------------- drain ----------------
+    regs_inc<TC_REGS_DRAIN>();
+    const int qd = warp & 3, half = (warp - 12) >> 2;
+    const int row = qd * 32 + lane, cols = tn / 2;  // tokens of this warp: 16, 32 or 64
+    const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(qd * 32) << 16) + static_cast<uint32_t>(half * cols);
+    float acc[64];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) sums[(cc * 16 + j) * TC_BM + col] = nk > 0 ? __uint_as_float(v[j]) : 0.0f;
+    for (int j = 0; j < 64; ++j) acc[j] = 0.0f;
+    bool ok = true;
+    RingAt t;
+    const int units = BWD ? (nk > 0 ? 1 : 0) : nk * UNITS;
+    const float* srow = p.scales + static_cast<size_t>(BWD ? 0 : min(mt * TC_BM + row, p.m - 1)) * p.G;
+    float ns = !BWD && units > 0 ? __ldg(srow + group_of<GU>(p.gi, ch0, 0)) : 1.0f;
+    for (int uc = 0; uc < units; ++uc) {
+      const float sc = ns;
+      if (!BWD && uc + 1 < units) ns = __ldg(srow + group_of<GU>(p.gi, ch0 + (uc + 1) / UNITS, (uc + 1) % UNITS));
+      if (!warp_wait(bar_tfull + 8 * t.s, t.ph, abort_flag, lane)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+#pragma unroll
+      for (int cc = 0; cc < 4; ++cc) {
+        if (cc * 16 < cols) {
+          uint32_t v[16];
+          tmem_ld_32x32b_x16(lane_base + static_cast<uint32_t>(t.s * tn + cc * 16), v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) acc[cc * 16 + j] = fmaf(sc, __uint_as_float(v[j]), acc[cc * 16 + j]);
+        }
       }
       tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_tempty + 8 * t.s);
+      t.next(2);
+    }
+    // sums as [token][row] over the operand ring (every MMA that read it has completed)
+    if (ok) {
+      float* sums = reinterpret_cast<float*>(smem);
+#pragma unroll
+      for (int j = 0; j < 64; ++j)
+        if (j < cols) sums[(half * cols + j) * TC_BM + row] = acc[j];
     }
   }
 
   __syncthreads();
   if (cs > 1) cluster_sync();
+  // tokens rank, rank + cs, ... of the tile: a warp takes a token, a lane four rows (columns of dX)
   if (!*abort_flag) {
-    for (int t = rank + cs * warp; t < tn; t += cs * (BW_THREADS / 32)) {
-      const int tok = t0 + t;
-      if (tok >= p.T) continue;
+    for (int t = rank + cs * warp; t < tn; t += cs * (TC_THREADS / 32)) {
+      const int tok = t0 + t, row = mt * TC_BM + 4 * lane;
+      if (tok >= p.T || (!BWD && row >= p.m)) continue;
       const uint32_t at = sbase + static_cast<uint32_t>((t * TC_BM + 4 * lane) * 4);
       float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       for (int o = 0; o < cs; ++o) {
@@ -656,31 +518,28 @@ __global__ void __launch_bounds__(BW_THREADS, 1)
         v.z += w.z;
         v.w += w.w;
       }
-      if (p.token_scale) {
-        const float s = p.token_scale[tok];
-        v.x *= s;
-        v.y *= s;
-        v.z *= s;
-        v.w *= s;
-      }
-      uint16_t* d = p.dX + static_cast<size_t>(tok) * p.lddx + kc * 128 + 4 * lane;
-      const uint32_t lo = p.bf16_out ? pack2<true>(v.x, v.y) : pack2<false>(v.x, v.y);
-      const uint32_t hi = p.bf16_out ? pack2<true>(v.z, v.w) : pack2<false>(v.z, v.w);
-      if (p.vec) {
-        *reinterpret_cast<uint2*>(d) = make_uint2(lo, hi);
+      if (BWD) {
+        const float s = go.token_scale ? go.token_scale[tok] : 1.0f;
+        uint16_t* o = go.dX + static_cast<size_t>(tok) * go.lddx + row;
+        const uint32_t lo = pack2<BF>(v.x * s, v.y * s), hi = pack2<BF>(v.z * s, v.w * s);
+        if (go.vec) {
+          *reinterpret_cast<uint2*>(o) = make_uint2(lo, hi);
+        } else {
+          o[0] = static_cast<uint16_t>(lo);
+          o[1] = static_cast<uint16_t>(lo >> 16);
+          o[2] = static_cast<uint16_t>(hi);
+          o[3] = static_cast<uint16_t>(hi >> 16);
+        }
       } else {
-        d[0] = static_cast<uint16_t>(lo);
-        d[1] = static_cast<uint16_t>(lo >> 16);
-        d[2] = static_cast<uint16_t>(hi);
-        d[3] = static_cast<uint16_t>(hi >> 16);
+        linear_epilogue4<BF>(p, tok, row, v);
       }
     }
   }
-  if (cs > 1) cluster_sync();
+  if (cs > 1) cluster_sync();  // no block leaves while its sums may still be read
   if (threadIdx.x == 0 && *abort_flag) atomicOr(p.status, ST_TIMEOUT);
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, static_cast<uint32_t>(tn));
+    tmem_dealloc(tmem_base, tmem_cols);
   }
 }
 
@@ -697,9 +556,7 @@ struct TcLaunch {
 };
 
 template <int BITS>
-cudaError_t launch_linear_tc(const TcLaunch& l, const CUtensorMap& codes, const CUtensorMap& x, const LinearTcArgs& a);
-template <int BITS>
-cudaError_t launch_linear_bwd_tc(const TcLaunch& l, const CUtensorMap& codes, const CUtensorMap& dz,
-                                 const CUtensorMap& dz_lo, const LinearBwdArgs& a);
+cudaError_t launch_packed_tc(const TcLaunch& l, bool backward, const CUtensorMap& codes, const CUtensorMap& x,
+                             const CUtensorMap& xlo, const LinearTcArgs& a, const GradOut& go, int parts);
 
 }  // namespace gptq
