@@ -32,8 +32,8 @@ constexpr int PR_TN = 256;                     // tokens of a tile
 constexpr int PR_A_BYTES = 128 * 128;          // an unpacked step: 128 x 64 values
 constexpr int PR_X_BYTES = 128 * 128;          // a block's half of a step's activations: 128 tokens x 64 values
 constexpr int PR_EPI_BYTES = 8 * 1024;         // per drain warp: 8 tokens x 32 rows of sums
-// Register split (setmaxnreg): 128 * (32 + 2 * 56 + 2 * 168) = 61440, what 640 threads of 96 start with.
-constexpr int PR_REGS_MISC = 32, PR_REGS_UNPACK = 56, PR_REGS_DRAIN = 168;
+// Register split (setmaxnreg): 128 * (32 + 2 * 48 + 2 * 176) = 61440, what 640 threads of 96 start with.
+constexpr int PR_REGS_MISC = 32, PR_REGS_UNPACK = 48, PR_REGS_DRAIN = 176;
 static_assert(PR_REGS_MISC + 2 * PR_REGS_UNPACK + 2 * PR_REGS_DRAIN <= 5 * 96, "register split");
 
 __host__ __device__ constexpr int pr_steps(int bits) { return bits == 8 ? 4 : 6; }  // steps in flight (even)
@@ -412,12 +412,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PR_THREADS, 1)
           tc_fence_after();
           const uint32_t at = lane_base + static_cast<uint32_t>(t.s * PR_TN);
 #pragma unroll
-          for (int cc = 0; cc < 8; ++cc) {
-            uint32_t v[16];
-            tmem_ld_32x32b_x16(at + cc * 16, v);
+          for (int cc = 0; cc < 4; ++cc) {
+            uint32_t v[32];
+            tmem_ld_32x32b_x32(at + cc * 32, v);
             tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 16; ++j) acc[cc * 16 + j] = fmaf(sc, __uint_as_float(v[j]), acc[cc * 16 + j]);
+            for (int j = 0; j < 32; ++j) acc[cc * 32 + j] = fmaf(sc, __uint_as_float(v[j]), acc[cc * 32 + j]);
           }
           tc_fence_before();
           __syncwarp();

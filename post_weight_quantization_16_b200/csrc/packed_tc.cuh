@@ -43,8 +43,8 @@ constexpr int TC_THREADS = 20 * 32;
 constexpr int TC_MAX_TN = 128;
 constexpr int TC_STEP_A = 128 * 128;          // an unpacked step: 128 x 64 values
 constexpr int TC_STEPS_MAX = 8;
-// Register split (setmaxnreg): 128 * (48 + 2 * 72 + 2 * 144) = 61440, what 640 threads of 96 start with.
-constexpr int TC_REGS_MISC = 48, TC_REGS_UNPACK = 72, TC_REGS_DRAIN = 144;
+// Register split (setmaxnreg): 128 * (40 + 2 * 64 + 2 * 152) = 60416 of the 61440 that 640 threads of 96 start with.
+constexpr int TC_REGS_MISC = 40, TC_REGS_UNPACK = 64, TC_REGS_DRAIN = 152;
 static_assert(TC_REGS_MISC + 2 * TC_REGS_UNPACK + 2 * TC_REGS_DRAIN <= 5 * 96, "register split");
 
 __host__ __device__ constexpr int tc_code_bytes(int bits) { return TC_BM * TC_BK * bits / 8; }
@@ -478,16 +478,18 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         break;
       }
       tc_fence_after();
+      // (all loads, then one wait: a load takes some 200 cycles while the MMAs run)
+      uint32_t v[4][16];
 #pragma unroll
-      for (int cc = 0; cc < 4; ++cc) {
+      for (int cc = 0; cc < 4; ++cc)
+        if (cc * 16 < cols) tmem_ld_32x32b_x16(lane_base + static_cast<uint32_t>(t.s * tn + cc * 16), v[cc]);
+      tmem_ld_wait();
+#pragma unroll
+      for (int cc = 0; cc < 4; ++cc)
         if (cc * 16 < cols) {
-          uint32_t v[16];
-          tmem_ld_32x32b_x16(lane_base + static_cast<uint32_t>(t.s * tn + cc * 16), v);
-          tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < 16; ++j) acc[cc * 16 + j] = fmaf(sc, __uint_as_float(v[j]), acc[cc * 16 + j]);
+          for (int j = 0; j < 16; ++j) acc[cc * 16 + j] = fmaf(sc, __uint_as_float(v[cc][j]), acc[cc * 16 + j]);
         }
-      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_tempty + 8 * t.s);
