@@ -135,6 +135,22 @@ __device__ __forceinline__ bool warp_wait_uniform(uint32_t bar, uint32_t parity,
   }
 }
 
+// (for barriers that a peer block arrives on)
+__device__ __forceinline__ bool warp_wait_uniform_cl(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  if (__all_sync(0xffffffffu, mbar_try_wait_cl(bar, parity))) return true;
+  uint64_t t0 = 0;
+  for (uint32_t i = 1;; ++i) {
+    if (__all_sync(0xffffffffu, mbar_try_wait_cl(bar, parity))) return true;
+    if ((i & 255u) == 0) {
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      const bool late = now - t0 > kWaitLimitNs;
+      if (__any_sync(0xffffffffu, late)) *abort_flag = 1;
+      if (__any_sync(0xffffffffu, late || *abort_flag)) return false;
+    }
+  }
+}
+
 template <bool BF>
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                           uint32_t b0, uint32_t b1) {

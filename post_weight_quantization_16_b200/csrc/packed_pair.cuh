@@ -93,7 +93,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PR_THREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + (bar_drain + 8 - sbase));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (a shuffled warp index is known to be uniform: operands of the MMAs stay in uniform registers)
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
   const int cluster = static_cast<int>(blockIdx.x >> 1), clusters = static_cast<int>(gridDim.x >> 1);
@@ -183,11 +184,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PR_THREADS, 1)
       }
       for (int i = max(0, issued - SC); i < issued; ++i)
         mbar_wait_drain(bar_cfull + 8 * (i % SC), static_cast<uint32_t>(i / SC) & 1u);
-    } else if (warp == 1 && lane == 0 && leader) {
-      // ---------------- MMA for the pair ----------------
+    } else if (warp == 1 && leader) {
+      // ---------------- MMA for the pair: the whole warp runs the loop, one lane issues ----------------
+      const bool issue = elect_one_sync();
       const uint32_t fmt = (BF && !BWD) ? 1u : 0u;
       const uint32_t idesc = idesc_make(fmt, fmt, BWD ? 1u : 0u, 0u, 256, PR_TN);
-      // This thread shares its scheduler with unpack and drain warps, so its instructions are few:
+      // This warp shares its scheduler with unpack and drain warps, so its instructions are few:
       // descriptors are those of step 0 plus the slot's and the 16-wide slice's offsets.
       // Forward: K-major; gradient: MN-major, 16 rows = two 8-row atoms, 64-column halves 8 KB apart.
       const uint64_t ad0 = BWD ? sdesc_sw128(a_base, PR_A_BYTES / 2, 1024) : sdesc_sw128(a_base, 16, 1024);
@@ -201,7 +203,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PR_THREADS, 1)
         for (int i = 0; i < p.steps && ok; ++i) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            if (!mbar_wait_bounded_cl(bar_full + 8 * x.s, x.ph, abort_flag)) {
+            if (!warp_wait_uniform_cl(bar_full + 8 * x.s, x.ph, abort_flag)) {
               ok = false;
               break;
             }
@@ -212,7 +214,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PR_THREADS, 1)
               // a unit starts and ends with this step's MMAs: gradient, the whole tile is one unit
               const bool first = BWD ? (h == 0 && i == 0) : (GU < 128 || h == 0);
               const bool last = BWD ? (h == 1 && i == p.steps - 1) : (GU < 128 || h == 1);
-              if (first && !mbar_wait_bounded_cl(bar_tempty + 8 * t.s, t.ph ^ 1u, abort_flag)) {
+              if (first && !warp_wait_uniform_cl(bar_tempty + 8 * t.s, t.ph ^ 1u, abort_flag)) {
                 ok = false;
                 break;
               }
@@ -221,11 +223,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PR_THREADS, 1)
 #pragma unroll
               for (int k = 0; k < 4 / SUB; ++k) {
                 const uint32_t kk = u * (4 / SUB) + k;
-                umma_f16_pair(d, ad + kk * A_SLICE, bd + kk * B_SLICE, idesc, (first && k == 0) ? 0u : 1u);
+                if (issue) umma_f16_pair(d, ad + kk * A_SLICE, bd + kk * B_SLICE, idesc, (first && k == 0) ? 0u : 1u);
               }
-              if (u == SUB - 1) umma_commit_pair_mc(bar_empty + 8 * x.s, 0x3);
+              if (u == SUB - 1 && issue) umma_commit_pair_mc(bar_empty + 8 * x.s, 0x3);
               if (last) {
-                umma_commit_pair_mc(bar_tfull + 8 * t.s, 0x3);
+                if (issue) umma_commit_pair_mc(bar_tfull + 8 * t.s, 0x3);
                 t.next();
               }
             }
@@ -235,7 +237,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PR_THREADS, 1)
         }
       }
       if (!ok) {  // MMAs may still be running: wait for them before tensor memory is released
-        umma_commit_pair(bar_drain);
+        if (issue) umma_commit_pair(bar_drain);
         mbar_wait_drain(bar_drain, 0);
       }
     }

@@ -263,7 +263,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + (bar_drain + 8 - sbase));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (a shuffled warp index is known to be uniform: operands of the MMAs stay in uniform registers)
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int cs = static_cast<int>(cluster_nctarank()), rank = static_cast<int>(cluster_ctarank());
   const int mt = static_cast<int>(blockIdx.x) / cs;  // tile of 128 rows of W, or of 128 columns (gradient)
   const int t0 = static_cast<int>(blockIdx.y) * tn;
@@ -338,8 +339,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       }
       for (int i = max(0, issued - SC); i < issued; ++i)
         mbar_wait_drain(bar_cfull + 8 * (i % SC), static_cast<uint32_t>(i / SC) & 1u);
-    } else if (warp == 1 && lane == 0) {
-      // ---------------- MMA ----------------
+    } else if (warp == 1) {
+      // ---------------- MMA: the whole warp runs the loop, one lane issues ----------------
+      const bool issue = elect_one_sync();
       const uint32_t fmt = (BF && !BWD) ? 1u : 0u;
       const uint32_t idesc = idesc_make(fmt, fmt, BWD ? 1u : 0u, 0u, TC_BM, static_cast<uint32_t>(tn));
       // forward: K-major; gradient: MN-major, 16 rows = two 8-row atoms, 64-column halves 8 KB apart
@@ -352,7 +354,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       for (int i = 0; i < nk && ok; ++i) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if (!mbar_wait_bounded(bar_full + 8 * x.s, x.ph, abort_flag)) {
+          if (!warp_wait_uniform(bar_full + 8 * x.s, x.ph, abort_flag)) {
             ok = false;
             break;
           }
@@ -362,7 +364,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
           for (int u = 0; u < SUB; ++u) {
             const bool first = BWD ? (h == 0 && i == 0) : (GU < 128 || h == 0);
             const bool last = BWD ? (h == 1 && i == nk - 1) : (GU < 128 || h == 1);
-            if (first && !mbar_wait_bounded(bar_tempty + 8 * t.s, t.ph ^ 1u, abort_flag)) {
+            if (first && !warp_wait_uniform(bar_tempty + 8 * t.s, t.ph ^ 1u, abort_flag)) {
               ok = false;
               break;
             }
@@ -371,11 +373,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
 #pragma unroll
             for (int k = 0; k < 4 / SUB; ++k) {
               const uint32_t kk = u * (4 / SUB) + k;
-              umma_f16(d, ad + kk * A_SLICE, bd + kk * B_SLICE, idesc, (first && k == 0) ? 0u : 1u);
+              if (issue) umma_f16(d, ad + kk * A_SLICE, bd + kk * B_SLICE, idesc, (first && k == 0) ? 0u : 1u);
             }
-            if (u == SUB - 1) umma_commit(bar_empty + 8 * x.s);
+            if (u == SUB - 1 && issue) umma_commit(bar_empty + 8 * x.s);
             if (last) {
-              umma_commit(bar_tfull + 8 * t.s);
+              if (issue) umma_commit(bar_tfull + 8 * t.s);
               t.next(2);
             }
           }
@@ -384,7 +386,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         }
       }
       if (!ok) {  // MMAs may still be running: wait for them before tensor memory is released
-        umma_commit(bar_drain);
+        if (issue) umma_commit(bar_drain);
         mbar_wait_drain(bar_drain, 0);
       }
     }
