@@ -55,13 +55,6 @@ struct PairArgs {
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
-// Waits of a whole warp on a barrier that the peer block arrives on too.
-__device__ __forceinline__ bool warp_wait_cl(uint32_t bar, uint32_t parity, volatile int* abort_flag, int lane) {
-  int ok = 1;
-  if (lane == 0) ok = mbar_wait_bounded_cl(bar, parity, abort_flag) ? 1 : 0;
-  __syncwarp();
-  return __shfl_sync(0xffffffffu, ok, 0) != 0;
-}
 // Position in a ring of N stages.
 template <int N>
 struct RingPos {
@@ -251,10 +244,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PR_THREADS, 1)
     const uint32_t lead_full = mapa_shared(bar_full, 0);
     const uint32_t dst0 = a_base + (BWD ? h * (PR_A_BYTES / 2) + (r & 63) * 128 : r * 128);
     constexpr int ZN = GU == 32 ? 2 : 1;  // groups of a half row
+    uint32_t w[2 * BITS];
     RingPos<SC> c;
+    auto take = [&]() {  // the next chunk's words
+      if (!warp_wait_uniform(bar_cfull + 8 * c.s, c.ph, abort_flag)) return false;
+      load_half_row<BITS>(smem + (c_base - sbase) + c.s * CODES, r, h, w);
+      return true;
+    };
     int as = grp;  // slot of this group's next step
     uint32_t aph = 0;
-    bool ok = true;
+    bool ok = cluster < ntiles && take();
     for (int tile = cluster; tile < ntiles && ok; tile += clusters) {
       const int mt = tile % p.tiles_m * 2 + static_cast<int>(rank);
       // row of W and its groups: forward row mt * 128 + r in chunk i; gradient row i * 128 + r in chunk mt
@@ -272,7 +271,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PR_THREADS, 1)
         }
       };
       load_sz(0);
-      for (int i = 0; i < p.steps; ++i) {
+      for (int i = 0; i < p.steps && ok; ++i) {
         float cs[ZN], cz[ZN];
 #pragma unroll
         for (int j = 0; j < ZN; ++j) {
@@ -280,13 +279,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PR_THREADS, 1)
           cs[j] = BWD ? ns[j] : 0.0f;
         }
         if (i + 1 < p.steps) load_sz((BWD && i + 1 >= p.chunks) ? i + 1 - p.chunks : i + 1);
-        if (!warp_wait(bar_cfull + 8 * c.s, c.ph, abort_flag, lane) ||
-            !warp_wait_cl(bar_empty + 8 * as, aph ^ 1u, abort_flag, lane)) {
+        if (!warp_wait_uniform_cl(bar_empty + 8 * as, aph ^ 1u, abort_flag)) {
           ok = false;
           break;
         }
-        uint32_t w[2 * BITS];
-        load_half_row<BITS>(smem + (c_base - sbase) + c.s * CODES, r, h, w);
         const uint32_t dst = dst0 + as * PR_A_BYTES;
 #pragma unroll
         for (int b = 0; b < 8; ++b) {
@@ -303,13 +299,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PR_THREADS, 1)
                          __byte_perm(q[0], q[1], 0x7632), __byte_perm(q[2], q[3], 0x7632));
           }
         }
+        // (the words were used above, so their stage can go back; the next chunk's are taken before this
+        // chunk's stores are fenced, which complete meanwhile)
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_cempty + 8 * c.s);
+        c.next();
+        if (i + 1 < p.steps || tile + clusters < ntiles) ok = take();
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bar_cempty + 8 * c.s);
-          mbar_arrive_remote(lead_full + 8 * as);
-        }
-        c.next();
+        if (lane == 0) mbar_arrive_remote(lead_full + 8 * as);
         as += 2;
         if (as >= NS) {
           as = grp;
@@ -373,7 +371,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PR_THREADS, 1)
         __syncwarp();
       };
       if (BWD) {
-        if (!warp_wait_cl(bar_tfull + 8 * t.s, t.ph, abort_flag, lane)) {
+        if (!warp_wait_uniform_cl(bar_tfull + 8 * t.s, t.ph, abort_flag)) {
           ok = false;
           break;
         }
@@ -407,7 +405,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PR_THREADS, 1)
         for (int uc = 0; uc < p.chunks * UNITS; ++uc) {
           const float sc = ns;
           if (uc + 1 < p.chunks * UNITS) ns = __ldg(srow + group_of<GU>(p.lin.gi, (uc + 1) / UNITS, (uc + 1) % UNITS));
-          if (!warp_wait_cl(bar_tfull + 8 * t.s, t.ph, abort_flag, lane)) {
+          if (!warp_wait_uniform_cl(bar_tfull + 8 * t.s, t.ph, abort_flag)) {
             ok = false;
             break;
           }

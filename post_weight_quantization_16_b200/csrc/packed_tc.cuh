@@ -415,8 +415,20 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     RingAt c;
     int as = grp;  // slot of this group's next step
     uint32_t aph = 0;
-    if (nk > 0) load_sz(0);
-    for (int i = 0; i < nk; ++i) {
+    // The words of the next chunk are taken before this chunk's stores are fenced, so that the stores
+    // complete meanwhile.
+    uint32_t w[2 * BITS];
+    auto take = [&]() {
+      if (!warp_wait_uniform(bar_cfull + 8 * c.s, c.ph, abort_flag)) return false;
+      load_half_row<BITS>(smem + (c_base - sbase) + c.s * CODES, r, h, w);
+      return true;
+    };
+    bool ok = nk > 0;
+    if (ok) {
+      load_sz(0);
+      ok = take();
+    }
+    for (int i = 0; i < nk && ok; ++i) {
       float cs_[ZN], cz[ZN];
 #pragma unroll
       for (int j = 0; j < ZN; ++j) {
@@ -424,11 +436,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         cs_[j] = BWD ? ns[j] : 0.0f;
       }
       if (i + 1 < nk) load_sz(i + 1);
-      if (!warp_wait(bar_cfull + 8 * c.s, c.ph, abort_flag, lane) ||
-          !warp_wait(bar_empty + 8 * as, aph ^ 1u, abort_flag, lane))
-        break;
-      uint32_t w[2 * BITS];
-      load_half_row<BITS>(smem + (c_base - sbase) + c.s * CODES, r, h, w);
+      if (!warp_wait_uniform(bar_empty + 8 * as, aph ^ 1u, abort_flag)) break;
       const uint32_t dst = dst0 + as * TC_STEP_A;
 #pragma unroll
       for (int b = 0; b < 8; ++b) {
@@ -445,13 +453,14 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                        __byte_perm(q[0], q[1], 0x7632), __byte_perm(q[2], q[3], 0x7632));
         }
       }
+      // (this chunk's words were used above, so its stage can go back)
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_cempty + 8 * c.s);
+      c.next(SC);
+      if (i + 1 < nk) ok = take();
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(bar_cempty + 8 * c.s);
-        mbar_arrive(bar_full + 8 * as);
-      }
-      c.next(SC);
+      if (lane == 0) mbar_arrive(bar_full + 8 * as);
       as += 2;
       if (as >= NS) {
         as = grp;
@@ -475,7 +484,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     for (int uc = 0; uc < units; ++uc) {
       const float sc = ns;
       if (!BWD && uc + 1 < units) ns = __ldg(srow + group_of<GU>(p.gi, ch0 + (uc + 1) / UNITS, (uc + 1) % UNITS));
-      if (!warp_wait(bar_tfull + 8 * t.s, t.ph, abort_flag, lane)) {
+      if (!warp_wait_uniform(bar_tfull + 8 * t.s, t.ph, abort_flag)) {
         ok = false;
         break;
       }
