@@ -65,6 +65,16 @@ cudaError_t by_bits(int bits, F&& f) {
   }
 }
 
+template <typename F>
+cudaError_t by_act(int act, F&& f) {
+  switch (act) {
+    case GPTQ_ACT_RELU: return f(std::integral_constant<int, ACT_RELU>());
+    case GPTQ_ACT_GELU: return f(std::integral_constant<int, ACT_GELU>());
+    case GPTQ_ACT_SILU: return f(std::integral_constant<int, ACT_SILU>());
+    default: return f(std::integral_constant<int, ACT_NONE>());
+  }
+}
+
 // Blocks of a cluster that split k: as many as two blocks per SM allow for `tiles` row tiles, each
 // with at least two chunks.
 int k_split(int64_t tiles, int chunks) {
@@ -78,11 +88,13 @@ constexpr int kDecodeTokens = 16;
 // Tokens up to which one block's 128-row tile runs; beyond, CTA pairs with 256-token tiles.
 constexpr int kSingleTokens = 128;
 
-// Tokens that the decode kernels lay out themselves, chunk range by chunk range, instead of a launch
-// of its own before them: every block of 128 rows repeats the layout, which is cheap for plain
-// 16-byte loads and for one or two gathered rows.
+// Whether the decode kernels lay out the tokens themselves, each block its chunk range, instead of a
+// launch before them: every block of 128 rows repeats the layout.  Measured with 4-bit layers: a
+// 4096 x 4096 one (4 chunks a block) takes 8.4 us with four tokens against 13.7 with the launch and
+// 9.1 / 13.6 with eight, an 11008 x 4096 one (11 chunks) 15.5 / 15.2 and 20.9 / 15.1; gathered through
+// an order, 10.5 / 13.9 and 16.1 / 13.9, and 17.2 / 15.2 already with two tokens.
 bool lay_out_locally(int64_t T, bool perm, int chunks_per_block) {
-  return T <= (perm ? 2 : 8) && T * chunks_per_block * 256 <= DEC_LOCAL_BYTES;
+  return T <= 8 && T * chunks_per_block <= (perm ? 16 : 44) && T * chunks_per_block * 256 <= DEC_LOCAL_BYTES;
 }
 
 size_t linear_workspace(int64_t T, int64_t n, int act_order) {
@@ -368,22 +380,29 @@ extern "C" gptq_status gptq_dequant_linear_backward(const gptq_linear_grad_args*
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   const uint16_t* dY = static_cast<const uint16_t*>(a.dY);
   const uint16_t* Z = a.act == GPTQ_ACT_NONE ? nullptr : static_cast<const uint16_t*>(a.preact);
-  const int vec4 = a.ld_dy % 4 == 0 && aligned_to(dY, 8) && (!Z || (m % 4 == 0 && aligned_to(Z, 8)));
-  if (a.dbias)
-    CK(launch_pdl(bf ? dbias_kernel<true> : dbias_kernel<false>, dim3((m + 127) / 128 * DBIAS_CLUSTER),
-                  dim3(DBIAS_WARPS * 32), 0, DBIAS_CLUSTER, st, dY, a.ld_dy, Z, T, m, a.act, vec4, a.dbias));
-  if (!a.dX) return GPTQ_OK;
+  const int vec = a.ld_dy % 8 == 0 && aligned16(dY) && (!Z || (m % 8 == 0 && aligned16(Z)));
   // dY is the operand itself when it is fp16, nothing is to be multiplied and TMA can read it
   const bool direct = aligned16(dY) && a.ld_dy % 8 == 0;
   grad_layout(a.T, m, n, a.W.perm ? 1 : 0, a.dtype, a.act, direct, &lay);
+  if (a.dbias)
+    CK(by_act(a.act, [&](auto k) {
+      constexpr int A = decltype(k)::value;
+      return launch_pdl(bf ? dbias_kernel<true, A> : dbias_kernel<false, A>,
+                        dim3((m + DBIAS_COLS - 1) / DBIAS_COLS * DBIAS_CLUSTER), dim3(DBIAS_WARPS * 32), 0, DBIAS_CLUSTER,
+                        st, dY, a.ld_dy, Z, T, m, vec, a.dbias);
+    }));
+  if (!a.dX) return GPTQ_OK;
   const uint16_t *hi = dY, *lo = dY;
   int64_t ldz = a.ld_dy;
   if (lay.parts >= 1) {
     uint16_t* h = reinterpret_cast<uint16_t*>(ws + lay.hi);
     uint16_t* o = lay.parts == 2 ? reinterpret_cast<uint16_t*>(ws + lay.lo) : nullptr;
     ldz = lay.ldz;
-    CK(launch_pdl(bf ? act_grad_kernel<true> : act_grad_kernel<false>, dim3(T), dim3(512), 0, 1, st, dY, a.ld_dy, Z, m,
-                  a.act, vec4, h, o, ldz, reinterpret_cast<float*>(ws + lay.scale)));
+    CK(by_act(a.act, [&](auto k) {
+      constexpr int A = decltype(k)::value;
+      return launch_pdl(bf ? act_grad_kernel<true, A> : act_grad_kernel<false, A>, dim3(T), dim3(512), 0, 1, st, dY,
+                        a.ld_dy, Z, m, vec, h, o, ldz, reinterpret_cast<float*>(ws + lay.scale));
+    }));
     hi = h;
     lo = o ? o : h;
   }
