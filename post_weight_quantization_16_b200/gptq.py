@@ -543,6 +543,30 @@ def dequant_moe(X: torch.Tensor, router: torch.Tensor, gate_up: tuple, down: tup
     return out, ids, weights
 
 
+def stack_experts(gates: list, ups: list, downs: list) -> tuple:
+    """(gate_up, down, perm) for dequant_moe from the experts' quantized projections: lists, one entry
+    per expert, of dicts with codes, scales, zeros and perm (or no perm) as quantize_layer,
+    rtn_quantize and awq_quantize return them.  An expert's gate and up share their input, so with
+    act-order they must share their perm too (it depends on the input alone).  The act-order of a down
+    projection is folded into the rows of its gate and up: h then comes out in down's sweep order.
+    A one-time layout: call it once per layer and keep the result."""
+    if not gates or len(gates) != len(ups) or len(gates) != len(downs):
+        raise ValueError("gates, ups and downs need one entry per expert each")
+    gate_up, down, perms = [], [], []
+    for e, (g, u, d) in enumerate(zip(gates, ups, downs)):
+        pg, pu, pd = g.get("perm"), u.get("perm"), d.get("perm")
+        if (pg is None) != (pu is None) or (pg is not None and not torch.equal(pg, pu)):
+            raise ValueError(f"expert {e}: gate and up have different input orders")
+        rows = (lambda t: t) if pd is None else (lambda t, i=pd.long(): t.index_select(0, i))
+        gate_up.append([torch.cat([rows(g[k]), rows(u[k])]) for k in ("codes", "scales", "zeros")])
+        down.append([d[k] for k in ("codes", "scales", "zeros")])
+        perms.append(pg)
+    if any((p is None) != (perms[0] is None) for p in perms):
+        raise ValueError("either every expert has an input order or none has")
+    return (tuple(torch.stack(t) for t in zip(*gate_up)), tuple(torch.stack(t) for t in zip(*down)),
+            None if perms[0] is None else torch.stack(perms))
+
+
 def _jobs(layers: list, dev: torch.device):
     jobs = (LayerJob * len(layers))()
     outs = []
