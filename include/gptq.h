@@ -351,18 +351,20 @@ enum { GPTQ_ACT_NONE = 0, GPTQ_ACT_RELU = 1, GPTQ_ACT_GELU = 2, GPTQ_ACT_SILU = 
 
 /* The linear layer:
  *   Z = X[:, perm] W^T + bias,   Y = act(Z) + residual
- * in fp32, each output rounded once.
+ * in fp32, each output rounded once.  (A group's sum of (code - zero) x comes before its scale, so
+ * it too must fit fp32: |x| up to about 1e34.)
  *   X        : device, dtype, [T x n] in original column order, row stride ld_x elements
  *              (ld_x >= n, ld_x % 8 == 0, 16-byte aligned base); 0 <= T <= 2^22 (0 is a no-op)
  *   bias     : device, dtype, [m], or NULL
  *   residual : device, dtype, [T x m] with row stride ld_res >= m, or NULL; may be Y itself when
  *              the strides and types agree
- *   Y        : device [T x m] with row stride ld_y >= m, dtype, or fp32 when y_fp32 is 1; must not
- *              overlap X
+ *   Y        : device [T x m] with row stride ld_y >= m, dtype, or fp32 when y_fp32 is 1
+ * Y and preact overlap neither X nor each other, nor the residual but for Y in its place
+ * (GPTQ_ERR_ARG; column slices of one buffer are fine).
  *   preact   : device, dtype, [T x m] contiguous, receives Z (the backward pass's input), or NULL
  *   workspace: device, 256-byte aligned, at least gptq_dequant_linear_workspace_bytes (a status
- *              word for gptq_dequant_matmul_check and, with a perm, X in sweep order); owned by the
- *              caller, may be reused by later calls on the same stream; calls that can run at the
+ *              word for gptq_dequant_matmul_check, which each call with T > 0 sets, and, with a perm
+ *              or at most 16 tokens, X in the kernels' order); owned by the caller, may be reused by later calls on the same stream; calls that can run at the
  *              same time need one each
  * Asynchronous on cuda_stream; no allocation and no synchronization, so a call can be captured
  * into a graph; arguments are checked before any launch; the result is deterministic. */
@@ -395,7 +397,8 @@ gptq_status gptq_dequant_linear(const gptq_linear_args* args, int device, void* 
  *   dY       : device, dtype, [T x m], row stride ld_dy >= m; 0 <= T <= 2^22
  *   preact   : device, dtype, [T x m] contiguous: Z as gptq_dequant_linear gave it; not read when
  *              act is none
- *   dX       : device, dtype, [T x n], original column order, row stride ld_dx >= n; or NULL
+ *   dX       : device, dtype, [T x n], original column order, row stride ld_dx >= n, overlapping
+ *              neither dY nor preact; or NULL
  *   dbias    : device fp32 [m], or NULL (zeros when T is 0)
  *   workspace: as above, gptq_dequant_linear_backward_workspace_bytes
  * At least one output.  Asynchronous on cuda_stream, capturable, deterministic. */
@@ -429,7 +432,8 @@ gptq_status gptq_dequant_linear_backward(const gptq_linear_grad_args* args, int 
  *               [E x 2I x H/g], perm [E x H] (both halves share their input's order) or NULL
  *   down      : m = H rows of n = I inputs per expert; perm must be NULL: the order of an act-order
  *               down projection is folded into the rows of gate and up (gptq.stack_experts)
- *   residual  : as in gptq_dequant_linear; Y: [T x H], dtype, row stride ld_y
+ *   residual  : as in gptq_dequant_linear; Y: [T x H], dtype, row stride ld_y, may be X or the
+ *               residual
  *   ids_out   : device int32 [T x top_k], or NULL;  weights_out: device fp32 [T x top_k], or NULL
  *   workspace : device, 256-byte aligned, gptq_dequant_moe_workspace_bytes, as above
  * H and I are multiples of 128, at most 65536; gate_up and down may differ in qp.group_size but not

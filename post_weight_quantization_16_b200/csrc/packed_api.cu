@@ -33,6 +33,22 @@ bool valid_packed(const gptq_packed& w) {
          (!w.perm || aligned16(w.perm));
 }
 
+// Whether `rows` rows of wa and wb bytes at strides lda and ldb share memory.  Column slices of one
+// buffer (equal strides) may lie between each other.
+bool overlap(const void* a, int64_t lda, int64_t wa, const void* b, int64_t ldb, int64_t wb, int64_t rows) {
+  if (!a || !b) return false;
+  uint64_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
+  if (pa > pb) {
+    std::swap(pa, pb);
+    std::swap(lda, ldb);
+    std::swap(wa, wb);
+  }
+  if (pa + static_cast<uint64_t>((rows - 1) * lda + wa) <= pb) return false;
+  if (rows == 1 || lda != ldb) return true;
+  const int64_t off = static_cast<int64_t>((pb - pa) % static_cast<uint64_t>(lda));
+  return off < wa || off + wb > lda;
+}
+
 int group_width(const gptq_packed& w) { return w.qp.group_size == -1 ? static_cast<int>(w.n) : w.qp.group_size; }
 
 GroupIndex group_index(int g) {
@@ -281,6 +297,17 @@ extern "C" gptq_status gptq_dequant_linear(const gptq_linear_args* args, int dev
     return GPTQ_ERR_ARG;
   if (a.residual && (a.ld_res < a.W.m || !aligned_to(a.residual, 2))) return GPTQ_ERR_ARG;
   if (a.workspace_bytes < linear_workspace(a.T, a.W.n, a.W.perm ? 1 : 0)) return GPTQ_ERR_ARG;
+  {
+    // outputs against inputs and each other; Y may take the residual's place
+    const int64_t ys = a.y_fp32 ? 4 : 2, yw = a.W.m * ys, w = a.W.m * 2;
+    const bool in_place = a.residual == a.Y && !a.y_fp32 && (a.ld_res == a.ld_y || a.T == 1);
+    if (overlap(a.X, a.ld_x * 2, a.W.n * 2, a.Y, a.ld_y * ys, yw, a.T) ||
+        overlap(a.X, a.ld_x * 2, a.W.n * 2, a.preact, w, w, a.T) ||
+        overlap(a.preact, w, w, a.Y, a.ld_y * ys, yw, a.T) ||
+        overlap(a.preact, w, w, a.residual, a.ld_res * 2, w, a.T) ||
+        (!in_place && overlap(a.residual, a.ld_res * 2, w, a.Y, a.ld_y * ys, yw, a.T)))
+      return GPTQ_ERR_ARG;
+  }
   const gptq_status ds = check_device(device);
   if (ds != GPTQ_OK) return ds;
   DeviceGuard dg(device);
@@ -326,7 +353,7 @@ extern "C" gptq_status gptq_dequant_linear(const gptq_linear_args* args, int dev
   DecodeLaunch l;
   l.bf16 = a.dtype == GPTQ_BF16;
   l.unit = std::min(g, 128);
-  l.nt = d.tiles <= 2 ? d.tiles : 4;
+  l.nt = d.tiles;
   l.cluster = k_split((m + DEC_ROWS - 1) / DEC_ROWS, d.chunks);
   l.device = device;
   l.stream = st;
@@ -366,6 +393,10 @@ extern "C" gptq_status gptq_dequant_linear_backward(const gptq_linear_grad_args*
                   a.workspace_bytes < need.total))
     return GPTQ_ERR_ARG;
   if (a.T > 0 && a.act != GPTQ_ACT_NONE && (!a.preact || !aligned_to(a.preact, 2))) return GPTQ_ERR_ARG;
+  if (a.T > 0 && (overlap(a.dY, a.ld_dy * 2, a.W.m * 2, a.dX, a.ld_dx * 2, a.W.n * 2, a.T) ||
+                  (a.act != GPTQ_ACT_NONE &&
+                   overlap(a.preact, a.W.m * 2, a.W.m * 2, a.dX, a.ld_dx * 2, a.W.n * 2, a.T))))
+    return GPTQ_ERR_ARG;
   if (a.T == 0 && !a.dbias) return GPTQ_OK;
   const gptq_status ds = check_device(device);
   if (ds != GPTQ_OK) return ds;
@@ -389,7 +420,8 @@ extern "C" gptq_status gptq_dequant_linear_backward(const gptq_linear_grad_args*
       constexpr int A = decltype(k)::value;
       return launch_pdl(bf ? dbias_kernel<true, A> : dbias_kernel<false, A>,
                         dim3((m + DBIAS_COLS - 1) / DBIAS_COLS * DBIAS_CLUSTER), dim3(DBIAS_WARPS * 32), 0, DBIAS_CLUSTER,
-                        st, dY, a.ld_dy, Z, T, m, vec, a.dbias);
+                        st, dY, a.ld_dy, Z, T, m, vec, a.dbias,
+                        reinterpret_cast<int*>(ws));
     }));
   if (!a.dX) return GPTQ_OK;
   const uint16_t *hi = dY, *lo = dY;
@@ -484,6 +516,10 @@ extern "C" gptq_status gptq_dequant_moe(const gptq_moe_args* args, int device, v
       !aligned_to(a.ids_out, 4) || !aligned_to(a.weights_out, 4))
     return GPTQ_ERR_ARG;
   if (a.workspace_bytes < lay.total) return GPTQ_ERR_ARG;
+  // (X is read before the last launch writes Y; the residual beside it)
+  if (!(a.residual == a.Y && (a.ld_res == a.ld_y || a.T == 1)) &&
+      overlap(a.residual, a.ld_res * 2, H * 2, a.Y, a.ld_y * 2, H * 2, a.T))
+    return GPTQ_ERR_ARG;
   const gptq_status ds = check_device(device);
   if (ds != GPTQ_OK) return ds;
   DeviceGuard dg(device);

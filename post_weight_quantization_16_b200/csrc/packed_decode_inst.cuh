@@ -39,38 +39,39 @@ struct Of {
   }
 };
 
-template <bool BF, int GU, typename F>
+template <bool MOE, bool BF, int GU, typename F>
 cudaError_t by_tiles(const DecodeLaunch& l, F&& f) {
   if (l.local) return f(Of<BF, GU, 1, true>());
   if (l.nt == 1) return f(Of<BF, GU, 1, false>());
-  if (l.nt == 2) return f(Of<BF, GU, 2, false>());
-  return f(Of<BF, GU, 4, false>());
+  if constexpr (MOE)  // (a segment of an expert has up to 32 tokens, the linear decode kernel 16)
+    if (l.nt == 4) return f(Of<BF, GU, 4, false>());
+  return f(Of<BF, GU, 2, false>());
 }
-template <bool BF, typename F>
+template <bool MOE, bool BF, typename F>
 cudaError_t by_unit(const DecodeLaunch& l, F&& f) {
-  if (l.unit == 32) return by_tiles<BF, 32>(l, f);
-  if (l.unit == 64) return by_tiles<BF, 64>(l, f);
-  return by_tiles<BF, 128>(l, f);
+  if (l.unit == 32) return by_tiles<MOE, BF, 32>(l, f);
+  if (l.unit == 64) return by_tiles<MOE, BF, 64>(l, f);
+  return by_tiles<MOE, BF, 128>(l, f);
 }
-template <typename F>
+template <bool MOE, typename F>
 cudaError_t by_type(const DecodeLaunch& l, F&& f) {
-  return l.bf16 ? by_unit<true>(l, f) : by_unit<false>(l, f);
+  return l.bf16 ? by_unit<MOE, true>(l, f) : by_unit<MOE, false>(l, f);
 }
 }  // namespace
 
 template <>
 cudaError_t launch_linear_decode<PACKED_BITS>(const DecodeLaunch& l, const CUtensorMap& codes,
                                               const LinearDecodeArgs& a) {
-  return by_type(l, [&](auto of) { return decltype(of)::linear(l, codes, a); });
+  return by_type<false>(l, [&](auto of) { return decltype(of)::linear(l, codes, a); });
 }
 template <>
 cudaError_t launch_moe_gate_up<PACKED_BITS>(const DecodeLaunch& l, const CUtensorMap& codes, const MoeArgs& a,
                                             int segments) {
-  return by_type(l, [&](auto of) { return decltype(of)::gate_up(l, codes, a, segments); });
+  return by_type<true>(l, [&](auto of) { return decltype(of)::gate_up(l, codes, a, segments); });
 }
 template <>
 cudaError_t launch_moe_down<PACKED_BITS>(const DecodeLaunch& l, const CUtensorMap& codes, const MoeArgs& a) {
-  return by_type(l, [&](auto of) { return decltype(of)::down(l, codes, a); });
+  return by_type<true>(l, [&](auto of) { return decltype(of)::down(l, codes, a); });
 }
 
 }  // namespace gptq

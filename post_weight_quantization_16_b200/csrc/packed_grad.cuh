@@ -35,7 +35,8 @@ __device__ __forceinline__ float at8(const uint4& v, int j) {
 }
 
 // One block per token.  scale_t = 2^e with the largest |dY| of the token in [2^(e+13), 2^(e+14))
-// (e clamped to [-100, 100]; 1 for a token without a finite, nonzero value), then hi + lo = dz /
+// (e clamped to [-126, 126], where both
+// scale_t and its inverse are normal; 1 for a token without a finite, nonzero value), then hi + lo = dz /
 // scale_t in fp16 (lo null: hi alone).  Rows of ldz (a multiple of 8) elements; the second pass finds
 // dY in the caches.  vec: rows of dY and Z allow 16-byte accesses.
 template <bool BF, int ACT>
@@ -63,7 +64,7 @@ __global__ void __launch_bounds__(512) act_grad_kernel(const uint16_t* __restric
 #pragma unroll
   for (int w = 0; w < 16; ++w) mx = fmaxf(mx, wmax[w]);
   int e = 0;
-  if (mx > 0.0f && mx < INFINITY) e = min(100, max(-100, ilogbf(mx) - 13));
+  if (mx > 0.0f && mx < INFINITY) e = min(126, max(-126, ilogbf(mx) - 13));
   const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
   if (threadIdx.x == 0) token_scale[t] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
 #pragma unroll 3
@@ -96,10 +97,12 @@ constexpr int DBIAS_CLUSTER = 8, DBIAS_WARPS = 8, DBIAS_COLS = 256;
 template <bool BF, int ACT>
 __global__ void __launch_bounds__(DBIAS_WARPS * 32) dbias_kernel(const uint16_t* __restrict__ dY, int64_t ld_dy,
                                                                  const uint16_t* __restrict__ Z, int T, int m, int vec,
-                                                                 float* __restrict__ dbias) {
+                                                                 float* __restrict__ dbias,
+                                                                 int* __restrict__ status) {
   __shared__ float part[DBIAS_WARPS][DBIAS_COLS];
   griddep_wait();
   griddep_launch_dependents();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *status = 0;  // (the only launch when dX is not asked for)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank());
   const int c0 = static_cast<int>(blockIdx.x) / DBIAS_CLUSTER * DBIAS_COLS, c = c0 + lane * 8, left = m - c;

@@ -381,6 +381,15 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+def _elsewhere(stream, like: torch.Tensor) -> bool:
+    """Whether `stream` is given and not the current one of the tensor's device."""
+    if stream is None:
+        return False
+    if stream.device_index != like.get_device():
+        raise ValueError(f"stream belongs to cuda:{stream.device_index}, the tensors to {like.device}")
+    return stream.cuda_stream != _raw_stream(stream.device_index)
+
+
 class _On:
     """Allocations and launches of a call on a stream that is not the current one."""
 
@@ -418,10 +427,11 @@ def dequant_linear(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, z
     zeros, perm as quantize_layer (or rtn_quantize, awq_quantize: perm None) wrote them; bias [m] and
     residual [T, m] in X's type; act one of ACT_NONE, ACT_RELU, ACT_GELU, ACT_SILU.  Returns Y [T, m]
     in X's type (or fp32 with out_dtype=torch.float32), and with want_preact also Z, the value the
-    activation was applied to, which dequant_linear_backward takes.  `out` may be `residual`.
+    activation was applied to, which dequant_linear_backward takes.  `out` may be `residual`,
+    but not share memory with X.
     Asynchronous on `stream` (default: the device's current one; another stream's allocations are made
     on it); can be captured into a graph."""
-    if stream is not None and stream.cuda_stream != _raw_stream(X.get_device()):
+    if _elsewhere(stream, X):
         with _On(stream):
             return dequant_linear(X, codes, scales, zeros, perm, bits, group_size, bias, act, residual, out_dtype,
                                   want_preact, out, workspace)
@@ -467,7 +477,7 @@ def dequant_linear_backward(dY: torch.Tensor, codes: torch.Tensor, scales: torch
     [T, m]; preact: the Z that dequant_linear(want_preact=True) gave (needed unless act is ACT_NONE).
     Returns dX [T, n] in dY's type, or (dX, dbias) with want_dbias (dbias fp32 [m]; dX is None with
     want_dx=False).  The residual's gradient is dY itself.  Asynchronous on `stream`."""
-    if stream is not None and stream.cuda_stream != _raw_stream(dY.get_device()):
+    if _elsewhere(stream, dY):
         with _On(stream):
             return dequant_linear_backward(dY, codes, scales, zeros, perm, bits, group_size, act, preact, want_dx,
                                            want_dbias, out, workspace)
@@ -510,8 +520,8 @@ def dequant_moe(X: torch.Tensor, router: torch.Tensor, gate_up: tuple, down: tup
     with the gate rows first; down = (codes [E, H, words], scales, zeros); perm: int32 [E, H], the
     act-order of each expert's gate and up, or None (stack_experts builds these from quantized
     layers).  Returns Y [T, H], the chosen experts [T, top_k] (int32, by descending probability) and
-    their weights [T, top_k] (fp32).  Asynchronous on `stream`."""
-    if stream is not None and stream.cuda_stream != _raw_stream(X.get_device()):
+    their weights [T, top_k] (fp32).  `out` may be X or `residual`.  Asynchronous on `stream`."""
+    if _elsewhere(stream, X):
         with _On(stream):
             return dequant_moe(X, router, gate_up, down, perm, bits, group_size, top_k, renormalize, act, residual,
                                down_group_size, out, workspace)
@@ -531,10 +541,10 @@ def dequant_moe(X: torch.Tensor, router: torch.Tensor, gate_up: tuple, down: tup
     if out is None:
         out = X.new_empty((T, H))
     y_ptr, ldy = _rows("out", out, T, H, X.dtype, index)
-    ids = X.new_empty((T, top_k), dtype=torch.int32)
-    weights = X.new_empty((T, top_k), dtype=torch.float32)
     L = lib()
     ws = _workspace(L.gptq_dequant_moe_workspace_bytes(T, E, top_k, H, I), workspace, X)
+    ids = X.new_empty((T, top_k), dtype=torch.int32)
+    weights = X.new_empty((T, top_k), dtype=torch.float32)
     a = _MOE_ARGS.pack(x_ptr, T, ldx, dt, router.data_ptr(), E, top_k, renormalize, act, *gu, *dn, r_ptr, ldr, y_ptr, ldy,
                        ids.data_ptr(), weights.data_ptr(), ws.data_ptr(), ws.numel())
     st = L.gptq_dequant_moe(a, index, _raw_stream(index))

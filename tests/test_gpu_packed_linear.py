@@ -302,6 +302,64 @@ def test_callers_workspace_and_refusals_on_the_device():
         G.dequant_linear_backward(torch.zeros(12, 64, device=DEV).half(), *c.layer, want_dx=False)
 
 
+def test_tiny_and_huge_gradients():
+    """Tokens of a bf16 dY scaled by powers of two give the same dX, scaled: dz is scaled per token."""
+    for T, m in ((20, 200), (300, 200)):
+        c = Case(T, m, 9472, 4, 128, "bf16", "none", True)
+        dY = torch.randn(T, m, device=DEV).to(c.dt)
+        e = torch.from_numpy(c.rng.integers(-110, 118, T)).to(DEV)
+        e[0], e[1] = -110, 117
+        base = G.dequant_linear_backward(dY, *c.layer).double()
+        got = G.dequant_linear_backward(torch.ldexp(dY.double(), e[:, None]).to(c.dt), *c.layer).double()
+        want = torch.ldexp(base, e[:, None])
+        normal = (want.abs() >= 2.0 ** -120) | (want == 0)      # below, fewer bits are left
+        assert torch.equal(got[normal], want[normal]) and normal.float().mean() > 0.9
+
+
+def test_offsets_past_32_bits():
+    """Strides and row counts whose element offsets exceed 2^31: the last rows are checked."""
+    big = torch.empty((5 << 30) // 2, dtype=torch.float16, device=DEV)
+    for T in (8, 9, 300):
+        c = Case(T, 2304, 256, 4, 128, "fp16", "none", True)
+        ld = (big.numel() // T - 4096) // 8 * 8
+        assert (T - 1) * ld > 1 << 31
+        view = lambda at, cols: torch.as_strided(big, (T, cols), (ld, 1), at)  # noqa: E731
+        x, res, out, dx = view(0, 256), view(256, 2304), view(256, 2304), view(2816, 256)
+        x.copy_(c.X)
+        r = torch.randn(T, 2304, device=DEV).half()
+        res.copy_(r)
+        G.dequant_linear(x, *c.layer, residual=res, out=out)
+        assert torch.equal(out, G.dequant_linear(c.X, *c.layer, residual=r))
+        G.dequant_linear_backward(out, *c.layer, out=dx)
+        assert torch.equal(dx, G.dequant_linear_backward(out.contiguous(), *c.layer))
+    del big, x, res, out, dx
+    T, m = 33000, 65600
+    c = Case(64, m, 128, 4, 128, "fp16", "silu", True, outliers=False)
+    X = torch.zeros(T, 128, dtype=c.dt, device=DEV)
+    X[-64:] = c.X
+    y, z = G.dequant_linear(X, *c.layer, act=G.ACT_SILU, want_preact=True)
+    want, tol, wz, tz = c.forward64()
+    close(y[-64:], want, tol, c.dt)
+    close(z[-64:], wz, tz, c.dt)
+    dX = G.dequant_linear_backward(y, *c.layer, act=G.ACT_SILU, preact=z)
+    g, tol, _ = grad64(c, y[-64:], z[-64:])
+    close(dX[-64:], g, tol, c.dt)
+    assert (dX[:-64] == 0).all()
+
+
+def test_status_words():
+    for T in (1, 16, 40, 600):
+        c = Case(T, 2304, 256, 4, 128, "bf16", "none", True)
+        ws = torch.full((1 << 26,), 255, dtype=torch.uint8, device=DEV)
+        check = lambda: G.lib().gptq_dequant_matmul_check(ws.data_ptr(), 0, None)  # noqa: E731
+        y = G.dequant_linear(c.X, *c.layer, workspace=ws)
+        assert check() == G.OK
+        for kw in (dict(want_dbias=True), dict(want_dx=False, want_dbias=True), {}):
+            ws.fill_(255)
+            G.dequant_linear_backward(y, *c.layer, workspace=ws, **kw)
+            assert check() == G.OK
+
+
 def test_after_quantizing_a_layer():
     """The path's own result in use: quantize a layer with act-order, apply it with bias and SiLU, and
     take the gradient."""

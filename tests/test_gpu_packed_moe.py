@@ -158,6 +158,11 @@ def test_strides_no_tokens_and_residual_in_place():
     buf = res.contiguous()
     y2, *_ = c.run(residual=buf, out=buf)
     assert y2 is buf and torch.equal(y2, y)
+    x = c.X.clone()
+    y3, *_ = c.run(X=x, residual=x, out=x)                       # a block's input, residual and output in one
+    assert y3 is x and torch.equal(x, c.run(residual=c.X)[0])
+    x = c.X[:5].clone()                                         # (the kernels that lay out X themselves)
+    assert torch.equal(c.run(X=x, residual=x, out=x)[0], c.run(X=c.X[:5], residual=c.X[:5])[0])
     y, ids, w = c.run(X=c.X[:0])
     assert y.shape == (0, 384) and ids.shape == w.shape == (0, 2)
 

@@ -13,6 +13,8 @@ from post_weight_quantization_16_b200 import build as B
 from post_weight_quantization_16_b200 import gptq as G
 
 P = 1 << 20  # an aligned address that no check dereferences
+Q = 1 << 40  # another, for outputs
+NO_DEVICE = -1  # what passes the checks of arguments ends here, with GPTQ_ERR_CUDA
 
 
 @pytest.fixture(scope="module")
@@ -25,23 +27,23 @@ def packed(m=64, n=512, bits=4, g=128, perm=0, codes=P, scales=P, zeros=P):
     return (codes, scales, zeros, perm, m, n, bits, g, 0)
 
 
-def linear(L, W=None, X=P, T=4, ldx=512, dtype=0, bias=0, res=0, ldr=0, act=0, Y=P, ldy=64, f32=0, preact=0, ws=P,
+def linear(L, W=None, X=P, T=4, ldx=512, dtype=0, bias=0, res=0, ldr=0, act=0, Y=Q, ldy=64, f32=0, preact=0, ws=P,
            wsb=1 << 20):
     a = G._LINEAR_ARGS.pack(X, T, ldx, dtype, *(W or packed()), bias, res, ldr, act, Y, ldy, f32, preact, ws, wsb)
-    return L.gptq_dequant_linear(a, 0, None)
+    return L.gptq_dequant_linear(a, NO_DEVICE, None)
 
 
-def backward(L, W=None, dY=P, T=4, ld=64, dtype=0, act=0, Z=0, dX=P, ldx=512, db=0, ws=P, wsb=1 << 20):
+def backward(L, W=None, dY=P, T=4, ld=64, dtype=0, act=0, Z=0, dX=Q, ldx=512, db=0, ws=P, wsb=1 << 20):
     a = G._LINEAR_GRAD_ARGS.pack(dY, T, ld, dtype, *(W or packed()), act, Z, dX, ldx, db, ws, wsb)
-    return L.gptq_dequant_linear_backward(a, 0, None)
+    return L.gptq_dequant_linear_backward(a, NO_DEVICE, None)
 
 
-def moe(L, T=4, E=8, k=2, gu=None, dn=None, X=P, ldx=512, R=P, renorm=1, act=3, dtype=0, res=0, ldr=0, Y=P, ldy=512, ws=P,
+def moe(L, T=4, E=8, k=2, gu=None, dn=None, X=P, ldx=512, R=P, renorm=1, act=3, dtype=0, res=0, ldr=0, Y=Q, ldy=512, ws=P,
         wsb=1 << 30):
     gu = gu or packed(m=512, n=512)
     dn = dn or packed(m=512, n=256)
     a = G._MOE_ARGS.pack(X, T, ldx, dtype, R, E, k, renorm, act, *gu, *dn, res, ldr, Y, ldy, 0, 0, ws, wsb)
-    return L.gptq_dequant_moe(a, 0, None)
+    return L.gptq_dequant_moe(a, NO_DEVICE, None)
 
 
 def test_argument_blocks_have_the_header_s_layout():
@@ -98,20 +100,22 @@ def test_linear_refusals(L):
               packed(g=384)):
         assert linear(L, W, ldx=max(512, W[5])) == E, W
     for kw in (dict(X=0), dict(X=P + 8), dict(ldx=504), dict(ldx=516), dict(T=-1), dict(T=(1 << 22) + 1), dict(dtype=2),
-               dict(act=4), dict(act=-1), dict(Y=0), dict(Y=P + 1), dict(ldy=63), dict(f32=2), dict(f32=1, Y=P + 2),
+               dict(act=4), dict(act=-1), dict(Y=0), dict(Y=Q + 1), dict(ldy=63), dict(f32=2), dict(f32=1, Y=Q + 2),
                dict(bias=P + 1), dict(res=P, ldr=63), dict(res=P + 1, ldr=64), dict(preact=P + 1), dict(ws=0), dict(ws=P + 128),
                dict(wsb=255)):
         assert linear(L, **kw) == E, kw
+    assert linear(L) == linear(L, act=3, res=P, ldr=64, bias=P) == G.ERR_CUDA   # the defaults are fine
     assert linear(L, T=0, X=0, Y=0, ws=0) == G.OK                              # nothing to do
 
 
 def test_backward_refusals(L):
     E = G.ERR_ARG
     assert L.gptq_dequant_linear_backward(None, 0, None) == E
-    for kw in (dict(W=packed(bits=7)), dict(dY=0), dict(dY=P + 1), dict(ld=63), dict(ldx=511), dict(dX=P + 1), dict(dtype=3),
+    for kw in (dict(W=packed(bits=7)), dict(dY=0), dict(dY=P + 1), dict(ld=63), dict(ldx=511), dict(dX=Q + 1), dict(dtype=3),
                dict(act=9), dict(act=3, Z=0), dict(act=3, Z=P + 1), dict(dX=0), dict(db=P + 2), dict(ws=0), dict(ws=P + 8),
                dict(dtype=1, wsb=256), dict(T=-1)):
         assert backward(L, **kw) == E, kw
+    assert backward(L) == backward(L, act=3, Z=P, db=P) == G.ERR_CUDA
     assert backward(L, T=0, dY=0, ws=0) == G.OK
 
 
@@ -124,7 +128,41 @@ def test_moe_refusals(L):
                dict(gu=packed(m=512, n=384)), dict(dn=packed(m=384, n=256)), dict(dn=packed(m=512, n=256, perm=P)),
                dict(dn=packed(m=512, n=256, bits=8)), dict(gu=packed(m=512, n=512, perm=P + 4))):
         assert moe(L, **kw) == E, kw
+    assert moe(L) == moe(L, res=P, ldr=512) == G.ERR_CUDA
     assert moe(L, T=0, X=0, Y=0, R=0, ws=0) == G.OK
+
+
+def test_outputs_that_overlap(L):
+    """X [4 x 512], Y and residual [4 x 64], 16-bit: refused where rows share memory, not where column
+    slices of one buffer lie side by side."""
+    E, ok = G.ERR_ARG, G.ERR_CUDA
+    for Y, ldy, want in ((P, 64, E), (P + 3 * 1024 + 1022, 64, E), (P + 4 * 1024, 64, ok), (P - 512, 64, ok), (P - 510, 64, E)):
+        assert linear(L, Y=Y, ldy=ldy) == want, (Y - P, ldy)
+    for at, want in ((1024, ok), (1022, E), (1152 - 128, ok), (1152 - 126, E), (0, E)):     # rows of 576 values
+        assert linear(L, ldx=576, Y=P + at, ldy=576) == want, at
+    assert linear(L, ldx=576, Y=P + 1024, ldy=576, f32=1) == E                 # fp32 rows: other strides
+    assert linear(L, T=1, ldx=576, Y=P + 1024, ldy=64) == ok
+    assert linear(L, res=Q, ldr=64) == ok                                      # in place
+    assert linear(L, res=Q, ldr=72) == linear(L, res=Q + 2, ldr=64) == linear(L, res=Q, ldr=64, f32=1) == E
+    assert linear(L, T=1, res=Q, ldr=72) == ok
+    assert linear(L, preact=Q) == linear(L, preact=P) == linear(L, preact=2 * Q, res=2 * Q, ldr=64) == E
+    assert linear(L, preact=2 * Q) == ok
+    assert backward(L, dY=Q) == backward(L, dY=Q + 4094) == backward(L, act=3, Z=Q) == E
+    assert backward(L, dY=Q + 4096) == backward(L, Z=Q) == ok                  # (Z is not read without an activation)
+    assert moe(L, res=Q, ldr=512) == moe(L, Y=P) == ok
+    assert moe(L, res=Q + 2, ldr=512) == moe(L, res=Q, ldr=520) == E
+
+
+def test_a_stream_of_another_device_is_refused():
+    class Stream:
+        device_index, cuda_stream = 1, 0
+
+    x, c, s = torch.zeros(2, 512, dtype=torch.float16), torch.zeros(4, 64, dtype=torch.int32), torch.zeros(4, 4)
+    for call in (lambda: G.dequant_linear(x, c, s, s, None, 4, 128, stream=Stream()),
+                 lambda: G.dequant_linear_backward(x, c, s, s, None, 4, 128, stream=Stream()),
+                 lambda: G.dequant_moe(x, x, (c, s, s), (c, s, s), None, 4, 128, 1, stream=Stream())):
+        with pytest.raises(ValueError, match="stream belongs"):
+            call()
 
 
 def test_binding_refuses_what_is_not_on_a_device():
