@@ -51,6 +51,13 @@ bool overlap(const void* a, int64_t lda, int64_t wa, const void* b, int64_t ldb,
 
 int group_width(const gptq_packed& w) { return w.qp.group_size == -1 ? static_cast<int>(w.n) : w.qp.group_size; }
 
+// Values of a scale or zero-point row that one aligned load takes.
+int param_vec(const gptq_packed& w) {
+  const int64_t G = w.n / group_width(w);
+  if (G % 4 == 0 && aligned16(w.scales) && aligned16(w.zeros)) return 4;
+  return G % 2 == 0 && aligned_to(w.scales, 8) && aligned_to(w.zeros, 8) ? 2 : 1;
+}
+
 GroupIndex group_index(int g) {
   GroupIndex gi;
   gi.div = g >= 128 ? g / 128 : 1;
@@ -238,12 +245,31 @@ bool grad_layout(int64_t T, int64_t m, int64_t n, int act_order, int dtype, int 
   return true;
 }
 
-// Tiles of a segment for T tokens: an expert gets a token at most once.
-int moe_nt(int64_t T) { return T <= 8 ? 1 : T <= 16 ? 2 : 4; }
+// Tiles of eight tokens in a segment; an expert with more tokens takes a second segment, which reads and
+// unpacks its weights again.  (An expert gets a token at most once.)  Measured, 2 tiles against 4: 24
+// tokens an expert 98 / 123 us (16 experts of 2048 x 1408), 12 tokens 259 / 306 (8 of 4096 x 11008), 32
+// tokens 723 / 586 there; fewer registers and smaller stages let three blocks share an SM.
+int moe_nt(int64_t T, int64_t E, int64_t top_k) { return T <= 8 ? 1 : T * top_k <= 28 * E ? 2 : 4; }
+// Their ring: three blocks per SM by shared memory where registers allow it, and the next launch's blocks
+// find room early (33 tokens over 64 experts: 123 us against 140 with two), else the deepest that two
+// hold (one token over 32 experts: 25.3 us against 26.0).
+int moe_ring(int64_t T, int nt) { return T <= 8 || nt == 4 ? DEC_SMEM : 66 * 1024; }
+// Blocks of the down product: clusters of `cluster` over the list of (segment, chunk), `splits` of them.
+struct DownSplit {
+  int cluster, splits;
+};
+DownSplit down_split(int64_t H, int64_t I, int64_t experts) {
+  DownSplit d;
+  const int tiles = static_cast<int>(H / DEC_ROWS), chunks = static_cast<int>(experts * (I / 128));
+  d.cluster = k_split(tiles, chunks);
+  d.splits = std::max(1, std::min(2 * kSms / (tiles * d.cluster), chunks / (4 * d.cluster)));
+  return d;
+}
 
 struct MoeLayout {
   int max_segments, max_tiles;
-  size_t logits, ids, weights, segments, tiles, expert, begin, count, tile0, tile_seg, pair, pweight, x, h, total;
+  DownSplit down;
+  size_t logits, ids, weights, segments, tiles, expert, begin, count, tile0, tile_seg, pair, pweight, x, h, partial, tickets, total;
 };
 bool moe_layout(int64_t T, int64_t E, int64_t top_k, int64_t H, int64_t I, MoeLayout* l) {
   if (T < 0 || T > MOE_MAX_T || E < 1 || E > MOE_MAX_E || top_k < 1 || top_k > E || top_k > MOE_MAX_TOPK ||
@@ -257,7 +283,7 @@ bool moe_layout(int64_t T, int64_t E, int64_t top_k, int64_t H, int64_t I, MoeLa
   };
   const int64_t pairs = T * top_k;
   // experts with a token, and what more than one segment (tile) of an expert adds
-  l->max_segments = static_cast<int>(std::min(pairs, std::min(E, pairs) + pairs / (8 * moe_nt(T))));
+  l->max_segments = static_cast<int>(std::min(pairs, std::min(E, pairs) + pairs / (8 * moe_nt(T, E, top_k))));
   l->max_tiles = static_cast<int>(std::min(pairs, std::min(E, pairs) + pairs / 8));
   l->logits = take(static_cast<size_t>(T) * E * 8);
   l->ids = take(pairs * 4);
@@ -273,6 +299,9 @@ bool moe_layout(int64_t T, int64_t E, int64_t top_k, int64_t H, int64_t I, MoeLa
   l->pweight = take(pairs * 4);
   l->x = take(static_cast<size_t>(l->max_tiles) * (H / 128) * FRAG_BYTES);
   l->h = take(static_cast<size_t>(l->max_tiles) * (I / 128) * FRAG_BYTES);
+  l->down = down_split(H, I, std::max<int64_t>(1, std::min(E, pairs)));
+  l->partial = take(l->down.splits > 1 ? static_cast<size_t>(l->down.splits) * T * H * 4 : 0);
+  l->tickets = take(l->down.splits > 1 ? static_cast<size_t>(H / DEC_ROWS) * l->down.cluster * 4 : 0);
   l->total = off;
   return true;
 }
@@ -337,6 +366,7 @@ extern "C" gptq_status gptq_dequant_linear(const gptq_linear_args* args, int dev
   d.m = m;
   d.chunks = n / 128;
   d.G = n / g;
+  d.vec = param_vec(a.W);
   d.gi = group_index(g);
   d.scales = a.W.scales;
   d.zeros = a.W.zeros;
@@ -354,6 +384,7 @@ extern "C" gptq_status gptq_dequant_linear(const gptq_linear_args* args, int dev
   l.bf16 = a.dtype == GPTQ_BF16;
   l.unit = std::min(g, 128);
   l.nt = d.tiles;
+  l.ring = DEC_SMEM;
   l.cluster = k_split((m + DEC_ROWS - 1) / DEC_ROWS, d.chunks);
   l.device = device;
   l.stream = st;
@@ -537,7 +568,7 @@ extern "C" gptq_status gptq_dequant_moe(const gptq_moe_args* args, int device, v
   r.H = static_cast<int>(H);
   r.top_k = a.top_k;
   r.renorm = a.renormalize;
-  r.seg_pairs = 8 * moe_nt(a.T);
+  r.seg_pairs = 8 * moe_nt(a.T, a.E, a.top_k);
   r.logits = reinterpret_cast<double*>(ws + lay.logits);
   r.ids = reinterpret_cast<int32_t*>(ws + lay.ids);
   r.weights = reinterpret_cast<float*>(ws + lay.weights);
@@ -552,6 +583,8 @@ extern "C" gptq_status gptq_dequant_moe(const gptq_moe_args* args, int device, v
   r.plan.tile_seg = reinterpret_cast<int*>(ws + lay.tile_seg);
   r.plan.pair = reinterpret_cast<int*>(ws + lay.pair);
   r.plan.weight = reinterpret_cast<float*>(ws + lay.pweight);
+  r.tickets = reinterpret_cast<int*>(ws + lay.tickets);
+  r.ntickets = lay.down.splits > 1 ? static_cast<int>(H / DEC_ROWS) * lay.down.cluster : 0;
   r.status = reinterpret_cast<int*>(ws);
   CUtensorMap gmap, dmap;
   gptq_status s = encode_codes(&gmap, a.gate_up, 64, a.E);
@@ -563,7 +596,8 @@ extern "C" gptq_status gptq_dequant_moe(const gptq_moe_args* args, int device, v
   const int gg = group_width(a.gate_up), gd = group_width(a.down);
   DecodeLaunch l;
   l.bf16 = bf;
-  l.nt = moe_nt(a.T);
+  l.nt = moe_nt(a.T, a.E, a.top_k);
+  l.ring = moe_ring(a.T, l.nt);
   l.device = device;
   l.stream = st;
   l.unit = std::min(gg, 128);
@@ -592,12 +626,17 @@ extern "C" gptq_status gptq_dequant_moe(const gptq_moe_args* args, int device, v
   m.dn_zeros = a.down.zeros;
   m.gu_G = m.H / gg;
   m.dn_G = m.I / gd;
+  m.gu_vec = param_vec(a.gate_up);
+  m.dn_vec = param_vec(a.down);
   m.gu_gi = group_index(gg);
   m.dn_gi = group_index(gd);
   m.act = a.act;
   m.dn_unit = std::min(gd, 128);
   m.h = ws + lay.h;
   m.status = r.status;
+  m.splits = lay.down.splits;
+  m.partial = reinterpret_cast<float*>(ws + lay.partial);
+  m.tickets = r.tickets;
   m.residual = static_cast<const uint16_t*>(a.residual);
   m.ld_res = a.ld_res;
   m.ldy = a.ld_y;
@@ -606,7 +645,7 @@ extern "C" gptq_status gptq_dequant_moe(const gptq_moe_args* args, int device, v
              [&](auto b) { return launch_moe_gate_up<decltype(b)::value>(l, gmap, m, lay.max_segments); }));
   l.unit = m.dn_unit;
   l.local = 0;
-  l.cluster = k_split(m.H / DEC_ROWS, static_cast<int>(std::min<int64_t>(a.E, pairs)) * (m.I / 128));
+  l.cluster = lay.down.cluster;
   CK(by_bits(a.down.qp.bits, [&](auto b) { return launch_moe_down<decltype(b)::value>(l, dmap, m); }));
   return GPTQ_OK;
 }

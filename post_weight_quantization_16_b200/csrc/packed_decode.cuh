@@ -401,15 +401,17 @@ constexpr int DEC_WARPS = 8;                        // consumer warps: 16 rows e
 constexpr int DEC_ROWS = 16 * DEC_WARPS;            // rows of a block
 constexpr int DEC_THREADS = (DEC_WARPS + 1) * 32;   // and the producer warp
 constexpr int DEC_MAX_STAGES = 12;
-constexpr int DEC_SMEM = 94 * 1024;                 // ring of a block: two blocks per SM
+constexpr int DEC_SMEM = 94 * 1024;                 // ring of a block at most: two blocks per SM
 
 __host__ __device__ constexpr int dec_code_bytes(int bits) { return DEC_ROWS * 16 * bits; }
 __host__ __device__ constexpr int dec_stage_bytes(int bits, int nt) { return dec_code_bytes(bits) + nt * FRAG_BYTES; }
-__host__ __device__ constexpr int dec_stages(int bits, int nt) {
-  const int s = DEC_SMEM / dec_stage_bytes(bits, nt);
+__host__ __device__ constexpr int dec_stages(int bits, int nt, int smem) {
+  const int s = smem / dec_stage_bytes(bits, nt);
   return s > DEC_MAX_STAGES ? DEC_MAX_STAGES : s;
 }
-__host__ __device__ constexpr int dec_ring_bytes(int bits, int nt) { return 128 + dec_stages(bits, nt) * dec_stage_bytes(bits, nt); }
+__host__ __device__ constexpr int dec_ring_bytes(int bits, int nt, int smem) {
+  return 128 + dec_stages(bits, nt, smem) * dec_stage_bytes(bits, nt);
+}
 
 // Start of the dynamic shared memory at the next multiple of 128 bytes.
 __device__ __forceinline__ uint8_t* align128(uint8_t* raw) {
@@ -437,32 +439,33 @@ template <int BITS, bool BF, int GU, int NT, bool XL>
 struct Ring {
   using Raw = RawChunk<BITS, GU>;
   static constexpr int UNITS = Raw::UNITS, BLOCKS = Raw::BLOCKS;
-  static constexpr int STAGES = dec_stages(BITS, XL ? 0 : NT), STAGE = dec_stage_bytes(BITS, XL ? 0 : NT),
-                       CODES = dec_code_bytes(BITS);
+  static constexpr int STAGE = dec_stage_bytes(BITS, XL ? 0 : NT), CODES = dec_code_bytes(BITS);
   static_assert(!XL || NT == 1, "local activations: one tile");
 
   uint32_t base, full, empty;  // shared-memory addresses: stages, barriers
+  int stages;
   volatile int* abort_flag;
 
   // Position in the ring: stage and the parity of its use.
   struct Cursor {
     int s = 0;
     uint32_t ph = 0;
-    __device__ __forceinline__ void next() {
-      if (++s == STAGES) {
+    __device__ __forceinline__ void next(int stages) {
+      if (++s == stages) {
         s = 0;
         ph ^= 1u;
       }
     }
   };
 
-  __device__ __forceinline__ void init(uint32_t smem_base, uint64_t* bars, int* flag) {
+  __device__ __forceinline__ void init(uint32_t smem_base, int n, uint64_t* bars, int* flag) {
+    stages = n;
     base = smem_base;
     full = smem_u32(bars);
-    empty = full + 8 * STAGES;
+    empty = full + 8 * stages;
     abort_flag = flag;
     if (threadIdx.x == 0) {
-      for (int s = 0; s < STAGES; ++s) {
+      for (int s = 0; s < stages; ++s) {
         mbar_init(full + 8 * s, 1);
         mbar_init(empty + 8 * s, DEC_WARPS);
       }
@@ -474,8 +477,8 @@ struct Ring {
 
   // Producer (one lane).  `it` counts stages over all segments of the block.
   __device__ __forceinline__ bool codes(const CUtensorMap* map, const Segment& g, int c, int it) const {
-    const int s = it % STAGES;
-    if (!mbar_wait_bounded(empty + 8 * s, (static_cast<uint32_t>(it / STAGES) & 1u) ^ 1u, abort_flag)) return false;
+    const int s = it % stages;
+    if (!mbar_wait_bounded(empty + 8 * s, (static_cast<uint32_t>(it / stages) & 1u) ^ 1u, abort_flag)) return false;
     const uint32_t fb = full + 8 * s, st = base + s * STAGE;
     mbar_arrive_expect_tx(fb, static_cast<uint32_t>(CODES + (XL ? 0 : g.tiles * FRAG_BYTES)));
     tma_load_2d(st, map, fb, c * (4 * BITS), g.row_a);
@@ -484,14 +487,14 @@ struct Ring {
   }
   __device__ __forceinline__ void acts(const Segment& g, int c, int it) const {
     if (XL) return;
-    const int s = it % STAGES;
+    const int s = it % stages;
     bulk_load(base + s * STAGE + CODES, g.x + static_cast<size_t>(c) * g.tiles * FRAG_BYTES,
               static_cast<uint32_t>(g.tiles * FRAG_BYTES), full + 8 * s);
   }
   // No copy may be in flight when the block leaves.
   __device__ __forceinline__ void drain(int issued) const {
-    for (int i = max(0, issued - STAGES); i < issued; ++i)
-      mbar_wait_drain(full + 8 * (i % STAGES), static_cast<uint32_t>(i / STAGES) & 1u);
+    for (int i = max(0, issued - stages); i < issued; ++i)
+      mbar_wait_drain(full + 8 * (i % stages), static_cast<uint32_t>(i / stages) & 1u);
   }
 
   // Local activations: pieces [chunk][block][token][quad position] of 16 bytes.
@@ -510,21 +513,47 @@ struct Ring {
   }
 
   // Consumer warp.  A lane fetches one of the four parameter rows of its quad's two weight rows:
-  // q = 0 scales of row a, 1 its zero-points, 2 and 3 those of row b; four consecutive units at a
-  // time, one window ahead (a window of a row is mostly one 32-byte sector); shuffles spread them.
+  // q = 0 scales of row a, 1 its zero-points, 2 and 3 those of row b; four units (a window) at a time,
+  // one window ahead; shuffles spread them.  The 32 lanes' addresses lie in 32 cache lines whatever a
+  // load's width, and the L1's tag lookups for them are what a load costs: with one load of 16 bytes
+  // instead of four of 4 the gate and up product of 64 experts took 56 us, not 65 (3 bits, groups of
+  // 64), and that of eight large ones 139, not 158.
   const float* param;
+  int pitch;  // units of a parameter row
+  int vec;    // values that a load can take by the rows' alignment: 4, 2 or 1
   GroupIndex gi;
-  // `left` units remain from unit `u0` of chunk c0 on.
-  __device__ __forceinline__ void window(float (&v)[4], int c0, int u0, int left) const {
+  // Units 4 w .. 4 w + 3 of the rows; chunks c0 .. c1 - 1 are wanted.
+  __device__ __forceinline__ void window(float (&v)[4], int w, int c0, int c1) const {
     if (UNITS > 1 || gi.div == 1) {
-      const float* at = param + c0 * UNITS + u0;
+      const float* at = param + 4 * w;
+      if (vec == 4) {
+        const float4 x = __ldg(reinterpret_cast<const float4*>(at));
+        v[0] = x.x;
+        v[1] = x.y;
+        v[2] = x.z;
+        v[3] = x.w;
+      } else if (vec == 2) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (j < left) v[j] = __ldg(at + j);
-    } else {
+        for (int j = 0; j < 4; j += 2) {
+          if (4 * w + j < pitch) {
+            const float2 x = __ldg(reinterpret_cast<const float2*>(at + j));
+            v[j] = x.x;
+            v[j + 1] = x.y;
+          }
+        }
+      } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (j < left) v[j] = __ldg(param + group_of<GU>(gi, c0 + u0 + j, 0));
+        for (int j = 0; j < 4; ++j)
+          if (4 * w + j < pitch) v[j] = __ldg(at + j);
+      }
+    } else {  // a group of several chunks: one load
+      int of = -1;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int g = group_of<GU>(gi, min(max(4 * w + j, c0), c1 - 1), 0);
+        v[j] = j > 0 && g == of ? v[j > 0 ? j - 1 : 0] : __ldg(param + g);
+        of = g;
+      }
     }
   }
 
@@ -537,18 +566,17 @@ struct Ring {
     const int q = lane & 3, src = lane & 28;
     uint32_t xat = XL ? xs + static_cast<uint32_t>((min(lane >> 2, xtok - 1) * 4 + q) * 16) : 0u;
     const uint32_t xstep = XL ? static_cast<uint32_t>(xtok * 64) : 0u;
-    int left = (c1 - c0) * UNITS, u0 = 0;
+    const int w1 = (c1 + PER - 1) / PER;
     float next[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    window(next, c0, 0, left);
-    while (left > 0) {
+    window(next, c0 / PER, c0, c1);
+    for (int w = c0 / PER; w < w1; ++w) {
       float now[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) now[j] = next[j];
-      u0 += 4;
-      window(next, c0, u0, left - 4);
+      if (w + 1 < w1) window(next, w + 1, c0, c1);
 #pragma unroll
       for (int jj = 0; jj < PER; ++jj) {
-        if (jj * UNITS < left) {
+        if (w * PER + jj >= c0 && w * PER + jj < c1) {
           if (!warp_wait_uniform(full + 8 * cur.s, cur.ph, abort_flag)) return false;
           const uint32_t st = base + cur.s * STAGE;
           Raw ra, rb;
@@ -593,10 +621,9 @@ struct Ring {
           asm volatile("fence.acq_rel.cta;" ::: "memory");
           __syncwarp();
           if (lane == 0) mbar_arrive(empty + 8 * cur.s);
-          cur.next();
+          cur.next(stages);
         }
       }
-      left -= 4;
     }
     return true;
   }
@@ -641,7 +668,8 @@ struct LinearDecodeArgs {
   int64_t ldx;
   const int32_t* perm;
   const float *scales, *zeros;
-  int T, tiles, m, chunks, G;
+  int stages;  // of the ring
+  int T, tiles, m, chunks, G, vec;
   GroupIndex gi;
   const uint16_t *bias, *residual;
   int64_t ld_res, ldy;
@@ -663,7 +691,7 @@ __global__ void __launch_bounds__(DEC_THREADS)
   const int cs = static_cast<int>(cluster_nctarank()), rank = static_cast<int>(cluster_ctarank());
   const int row0 = static_cast<int>(blockIdx.x) / cs * DEC_ROWS;
   Ring<BITS, BF, GU, NT, XL> r;
-  r.init(smem_u32(dec_smem), bars, &abort_flag);
+  r.init(smem_u32(dec_smem), p.stages, bars, &abort_flag);
   Segment sg;
   sg.row_a = row0;
   sg.row_b = row0 + 64;
@@ -677,7 +705,7 @@ __global__ void __launch_bounds__(DEC_THREADS)
   }
   if (warp == DEC_WARPS) {
     if (lane == 0) {
-      const int n = sg.c1 - sg.c0, ahead = min(Ring<BITS, BF, GU, NT, XL>::STAGES, n);
+      const int n = sg.c1 - sg.c0, ahead = min(r.stages, n);
       int it = 0;
       // the launch before this one laid out x and had waited for all earlier work: the weights can
       // be read before it ends, x cannot
@@ -700,9 +728,11 @@ __global__ void __launch_bounds__(DEC_THREADS)
     const int ra = warp * 16 + g, rb = ra + 8;
     // (rows past m repeat the last one's parameters, unstored)
     r.param = ((q & 1) ? p.zeros : p.scales) + static_cast<size_t>(min(row0 + ((q & 2) ? rb : ra), p.m - 1)) * p.G;
+    r.pitch = p.G;
+    r.vec = p.vec;
     r.gi = p.gi;
     if (XL)
-      r.lay_out(reinterpret_cast<uint4*>(dec_smem + dec_ring_bytes(BITS, 0) - 128), sg.c0, sg.c1, p.T, p.perm,
+      r.lay_out(reinterpret_cast<uint4*>(dec_smem + p.stages * dec_stage_bytes(BITS, 0)), sg.c0, sg.c1, p.T, p.perm,
                 [&](int n) { return p.X + n * p.ldx; });
     typename Ring<BITS, BF, GU, NT, XL>::Cursor cur;
     r.template consume<NT>(sg.c0, sg.c1, ra * (16 * BITS), rb * (16 * BITS), lane, cur, acc);
@@ -779,12 +809,16 @@ struct MoeArgs {
   int64_t ldx;
   const int32_t* perm;
   MoePlan plan;
+  int stages;      // of the ring
   int T, E, top_k, H, I;
   const float *gu_scales, *gu_zeros, *dn_scales, *dn_zeros;
-  int gu_G, dn_G;
+  int gu_G, dn_G, gu_vec, dn_vec;
   GroupIndex gu_gi, dn_gi;
   int act, dn_unit;
   uint8_t* h;  // fragment order, as x with I / 128 chunks
+  int splits;      // of the down product's list, beyond the cluster's
+  float* partial;  // splits > 1: [splits][T][H]
+  int* tickets;    // and a count per block of a split, zero before the call's down product
   const uint16_t* residual;
   int64_t ld_res, ldy;
   uint16_t* Y;
@@ -806,7 +840,7 @@ __global__ void __launch_bounds__(DEC_THREADS)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   const int cs = static_cast<int>(cluster_nctarank()), rank = static_cast<int>(cluster_ctarank());
   Ring<BITS, BF, GU, NT, XL> r;
-  r.init(smem_u32(dec_smem), bars, &abort_flag);
+  r.init(smem_u32(dec_smem), p.stages, bars, &abort_flag);
   griddep_wait();
   griddep_launch_dependents();
   const int seg = static_cast<int>(blockIdx.y);
@@ -838,9 +872,11 @@ __global__ void __launch_bounds__(DEC_THREADS)
       for (int j = 0; j < 4; ++j) acc[t][j] = 0.0f;
     const int ra = warp * 8 + g;
     r.param = ((q & 1) ? p.gu_zeros : p.gu_scales) + static_cast<size_t>(((q & 2) ? sg.row_b : sg.row_a) + ra) * p.gu_G;
+    r.pitch = p.gu_G;
+    r.vec = p.gu_vec;
     r.gi = p.gu_gi;
     if (XL)
-      r.lay_out(reinterpret_cast<uint4*>(dec_smem + dec_ring_bytes(BITS, 0) - 128), sg.c0, sg.c1, count,
+      r.lay_out(reinterpret_cast<uint4*>(dec_smem + p.stages * dec_stage_bytes(BITS, 0)), sg.c0, sg.c1, count,
                 p.perm ? p.perm + static_cast<size_t>(e) * p.H : nullptr,
                 [&](int n) { return p.X + p.plan.pair[p.plan.begin[seg] + n] / p.top_k * p.ldx; });
     typename Ring<BITS, BF, GU, NT, XL>::Cursor cur;
@@ -881,28 +917,32 @@ __global__ void __launch_bounds__(DEC_THREADS)
 // y = sum over the token's experts of weight * h Wd^T, + residual.  A block owns 128 output rows of
 // every expert and, in a cluster, an even share of the list of (segment, chunk); each segment's
 // sums are added, times the routing weight, into a row per token in shared memory (a warp owns its
-// 16 columns of it); the shares meet over the cluster in a fixed order.  One pass, no sums in global
-// memory, no atomics.
+// 16 columns of it); the shares meet over the cluster in a fixed order.  Where the row tiles and
+// clusters of eight leave SMs idle, grid.y splits the list further: each split's block leaves its
+// sums in `partial`, and the last of them to come adds all in their order, so the result does not
+// depend on which it was (33 tokens over 64 experts: 41 us against 63 on the 64 SMs that 16 clusters of
+// eight are packed on; clusters of 16 gained half as much).
 template <int BITS, bool BF, int GU, int NT>
 __global__ void __launch_bounds__(DEC_THREADS)
     moe_down_kernel(const __grid_constant__ CUtensorMap codes_map, const MoeArgs p) {
   extern __shared__ uint8_t dec_smem_raw[];  // ring, then float [T][DEC_ROWS]
   __shared__ __align__(8) uint64_t bars[2 * DEC_MAX_STAGES];
-  __shared__ int abort_flag;
+  __shared__ int abort_flag, last;
   uint8_t* dec_smem = align128(dec_smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   const int cs = static_cast<int>(cluster_nctarank()), rank = static_cast<int>(cluster_ctarank());
   const int row0 = static_cast<int>(blockIdx.x) / cs * DEC_ROWS;
-  float* ysum = reinterpret_cast<float*>(dec_smem + dec_ring_bytes(BITS, NT) - 128);
+  float* ysum = reinterpret_cast<float*>(dec_smem + p.stages * dec_stage_bytes(BITS, NT));
   for (int i = threadIdx.x; i < p.T * DEC_ROWS; i += DEC_THREADS) ysum[i] = 0.0f;
   Ring<BITS, BF, GU, NT, false> r;
-  r.init(smem_u32(dec_smem), bars, &abort_flag);
+  r.init(smem_u32(dec_smem), p.stages, bars, &abort_flag);
   griddep_wait();
   griddep_launch_dependents();
   const int chunks = p.I / 128;
   const int total = *p.plan.segments * chunks;
-  const int w0 = static_cast<int>(static_cast<int64_t>(total) * rank / cs);
-  const int w1 = static_cast<int>(static_cast<int64_t>(total) * (rank + 1) / cs);
+  const int share = static_cast<int>(blockIdx.y) * cs + rank, shares = p.splits * cs;
+  const int w0 = static_cast<int>(static_cast<int64_t>(total) * share / shares);
+  const int w1 = static_cast<int>(static_cast<int64_t>(total) * (share + 1) / shares);
   auto segment_at = [&](int w, int& seg) {
     Segment sg;
     seg = w / chunks;
@@ -934,6 +974,8 @@ __global__ void __launch_bounds__(DEC_THREADS)
     }
   } else {
     typename Ring<BITS, BF, GU, NT, false>::Cursor cur;
+    r.pitch = p.dn_G;
+    r.vec = p.dn_vec;
     r.gi = p.dn_gi;
     const int ra = warp * 16 + g, rb = ra + 8;
     for (int w = w0; w < w1;) {
@@ -968,13 +1010,37 @@ __global__ void __launch_bounds__(DEC_THREADS)
   } else {
     __syncthreads();
   }
-  for (int i = rank * DEC_THREADS + static_cast<int>(threadIdx.x); i < p.T * DEC_ROWS && !abort_flag;
-       i += cs * DEC_THREADS) {
-    float v = 0.0f;
-    for (int o = 0; o < cs; ++o) v += cs > 1 ? ld_dsmem_f(mapa_shared(smem_u32(&ysum[i]), o)) : ysum[i];
+  const int first = rank * DEC_THREADS + static_cast<int>(threadIdx.x), stride = cs * DEC_THREADS;
+  auto finish = [&](int i, float v) {
     const int tok = i / DEC_ROWS, row = row0 + i % DEC_ROWS;
     if (p.residual) v += h2f<BF>(p.residual[static_cast<size_t>(tok) * p.ld_res + row]);
     p.Y[static_cast<size_t>(tok) * p.ldy + row] = f2h<BF>(v);
+  };
+  // (rows of `partial` hold T * H sums)
+  auto at = [&](int split, int i) {
+    return p.partial + (static_cast<size_t>(split) * p.T + i / DEC_ROWS) * p.H + row0 + i % DEC_ROWS;
+  };
+  for (int i = first; i < p.T * DEC_ROWS && !abort_flag; i += stride) {
+    float v = 0.0f;
+    for (int o = 0; o < cs; ++o) v += cs > 1 ? ld_dsmem_f(mapa_shared(smem_u32(&ysum[i]), o)) : ysum[i];
+    if (p.splits == 1)
+      finish(i, v);
+    else
+      __stcg(at(static_cast<int>(blockIdx.y), i), v);
+  }
+  if (p.splits > 1) {
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) last = atomicAdd(p.tickets + blockIdx.x, 1) == p.splits - 1;
+    __syncthreads();
+    if (last) {
+      __threadfence();
+      for (int i = first; i < p.T * DEC_ROWS && !abort_flag; i += stride) {
+        float v = 0.0f;
+        for (int o = 0; o < p.splits; ++o) v += __ldcg(at(o, i));
+        finish(i, v);
+      }
+    }
   }
   if (cs > 1) cluster_sync();
   if (threadIdx.x == 0 && abort_flag) atomicOr(p.status, ST_TIMEOUT);
@@ -990,16 +1056,17 @@ struct DecodeLaunch {
   int local;     // tokens whose activations the blocks lay out themselves (nt = 1), 0: none
   int chunks;    // chunks of a block at most (local)
   int cluster;   // blocks that split k
+  int ring;      // bytes of the ring at most
   int device;
   cudaStream_t stream;
 };
 
 template <int BITS>
-cudaError_t launch_linear_decode(const DecodeLaunch& l, const CUtensorMap& codes, const LinearDecodeArgs& a);
+cudaError_t launch_linear_decode(const DecodeLaunch& l, const CUtensorMap& codes, LinearDecodeArgs& a);
 template <int BITS>
-cudaError_t launch_moe_gate_up(const DecodeLaunch& l, const CUtensorMap& codes, const MoeArgs& a, int segments);
+cudaError_t launch_moe_gate_up(const DecodeLaunch& l, const CUtensorMap& codes, MoeArgs& a, int segments);
 template <int BITS>
-cudaError_t launch_moe_down(const DecodeLaunch& l, const CUtensorMap& codes, const MoeArgs& a);
+cudaError_t launch_moe_down(const DecodeLaunch& l, const CUtensorMap& codes, MoeArgs& a);
 
 // A launch that may overlap the end of the kernel before it (every kernel here waits for that
 // kernel before it touches what it wrote).

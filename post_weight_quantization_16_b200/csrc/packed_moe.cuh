@@ -83,6 +83,8 @@ struct RouterArgs {
   int32_t* ids_out;    // the caller's copies, or null
   float* weights_out;
   MoePlan plan;
+  int* tickets;        // of the down product, set to zero here
+  int ntickets;
   int* status;
 };
 
@@ -105,6 +107,7 @@ __global__ void __launch_bounds__(ROUTER_WARPS * 32) moe_router_kernel(const Rou
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   const int rank = static_cast<int>(cluster_ctarank());
   if (rank == 0 && threadIdx.x == 0) *p.status = 0;
+  for (int i = rank * ROUTER_WARPS * 32 + threadIdx.x; i < p.ntickets; i += ROUTER_CLUSTER * ROUTER_WARPS * 32) p.tickets[i] = 0;
   const int et = (p.E + 15) / 16, tt = (p.T + 7) / 8, blocks = p.H / 32;
   constexpr int KW = ROUTER_WARPS / 2;  // warps of a tile
   const int half = warp / KW, kw = warp % KW;

@@ -100,6 +100,10 @@ CASES = [
     (100, 7, 1, 384, 128, 4, 128, 128, "fp16", "silu", True, True),
     (128, 64, 8, 256, 128, 3, 128, 32, "fp16", "silu", True, True),
     (128, 1, 1, 256, 384, 4, 128, 128, "bf16", "silu", True, True),
+    (128, 2, 2, 256, 256, 3, 32, 128, "fp16", "silu", True, True),
+    (127, 3, 1, 384, 512, 8, 64, 64, "bf16", "gelu", False, True),
+    (90, 3, 1, 256, 256, 2, -1, 32, "bf16", "silu", True, False),
+    (30, 256, 16, 128, 128, 4, 32, 64, "fp16", "silu", True, True),
     (48, 8, 2, 2048, 1408, 4, 128, 128, "bf16", "none", True, True),
 ]
 
