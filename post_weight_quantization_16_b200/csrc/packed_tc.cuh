@@ -19,7 +19,9 @@
 // 128: the MMAs take 512 cycles, unpacking about 320 of the integer pipes, the drain 128: all three
 // overlap.  The blocks of a cluster split k when there are few tiles; their sums meet over
 // distributed shared memory in a fixed order, in the epilogue that also adds the bias, applies the
-// activation and adds the residual: one launch, deterministic.
+// activation and adds the residual: one launch, deterministic.  77 tokens through 11008 x 4096 with 3
+// bits take 39 us (the bytes and the products would take 4): 32 chunks of unpacking, hand-over and drain
+// one behind the other in 86 blocks; 500 tokens' gradient through 4096 x 4096 43 us.
 //
 // Gradient: dX[t][perm[k]] = scale_t * sum over rows r of W16[r][k] * dz[t][r],
 //     W16 = fp16( fp32(u - z) * s ),   dz[t][r] = dY[t][r] act'(Z[t][r]) / scale_t  in fp16
