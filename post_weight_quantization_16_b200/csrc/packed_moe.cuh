@@ -89,22 +89,27 @@ struct RouterArgs {
   int* status;
 };
 
-// One cluster.  (1) Logits: tiles of 16 experts x 8 tokens go round the blocks, two at a time; a
-// tile's eight warps split H; products of 16-bit values are exact in fp32, 128 columns are summed on the tensor cores
-// and the partial sums of those in fp64, so the order of the choices is that of the 64-bit logits
-// but for logits that agree to about 1e-7.  (2) Softmax and top-k: a warp per token, in fp64; equal
-// values go to the lower expert; a NaN logit is chosen last (its weights are NaN).  (3) The lists:
-// block 0, a warp per expert, by ballots over the T * top_k choices, so positions are deterministic.
-// 14 us for one token over 32 experts, 23 for 33 over 64 (2048 wide, profiled alone): a chain of trips
-// to memory and cluster barriers, with little in each.
+// One cluster.  (1) Logits: tiles of 16 experts x 8 tokens go round the blocks, as many at a time as a
+// round of all needs; a tile's warps split H; products of 16-bit values are exact in fp32, 128 columns
+// are summed on the tensor cores and the partial sums of those in fp64, so the order of the choices is
+// that of the 64-bit logits but for logits that agree to about 1e-7.  (2) Softmax and top-k: a warp per
+// token, in fp64; equal values go to the lower expert; a NaN logit is chosen last (its weights are
+// NaN).  (3) The lists, in block 0: a thread per choice, whose place is what its expert has before its
+// group of 32 choices and its rank inside it, so positions are deterministic.
+// By its own clock: 7 us for two tokens over 32 experts (2048 wide), 18 for 33 over 64, of which 9 are the
+// logits (eight SMs fetch R and X, four trips to memory each), 5 the softmax and the choices, 4 the
+// lists and barriers (lists by a warp per expert took 7 more).
 template <bool BF>
 __global__ void __launch_bounds__(ROUTER_WARPS * 32) moe_router_kernel(const RouterArgs p) {
-  __shared__ double red[ROUTER_WARPS][128];
+  constexpr int CHOICES = MOE_MAX_T * MOE_MAX_TOPK, MINE = CHOICES / (ROUTER_WARPS * 32);
+  __shared__ union {
+    double red[ROUTER_WARPS][128];             // (1)
+    uint16_t before[CHOICES / 32 * MOE_MAX_E];  // (3) [group of choices][expert]
+  } sh;
   __shared__ int counts[MOE_MAX_E];
   __shared__ int begins[MOE_MAX_E];
   __shared__ int slots[MOE_MAX_E];
   __shared__ int tiles[MOE_MAX_E];
-  __shared__ int chosen_ids[MOE_MAX_T * MOE_MAX_TOPK];
   griddep_wait();
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
@@ -112,25 +117,38 @@ __global__ void __launch_bounds__(ROUTER_WARPS * 32) moe_router_kernel(const Rou
   if (rank == 0 && threadIdx.x == 0) *p.status = 0;
   for (int i = rank * ROUTER_WARPS * 32 + threadIdx.x; i < p.ntickets; i += ROUTER_CLUSTER * ROUTER_WARPS * 32) p.tickets[i] = 0;
   const int et = (p.E + 15) / 16, tt = (p.T + 7) / 8, blocks = p.H / 32;
-  constexpr int KW = ROUTER_WARPS / 2;  // warps of a tile
-  const int half = warp / KW, kw = warp % KW;
-  for (int first = rank * 2; first < et * tt; first += ROUTER_CLUSTER * 2) {
-    const int tile = min(first + half, et * tt - 1);  // (an odd last tile is computed twice, alike)
+  const int ntiles = et * tt;
+  int at_once = 1;  // tiles of a block
+  while (at_once < ROUTER_WARPS && at_once * ROUTER_CLUSTER < ntiles) at_once *= 2;
+  const int KW = ROUTER_WARPS / at_once, slot = warp / KW, kw = warp % KW;  // warps of a tile
+  for (int first = rank * at_once; first < ntiles; first += ROUTER_CLUSTER * at_once) {
+    const int tile = min(first + slot, ntiles - 1);  // (past the last: computed again, alike)
     const int e0 = (tile % et) * 16, t0 = (tile / et) * 8;
     const uint16_t* ra = p.R + static_cast<size_t>(min(e0 + g, p.E - 1)) * p.H + q * 8;
     const uint16_t* rb = p.R + static_cast<size_t>(min(e0 + g + 8, p.E - 1)) * p.H + q * 8;
     const uint16_t* x = p.X + static_cast<size_t>(min(t0 + g, p.T - 1)) * p.ldx + q * 8;
     double acc[4] = {0.0, 0.0, 0.0, 0.0};
     const int b0 = blocks * kw / KW, b1 = blocks * (kw + 1) / KW;
+    uint4 na[4], nb[4], nx[4];
+    auto load = [&](int b) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int at = min(b + j, b1 - 1) * 32;
+        na[j] = *reinterpret_cast<const uint4*>(ra + at);
+        nb[j] = *reinterpret_cast<const uint4*>(rb + at);
+        nx[j] = *reinterpret_cast<const uint4*>(x + at);
+      }
+    };
+    if (b0 < b1) load(b0);
     for (int b = b0; b < b1; b += 4) {
       uint4 va[4], vb[4], vx[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int at = min(b + j, b1 - 1) * 32;
-        va[j] = *reinterpret_cast<const uint4*>(ra + at);
-        vb[j] = *reinterpret_cast<const uint4*>(rb + at);
-        vx[j] = *reinterpret_cast<const uint4*>(x + at);
+        va[j] = na[j];
+        vb[j] = nb[j];
+        vx[j] = nx[j];
       }
+      if (b + 4 < b1) load(b + 4);
       float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -143,17 +161,15 @@ __global__ void __launch_bounds__(ROUTER_WARPS * 32) moe_router_kernel(const Rou
       for (int j = 0; j < 4; ++j) acc[j] += static_cast<double>(d[j]);
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) red[warp][lane * 4 + j] = acc[j];
+    for (int j = 0; j < 4; ++j) sh.red[warp][lane * 4 + j] = acc[j];
     __syncthreads();
-    if (threadIdx.x < 256) {
-      const int hh = threadIdx.x >> 7, i = threadIdx.x & 127;
-      const int mine = first + hh;
+    for (int k = threadIdx.x; k < at_once * 128; k += ROUTER_WARPS * 32) {
+      const int mine = first + (k >> 7), i = k & 127;
       double v = 0.0;
-#pragma unroll
-      for (int w = 0; w < KW; ++w) v += red[hh * KW + w][i];
+      for (int w = 0; w < KW; ++w) v += sh.red[(k >> 7) * KW + w][i];
       const int l = i >> 2, j = i & 3;
       const int e = (mine % et) * 16 + (l >> 2) + 8 * (j >> 1), t = (mine / et) * 8 + 2 * (l & 3) + (j & 1);
-      if (mine < et * tt && e < p.E && t < p.T) p.logits[static_cast<size_t>(t) * p.E + e] = v;
+      if (mine < ntiles && e < p.E && t < p.T) p.logits[static_cast<size_t>(t) * p.E + e] = v;
     }
     __syncthreads();
   }
@@ -186,6 +202,7 @@ __global__ void __launch_bounds__(ROUTER_WARPS * 32) moe_router_kernel(const Rou
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     int my_id = 0;
+    unsigned long long my_key = 0;
     for (int k = 0; k < p.top_k; ++k) {
       unsigned long long bk = 0;
       unsigned bi = 0xffffffffu;
@@ -202,17 +219,25 @@ __global__ void __launch_bounds__(ROUTER_WARPS * 32) moe_router_kernel(const Rou
 #pragma unroll
       for (int i = 0; i < PER; ++i)
         if (static_cast<unsigned>(lane + 32 * i) == id) key[i] = 0;
-      if (lane == k) my_id = static_cast<int>(id);
+      if (lane == k) {
+        my_id = static_cast<int>(id);
+        my_key = (static_cast<unsigned long long>(hi) << 32) | lo;
+      }
     }
     // (top_k <= E: every round finds an expert)
     double mine = 0.0;
-    if (lane < p.top_k) mine = exp(__ldcg(p.logits + static_cast<size_t>(t) * p.E + my_id) - best) / sum;
-    double chosen = mine;
+    if (lane < p.top_k) {
+      const unsigned long long u = (my_key >> 63) ? my_key & 0x7FFFFFFFFFFFFFFFull : ~my_key;
+      mine = my_key == 1ull ? __longlong_as_double(0x7FF8000000000000ll) : exp(__longlong_as_double(static_cast<long long>(u)) - best);
+    }
+    if (p.renorm) {
+      sum = mine;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) chosen += __shfl_xor_sync(0xffffffffu, chosen, o);
+      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    }
     if (lane < p.top_k) {
       const size_t o = static_cast<size_t>(t) * p.top_k + lane;
-      const float w = static_cast<float>(p.renorm ? mine / chosen : mine);
+      const float w = static_cast<float>(mine / sum);
       p.ids[o] = my_id;
       p.weights[o] = w;
       if (p.ids_out) p.ids_out[o] = my_id;
@@ -222,14 +247,39 @@ __global__ void __launch_bounds__(ROUTER_WARPS * 32) moe_router_kernel(const Rou
   cluster_sync();  // the choices are written
   if (rank != 0) return;
 
-  const int pairs = p.T * p.top_k;
-  for (int i = threadIdx.x; i < pairs; i += ROUTER_WARPS * 32) chosen_ids[i] = __ldcg(p.ids + i);
+  const int pairs = p.T * p.top_k, groups = (pairs + 31) / 32;
+  int id[MINE], place[MINE];
+  float weight[MINE];
+#pragma unroll
+  for (int j = 0; j < MINE; ++j) {
+    const int i = threadIdx.x + j * ROUTER_WARPS * 32;
+    id[j] = -1;
+    if (i < pairs) {
+      id[j] = __ldcg(p.ids + i);
+      weight[j] = __ldcg(p.weights + i);
+    }
+  }
+  for (int k = threadIdx.x; k < groups * p.E; k += ROUTER_WARPS * 32) sh.before[k] = 0;
   __syncthreads();
-  for (int e = warp; e < p.E; e += ROUTER_WARPS) {
+#pragma unroll
+  for (int j = 0; j < MINE; ++j) {
+    if (j * ROUTER_WARPS * 32 < pairs) {
+      const unsigned same = __match_any_sync(0xffffffffu, id[j]);
+      place[j] = __popc(same & ((1u << lane) - 1u));
+      if (id[j] >= 0 && place[j] == 0)
+        sh.before[(warp + j * ROUTER_WARPS) * p.E + id[j]] = static_cast<uint16_t>(__popc(same));
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x < p.E) {
     int n = 0;
-    for (int i = lane; i < (pairs + 31) / 32 * 32; i += 32)
-      n += __popc(__ballot_sync(0xffffffffu, i < pairs && chosen_ids[i] == e));
-    if (lane == 0) counts[e] = n;
+    for (int k = 0; k < groups; ++k) {
+      uint16_t& at = sh.before[k * p.E + threadIdx.x];
+      const int here = at;
+      at = static_cast<uint16_t>(n);
+      n += here;
+    }
+    counts[threadIdx.x] = n;
   }
   __syncthreads();
   if (warp == 0) {
@@ -265,20 +315,16 @@ __global__ void __launch_bounds__(ROUTER_WARPS * 32) moe_router_kernel(const Rou
     }
   }
   __syncthreads();
+#pragma unroll
+  for (int j = 0; j < MINE; ++j) {
+    if (id[j] >= 0) {
+      const int o = begins[id[j]] + sh.before[(warp + j * ROUTER_WARPS) * p.E + id[j]] + place[j];
+      p.plan.pair[o] = threadIdx.x + j * ROUTER_WARPS * 32;
+      p.plan.weight[o] = weight[j];
+    }
+  }
   for (int e = warp; e < p.E; e += ROUTER_WARPS) {
     const int n = counts[e];
-    if (n == 0) continue;
-    int at = begins[e];
-    for (int i = lane; i < (pairs + 31) / 32 * 32; i += 32) {
-      const bool mine = i < pairs && chosen_ids[i] == e;
-      const unsigned m = __ballot_sync(0xffffffffu, mine);
-      if (mine) {
-        const int o = at + __popc(m & ((1u << lane) - 1u));
-        p.plan.pair[o] = i;
-        p.plan.weight[o] = __ldcg(p.weights + i);
-      }
-      at += __popc(m);
-    }
     const int per = p.seg_pairs;  // a multiple of 8
     for (int k = lane; k * per < n; k += 32) {
       const int s = slots[e] + k;
