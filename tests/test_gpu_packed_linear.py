@@ -88,6 +88,8 @@ FORWARD = [
     (300, 9473, 256, 3, 32, "fp16", "gelu", False, True, False, True, False),
     (1030, 2570, 512, 2, 64, "bf16", "relu", True, False, True, False, False),
     (2048, 1290, 1152, 8, 128, "fp16", "none", True, True, True, False, True),
+    (19, 130, 65536, 4, 128, "bf16", "none", True, False, False, False, False),       # rows too wide for pairs
+    (1185, 128, 1024, 4, 64, "fp16", "none", True, False, False, False, False),        # an odd last row of a pair
     (700, 4101, 768, 4, 384, "fp16", "silu", False, True, False, True, False),
 ]
 
