@@ -11,9 +11,10 @@
 //   warp 0        activations by TMA (128-byte swizzle)
 //   warp 3        codes by TMA (no swizzle)
 //   warp 1        tensor-memory allocation and MMA issue (one lane)
-//   warps 4-11    unpack codes into the swizzled operand tile: two groups of four warps, each its half
-//                 of every chunk
-//   warps 12-19   drain: lane = weight row, each warp half of the tokens
+//   warps 4-19    unpack codes into the swizzled operand tile: four groups of four warps, each its half
+//                 of every other chunk (two groups, each its half of every chunk, left the 500 tokens'
+//                 gradient below at 43 us: a warp's chain of waits, loads and stores was the bound)
+//   warps 20-27   drain: lane = weight row, each warp half of the tokens
 // Operands move in steps of 64 along k through a ring deep enough to hide the hand-over between the
 // unpack warps and the MMA (about 2700 cycles there and back).  Cost of a 128-column chunk at TN =
 // 128: the MMAs take 512 cycles, unpacking about 320 of the integer pipes, the drain 128: all three
@@ -21,7 +22,7 @@
 // distributed shared memory in a fixed order, in the epilogue that also adds the bias, applies the
 // activation and adds the residual: one launch, deterministic.  77 tokens through 11008 x 4096 with 3
 // bits take 39 us (the bytes and the products would take 4): 32 chunks of unpacking, hand-over and drain
-// one behind the other in 86 blocks; 500 tokens' gradient through 4096 x 4096 43 us.
+// one behind the other in 86 blocks; 500 tokens' gradient through 4096 x 4096 39 us.
 //
 // Gradient: dX[t][perm[k]] = scale_t * sum over rows r of W16[r][k] * dz[t][r],
 //     W16 = fp16( fp32(u - z) * s ),   dz[t][r] = dY[t][r] act'(Z[t][r]) / scale_t  in fp16
@@ -41,13 +42,13 @@ namespace gptq {
 
 constexpr int TC_BM = 128;                    // weight rows of a block
 constexpr int TC_BK = 128;                    // columns of a chunk (two 64-column swizzle atoms)
-constexpr int TC_THREADS = 20 * 32;
+constexpr int TC_THREADS = 28 * 32;
 constexpr int TC_MAX_TN = 128;
 constexpr int TC_STEP_A = 128 * 128;          // an unpacked step: 128 x 64 values
 constexpr int TC_STEPS_MAX = 8;
-// Register split (setmaxnreg): 128 * (40 + 2 * 64 + 2 * 152) = 60416 of the 61440 that 640 threads of 96 start with.
-constexpr int TC_REGS_MISC = 40, TC_REGS_UNPACK = 64, TC_REGS_DRAIN = 152;
-static_assert(TC_REGS_MISC + 2 * TC_REGS_UNPACK + 2 * TC_REGS_DRAIN <= 5 * 96, "register split");
+// Register split (setmaxnreg): 128 * (40 + 4 * 56 + 2 * 120) = 64512, what 896 threads of 72 start with.
+constexpr int TC_REGS_MISC = 40, TC_REGS_UNPACK = 56, TC_REGS_DRAIN = 120;
+static_assert(TC_REGS_MISC + 4 * TC_REGS_UNPACK + 2 * TC_REGS_DRAIN <= 7 * 72, "register split");
 
 __host__ __device__ constexpr int tc_code_bytes(int bits) { return TC_BM * TC_BK * bits / 8; }
 __host__ __device__ constexpr int tc_code_chunks(int bits) { return bits == 8 ? 2 : 3; }  // in flight
@@ -392,12 +393,12 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         mbar_wait_drain(bar_drain, 0);
       }
     }
-  } else if (warp < 12) {
+  } else if (warp < 20) {
     // ---------------- unpack ----------------
-    // Forward: group 0 takes columns 0-63 of every chunk, group 1 columns 64-127, a thread one row.
-    // Gradient: group 0 takes rows 0-63 of every chunk, group 1 rows 64-127, two threads per row.
+    // Forward: grp 0 takes columns 0-63 of a chunk, 1 columns 64-127, a thread one row.  Gradient: grp 0
+    // takes rows 0-63, 1 rows 64-127, two threads per row.  par: the even or the odd chunks.
     regs_dec<TC_REGS_UNPACK>();
-    const int d = threadIdx.x & 127, grp = (warp - 4) >> 2;
+    const int d = threadIdx.x & 127, grp = ((warp - 4) >> 2) & 1, par = (warp - 4) >> 3;
     const int r = BWD ? grp * 64 + (d >> 1) : d, h = BWD ? d & 1 : grp, r7 = r & 7;
     const uint32_t dst0 = a_base + (BWD ? h * (TC_STEP_A / 2) + (r & 63) * 128 : r * 128);
     constexpr int ZN = GU == 32 ? 2 : 1;  // groups of a half row
@@ -415,7 +416,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       }
     };
     RingAt c;
-    int as = grp;  // slot of this group's next step
+    c.s = par;
+    int as = 2 * par + grp;  // slot of this group's next step
     uint32_t aph = 0;
     // The words of the next chunk are taken before this chunk's stores are fenced, so that the stores
     // complete meanwhile.
@@ -425,19 +427,19 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       load_half_row<BITS>(smem + (c_base - sbase) + c.s * CODES, r, h, w);
       return true;
     };
-    bool ok = nk > 0;
+    bool ok = nk > par;
     if (ok) {
-      load_sz(0);
+      load_sz(par);
       ok = take();
     }
-    for (int i = 0; i < nk && ok; ++i) {
+    for (int i = par; i < nk && ok; i += 2) {
       float cs_[ZN], cz[ZN];
 #pragma unroll
       for (int j = 0; j < ZN; ++j) {
         cz[j] = nz[j];
         cs_[j] = BWD ? ns[j] : 0.0f;
       }
-      if (i + 1 < nk) load_sz(i + 1);
+      if (i + 2 < nk) load_sz(i + 2);
       if (!warp_wait_uniform(bar_empty + 8 * as, aph ^ 1u, abort_flag)) break;
       const uint32_t dst = dst0 + as * TC_STEP_A;
 #pragma unroll
@@ -459,20 +461,21 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_cempty + 8 * c.s);
       c.next(SC);
-      if (i + 1 < nk) ok = take();
+      c.next(SC);
+      if (i + 2 < nk) ok = take();
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_full + 8 * as);
-      as += 2;
+      as += 4;
       if (as >= NS) {
-        as = grp;
+        as -= NS;
         aph ^= 1u;
       }
     }
   } else {
     // ---------------- drain ----------------
     regs_inc<TC_REGS_DRAIN>();
-    const int qd = warp & 3, half = (warp - 12) >> 2;
+    const int qd = warp & 3, half = (warp - 20) >> 2;
     const int row = qd * 32 + lane, cols = tn / 2;  // tokens of this warp: 16, 32 or 64
     const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(qd * 32) << 16) + static_cast<uint32_t>(half * cols);
     float acc[64];
@@ -491,18 +494,21 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         break;
       }
       tc_fence_after();
-      // (all loads, then one wait: a load takes some 200 cycles while the MMAs run)
-      uint32_t v[4][16];
+      // (two loads, then one wait: a load takes some 200 cycles while the MMAs run; four need registers)
 #pragma unroll
-      for (int cc = 0; cc < 4; ++cc)
-        if (cc * 16 < cols) tmem_ld_32x32b_x16(lane_base + static_cast<uint32_t>(t.s * tn + cc * 16), v[cc]);
-      tmem_ld_wait();
+      for (int c2 = 0; c2 < 4; c2 += 2) {
+        uint32_t v[2][16];
 #pragma unroll
-      for (int cc = 0; cc < 4; ++cc)
-        if (cc * 16 < cols) {
+        for (int cc = 0; cc < 2; ++cc)
+          if ((c2 + cc) * 16 < cols) tmem_ld_32x32b_x16(lane_base + static_cast<uint32_t>(t.s * tn + (c2 + cc) * 16), v[cc]);
+        tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < 16; ++j) acc[cc * 16 + j] = fmaf(sc, __uint_as_float(v[cc][j]), acc[cc * 16 + j]);
-        }
+        for (int cc = 0; cc < 2; ++cc)
+          if ((c2 + cc) * 16 < cols) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) acc[(c2 + cc) * 16 + j] = fmaf(sc, __uint_as_float(v[cc][j]), acc[(c2 + cc) * 16 + j]);
+          }
+      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_tempty + 8 * t.s);
