@@ -29,11 +29,14 @@ inline gptq_status cuda_fail(cudaError_t e, const char* what) {
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Makes `dev` the calling thread's device until the end of the scope.  The device is set also where it
+// is the current one already: on a host thread that has not used CUDA yet it is that call that binds
+// the device's context, and encoding a tensor map, the first thing some entry points do, needs one.
 class DeviceGuard {
  public:
   explicit DeviceGuard(int dev) : dev_(dev) {
     cudaGetDevice(&prev_);
-    if (prev_ != dev_) cudaSetDevice(dev_);
+    cudaSetDevice(dev_);
   }
   ~DeviceGuard() {
     if (prev_ != dev_) cudaSetDevice(prev_);
