@@ -325,8 +325,12 @@ gptq_status gptq_dequant_matmul_check(void* workspace, int device, void* cuda_st
  * mixture-of-experts layer ("模型量化实战：从 INT8 PTQ 到 GPTQ 的精度保持与推理加速全解析" §4.3,
  * and the group sizes that "GPTQ量化损失深度解析：原理、影响与优化策略" gives for MoE layers).
  *
- * A packed layer is what gptq_quantize_layer, gptq_rtn_quantize or gptq_awq_quantize wrote:
+ * A packed layer is what gptq_quantize_layer or gptq_rtn_quantize wrote:
  *   W[r][k] = (code[r][k] - zero[r][k / g]) * scale[r][k / g]        (sweep order k)
+ * Where there is a channel scale (gptq_awq_quantize; gptq_rtn_quantize given one) the codes are those of
+ * the scaled weight, and the calls below multiply by that: the caller divides X by channel_scale[c] before
+ * gptq_dequant_linear, and dX by it after gptq_dequant_linear_backward.  gptq_dequant_moe takes no such
+ * layer: its router reads the same X as the experts, and each expert has scales of its own.
  * The zeros are integers in [0, 2^bits - 1].  Unlike gptq_dequant_matmul, the products below do
  * not round W to 16 bits: code - zero is exact in the activations' type and the scale multiplies
  * each group's fp32 sum.

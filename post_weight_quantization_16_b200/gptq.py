@@ -424,8 +424,9 @@ def dequant_linear(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, z
                    stream: torch.cuda.Stream | None = None):
     """Y = act(X[:, perm] W^T + bias) + residual with a packed W (gptq_dequant_linear).  X: fp16 or
     bf16 [T, n] device tensor in original column order (row stride a multiple of 8); codes, scales,
-    zeros, perm as quantize_layer (or rtn_quantize, awq_quantize: perm None) wrote them; bias [m] and
-    residual [T, m] in X's type; act one of ACT_NONE, ACT_RELU, ACT_GELU, ACT_SILU.  Returns Y [T, m]
+    zeros, perm as quantize_layer (or rtn_quantize: perm None) wrote them (the product is with the scaled
+    weight where the layer has a channel_scale, as awq_quantize's: divide X by it before, and dX after
+    dequant_linear_backward); bias [m] and residual [T, m] in X's type; act one of ACT_NONE, ACT_RELU, ACT_GELU, ACT_SILU.  Returns Y [T, m]
     in X's type (or fp32 with out_dtype=torch.float32), and with want_preact also Z, the value the
     activation was applied to, which dequant_linear_backward takes.  `out` may be `residual`,
     but not share memory with X.
@@ -555,8 +556,10 @@ def dequant_moe(X: torch.Tensor, router: torch.Tensor, gate_up: tuple, down: tup
 
 def stack_experts(gates: list, ups: list, downs: list) -> tuple:
     """(gate_up, down, perm) for dequant_moe from the experts' quantized projections: lists, one entry
-    per expert, of dicts with codes, scales, zeros and perm (or no perm) as quantize_layer,
-    rtn_quantize and awq_quantize return them.  An expert's gate and up share their input, so with
+    per expert, of dicts with codes, scales, zeros and perm (or no perm) as quantize_layer and
+    rtn_quantize return them.  A layer with a channel_scale other than 1 (awq_quantize, rtn_quantize given
+    one) is refused: its codes are those of the scaled weight, and dequant_moe has no place where an
+    expert's input could be divided by it.  An expert's gate and up share their input, so with
     act-order they must share their perm too (it depends on the input alone).  The act-order of a down
     projection is folded into the rows of its gate and up: h then comes out in down's sweep order.
     A one-time layout: call it once per layer and keep the result."""
@@ -564,6 +567,10 @@ def stack_experts(gates: list, ups: list, downs: list) -> tuple:
         raise ValueError("gates, ups and downs need one entry per expert each")
     gate_up, down, perms = [], [], []
     for e, (g, u, d) in enumerate(zip(gates, ups, downs)):
+        for name, q in (("gate", g), ("up", u), ("down", d)):
+            c = q.get("channel_scale")
+            if c is not None and not bool((c == 1).all()):
+                raise ValueError(f"expert {e}: {name} has a channel_scale, which dequant_moe cannot divide out")
         pg, pu, pd = g.get("perm"), u.get("perm"), d.get("perm")
         if (pg is None) != (pu is None) or (pg is not None and not torch.equal(pg, pu)):
             raise ValueError(f"expert {e}: gate and up have different input orders")
@@ -677,8 +684,8 @@ def rtn_quantize(W: torch.Tensor, bits: int = 8, group_size: int = -1, sym: bool
                  stream: torch.cuda.Stream | None = None) -> dict:
     """Round-to-nearest with a clipped range (gptq_rtn_quantize; the page's INT8 LinearQuantizer
     is bits 8, per-channel, symmetric, clip_ratio 0.99).  W: fp16 [m, n]; channel_scale: fp32 [n]
-    or None.  Returns device tensors codes, scales, zeros and (optionally) w_hat, in original
-    column order."""
+    or None.  Returns device tensors codes, scales, zeros, channel_scale (where one was given) and
+    (optionally) w_hat, in original column order."""
     m, n = W.shape
     dev = W.device
     stream = stream if stream is not None else torch.cuda.current_stream(dev)
@@ -687,6 +694,8 @@ def rtn_quantize(W: torch.Tensor, bits: int = 8, group_size: int = -1, sym: bool
            "scales": torch.empty((m, n // g), dtype=torch.float32, device=dev),
            "zeros": torch.empty((m, n // g), dtype=torch.float32, device=dev),
            "w_hat": torch.empty((m, n), dtype=torch.float32, device=dev) if want_w_hat else None}
+    if channel_scale is not None:
+        out["channel_scale"] = channel_scale
     qp = QParams(int(bits), int(group_size), int(bool(sym)))
     _check(lib().gptq_rtn_quantize(_ptr(W), m, n, qp, float(clip_ratio), _ptr(channel_scale), _ptr(out["codes"]),
                                    _ptr(out["scales"]), _ptr(out["zeros"]), _ptr(out["w_hat"]), dev.index,

@@ -222,3 +222,19 @@ def test_stack_experts_folds_the_down_order_into_the_rows():
     mixed = [dict(d, perm=None) if e else d for e, d in enumerate(gates)]
     with pytest.raises(ValueError, match="every expert|different"):
         G.stack_experts(mixed, [dict(d, perm=None) if e else gates[0] for e, d in enumerate(gates)], downs)
+
+
+def test_stack_experts_refuses_layers_with_a_channel_scale():
+    """Codes of a channel-scaled weight (AWQ) are not those of the weight: no expert may have them."""
+    codes, s = torch.zeros(128, 16, dtype=torch.int32), torch.ones(128, 1)
+    plain = {"codes": codes, "scales": s, "zeros": s}
+    one = dict(plain, channel_scale=torch.ones(128))
+    scaled = dict(plain, channel_scale=torch.cat([torch.ones(127), torch.full((1,), 2.0)]))
+    gu, dn, perm = G.stack_experts([plain, one], [plain, one], [one, plain])
+    assert gu[0].shape == (2, 256, 16) and dn[0].shape == (2, 128, 16) and perm is None
+    for at, name in enumerate(("gate", "up", "down")):
+        for e in range(2):
+            parts = [[plain, plain] for _ in range(3)]
+            parts[at][e] = scaled
+            with pytest.raises(ValueError, match=f"expert {e}: {name} has a channel_scale"):
+                G.stack_experts(*parts)
