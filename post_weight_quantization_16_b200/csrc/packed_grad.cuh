@@ -34,12 +34,14 @@ __device__ __forceinline__ float at8(const uint4& v, int j) {
   return h2f<BF>(static_cast<uint16_t>((j & 1) ? w >> 16 : w & 0xFFFFu));
 }
 
-// One block per token.  scale_t = 2^e with the largest |dY| of the token in [2^(e+13), 2^(e+14))
-// (e clamped to [-126, 126], where both
-// scale_t and its inverse are normal; 1 for a token without a finite, nonzero value), then hi + lo = dz /
-// scale_t in fp16 (lo null: hi alone).  Rows of ldz (a multiple of 8) elements; the second pass finds
-// dY in the caches.  vec: rows of dY and Z allow 16-byte accesses.  4096 x 11008 values with SiLU: 57 us
-// (4.7 TB/s).
+// One block per token.  scale_t = 2^e with the largest finite |dz| of the token, dz = dY act'(Z), in
+// [2^(e+13), 2^(e+14)) (e clamped to [-126, 126], where both scale_t and its inverse are normal; 1 for a
+// token without a finite, nonzero value), then hi + lo = dz / scale_t in fp16 (lo null: hi alone).  (The
+// largest |dY| would not do: an outlier that act' masks would push what is left into fp16's subnormals.)
+// Rows of ldz (a multiple of 8) elements.  A thread keeps its first GRAD_KEPT eights of dz in registers, so
+// rows of up to 12288 values are read and act' evaluated once; what is beyond is computed again.  vec:
+// rows of dY and Z allow 16-byte accesses.
+constexpr int GRAD_KEPT = 3;
 template <bool BF, int ACT>
 __global__ void __launch_bounds__(512) act_grad_kernel(const uint16_t* __restrict__ dY, int64_t ld_dy,
                                                        const uint16_t* __restrict__ Z, int m, int vec,
@@ -51,12 +53,36 @@ __global__ void __launch_bounds__(512) act_grad_kernel(const uint16_t* __restric
   const size_t t = blockIdx.x;
   const uint16_t* dy = dY + t * ld_dy;
   const uint16_t* z = Z + t * m;
-  float mx = 0.0f;
-#pragma unroll 3
-  for (int r = threadIdx.x * 8; r < m; r += 4096) {
-    const uint4 v = load8(dy + r, vec && r + 8 <= m, m - r);
+  // eight values of dz from column r
+  auto eight = [&](int r, float (&x)[8]) {
+    const bool whole = vec && r + 8 <= m;
+    const uint4 v = load8(dy + r, whole, m - r);
+    uint4 zv = {};
+    if (ACT != ACT_NONE) zv = load8(z + r, whole, m - r);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fabsf(at8<BF>(v, j)));
+    for (int j = 0; j < 8; ++j) x[j] = at8<BF>(v, j) * (ACT != ACT_NONE ? act_grad<ACT>(at8<BF>(zv, j)) : 1.0f);
+  };
+  float mx = 0.0f;
+  auto largest = [&](const float (&x)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float a = fabsf(x[j]);
+      mx = fmaxf(mx, a < INFINITY ? a : 0.0f);
+    }
+  };
+  float kept[GRAD_KEPT][8];
+#pragma unroll
+  for (int k = 0; k < GRAD_KEPT; ++k) {
+    const int r = static_cast<int>(threadIdx.x) * 8 + k * 4096;
+    if (r < m) {
+      eight(r, kept[k]);
+      largest(kept[k]);
+    }
+  }
+  for (int r = threadIdx.x * 8 + GRAD_KEPT * 4096; r < m; r += 4096) {
+    float x[8];
+    eight(r, x);
+    largest(x);
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -65,18 +91,12 @@ __global__ void __launch_bounds__(512) act_grad_kernel(const uint16_t* __restric
 #pragma unroll
   for (int w = 0; w < 16; ++w) mx = fmaxf(mx, wmax[w]);
   int e = 0;
-  if (mx > 0.0f && mx < INFINITY) e = min(126, max(-126, ilogbf(mx) - 13));
+  if (mx > 0.0f) e = min(126, max(-126, ilogbf(mx) - 13));
   const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
   if (threadIdx.x == 0) token_scale[t] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-#pragma unroll 3
-  for (int r = threadIdx.x * 8; r < m; r += 4096) {
-    const bool whole = vec && r + 8 <= m;
-    const uint4 v = load8(dy + r, whole, m - r);
-    uint4 zv = {};
-    if (ACT != ACT_NONE) zv = load8(z + r, whole, m - r);
-    float x[8];
+  auto store = [&](int r, float (&x)[8]) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = at8<BF>(v, j) * inv * (ACT != ACT_NONE ? act_grad<ACT>(at8<BF>(zv, j)) : 1.0f);
+    for (int j = 0; j < 8; ++j) x[j] *= inv;
     // (rows are padded to a multiple of 8: a whole group always has room)
     const uint4 h = make_uint4(pack2<false>(x[0], x[1]), pack2<false>(x[2], x[3]), pack2<false>(x[4], x[5]),
                                pack2<false>(x[6], x[7]));
@@ -87,6 +107,16 @@ __global__ void __launch_bounds__(512) act_grad_kernel(const uint16_t* __restric
       *reinterpret_cast<uint4*>(lo + t * ldz + r) = make_uint4(
           pack2<false>(x[0], x[1]), pack2<false>(x[2], x[3]), pack2<false>(x[4], x[5]), pack2<false>(x[6], x[7]));
     }
+  };
+#pragma unroll
+  for (int k = 0; k < GRAD_KEPT; ++k) {
+    const int r = static_cast<int>(threadIdx.x) * 8 + k * 4096;
+    if (r < m) store(r, kept[k]);
+  }
+  for (int r = threadIdx.x * 8 + GRAD_KEPT * 4096; r < m; r += 4096) {
+    float x[8];
+    eight(r, x);
+    store(r, x);
   }
 }
 
