@@ -394,10 +394,11 @@ gptq_status gptq_dequant_linear(const gptq_linear_args* args, int device, void* 
 
 /* The gradient of the linear layer (W frozen: what adapters and the layers below train on):
  *   dZ = dY * act'(Z),   dX[:, perm] = dZ W16,   dbias = sum over tokens of dZ
- * (the residual's gradient is dY).  W16 is the fp16 weight of gptq_dequant_matmul: the sum runs
- * over the rows, across which the scale varies, so the weights enter as 16-bit values.  dZ enters
- * as fp16 values scaled by a power of two per token (two values, a high and a low part, when dtype
- * is fp16 and act is GELU or SiLU); sums are fp32.
+ * (the residual's gradient is dY).  W16 is W rounded to 11 significant bits: the sum runs over the
+ * rows, across which the scale varies, so the weights enter as fp16 values, times a power of two per 128
+ * columns that fits them to fp16's range whatever the scales are (weights below 2^-29 of the largest that
+ * those columns can hold lose bits).  dZ enters as fp16 values scaled by a power of two per token (two
+ * values, a high and a low part, when dtype is fp16 and act is GELU or SiLU); sums are fp32.
  *   dY       : device, dtype, [T x m], row stride ld_dy >= m; 0 <= T <= 2^22
  *   preact   : device, dtype, [T x m] contiguous: Z as gptq_dequant_linear gave it; not read when
  *              act is none

@@ -225,7 +225,7 @@ gptq_status linear_many_tokens(const gptq_linear_args& a, const uint16_t* X, int
 struct GradLayout {
   int parts;       // 0: dY itself is the operand, else fp16 values of dz (1, or 2: high and low)
   int64_t ldz;
-  size_t scale, hi, lo, dx, total;
+  size_t scale, exponent, hi, lo, dx, total;
 };
 bool grad_layout(int64_t T, int64_t m, int64_t n, int act_order, int dtype, int act, bool direct, GradLayout* l) {
   if (T < 0 || T > kPackedMaxT || m < 1 || m > kPackedMaxM || !valid_width(n) ||
@@ -242,6 +242,7 @@ bool grad_layout(int64_t T, int64_t m, int64_t n, int act_order, int dtype, int 
   };
   const size_t dz = static_cast<size_t>(T) * l->ldz * 2;
   l->scale = take(static_cast<size_t>(T) * 4);
+  l->exponent = take(static_cast<size_t>(n / 128) * 4);
   l->hi = take(l->parts >= 1 ? dz : 0);
   l->lo = take(l->parts == 2 ? dz : 0);
   l->dx = take(act_order ? static_cast<size_t>(T) * n * 2 : 0);
@@ -462,22 +463,34 @@ extern "C" gptq_status gptq_dequant_linear_backward(const gptq_linear_grad_args*
                         reinterpret_cast<int*>(ws));
     }));
   if (!a.dX) return GPTQ_OK;
+  const int g = group_width(a.W);
   const uint16_t *hi = dY, *lo = dY;
   int64_t ldz = a.ld_dy;
-  if (lay.parts >= 1) {
-    uint16_t* h = reinterpret_cast<uint16_t*>(ws + lay.hi);
+  {
+    uint16_t* h = lay.parts >= 1 ? reinterpret_cast<uint16_t*>(ws + lay.hi) : nullptr;
     uint16_t* o = lay.parts == 2 ? reinterpret_cast<uint16_t*>(ws + lay.lo) : nullptr;
-    ldz = lay.ldz;
+    ColumnArgs cols;
+    cols.scales = a.W.scales;
+    cols.G = n / g;
+    cols.per = g >= 128 ? 1 : 128 / g;
+    cols.bits = a.W.qp.bits;
+    cols.chunks = n / 128;
+    cols.gi = group_index(g);
+    cols.exponent = reinterpret_cast<int*>(ws + lay.exponent);
     CK(by_act(a.act, [&](auto k) {
       constexpr int A = decltype(k)::value;
-      return launch_pdl(bf ? act_grad_kernel<true, A> : act_grad_kernel<false, A>, dim3(T), dim3(512), 0, 1, st, dY,
-                        a.ld_dy, Z, m, vec, h, o, ldz, reinterpret_cast<float*>(ws + lay.scale));
+      const auto kernel = bf ? (m <= 4096 ? act_grad_kernel<true, A, 1> : act_grad_kernel<true, A, 3>)
+                             : (m <= 4096 ? act_grad_kernel<false, A, 1> : act_grad_kernel<false, A, 3>);
+      return launch_pdl(kernel, dim3(cols.chunks + (h ? T : 0)), dim3(512), 0, 1, st, dY, a.ld_dy, Z, m, vec, h, o, lay.ldz,
+                        reinterpret_cast<float*>(ws + lay.scale), cols);
     }));
-    hi = h;
-    lo = o ? o : h;
+    if (h) {
+      ldz = lay.ldz;
+      hi = h;
+      lo = o ? o : h;
+    }
   }
   LinearTcArgs d = {};
-  const int g = group_width(a.W);
   d.T = T;
   d.m = m;
   d.chunks = (m + 127) / 128;
@@ -489,6 +502,7 @@ extern "C" gptq_status gptq_dequant_linear_backward(const gptq_linear_grad_args*
   d.status = reinterpret_cast<int*>(ws);
   GradOut go;
   go.token_scale = lay.parts >= 1 ? reinterpret_cast<const float*>(ws + lay.scale) : nullptr;
+  go.exponent = reinterpret_cast<const int*>(ws + lay.exponent);
   go.dX = a.W.perm ? reinterpret_cast<uint16_t*>(ws + lay.dx) : static_cast<uint16_t*>(a.dX);
   go.lddx = a.W.perm ? n : a.ld_dx;
   go.n = n;

@@ -34,23 +34,62 @@ __device__ __forceinline__ float at8(const uint4& v, int j) {
   return h2f<BF>(static_cast<uint16_t>((j & 1) ? w >> 16 : w & 0xFFFFu));
 }
 
-// One block per token.  scale_t = 2^e with the largest finite |dz| of the token, dz = dY act'(Z), in
+// Exponent e[c] of a block of 128 columns of W: (u - z) s 2^e lies below 2^15 for every row, and the largest
+// scale's weights near it, so that the product's fp16 weights keep 11 significant bits down to 2^-29 of
+// the block's largest, whatever the layer's scales are (a scale of 1e-7 would leave its codes in fp16's
+// subnormals, one of 1e4 above its largest value).  One block, 512 threads; scales that are not finite do
+// not count.  A row of every group is one 32-byte sector: 11008 rows take 2 us beside the tokens' blocks.
+__device__ __forceinline__ void column_exponent(const float* __restrict__ scales, int m, int G, GroupIndex gi, int per,
+                                                int bits, int chunk, int* __restrict__ out) {
+  __shared__ float wmax[16];
+  const float* first = scales + (per > 1 ? chunk * per : gi.div == 1 ? chunk : static_cast<int>(__umulhi(static_cast<uint32_t>(chunk), gi.magic)));
+  const int shift = per == 4 ? 2 : per - 1;  // per: groups of the block, 1, 2 or 4
+  float mx = 0.0f;
+#pragma unroll 8
+  for (int64_t i = threadIdx.x; i < static_cast<int64_t>(m) * per; i += 512) {
+    const float a = fabsf(__ldg(first + (i >> shift) * G + (i & (per - 1))));
+    mx = fmaxf(mx, a < INFINITY ? a : 0.0f);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  if ((threadIdx.x & 31) == 0) wmax[threadIdx.x >> 5] = mx;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < 16; ++w) mx = fmaxf(mx, wmax[w]);
+    out[chunk] = mx > 0.0f ? min(126, max(-126, 14 - bits - ilogbf(mx))) : 0;
+  }
+}
+
+// What the blocks of act_grad_kernel before the tokens' take: one per 128 columns of W.
+struct ColumnArgs {
+  const float* scales;
+  int G, per, bits, chunks;
+  GroupIndex gi;
+  int* exponent;  // [chunks]
+};
+
+// Blocks 0 .. chunks - 1: the weights' exponents.  Then one block per token (the grid has none when dY itself
+// is the operand).  scale_t = 2^e with the largest finite |dz| of the token, dz = dY act'(Z), in
 // [2^(e+13), 2^(e+14)) (e clamped to [-126, 126], where both scale_t and its inverse are normal; 1 for a
 // token without a finite, nonzero value), then hi + lo = dz / scale_t in fp16 (lo null: hi alone).  (The
 // largest |dY| would not do: an outlier that act' masks would push what is left into fp16's subnormals.)
-// Rows of ldz (a multiple of 8) elements.  A thread keeps its first GRAD_KEPT eights of dz in registers, so
-// rows of up to 12288 values are read and act' evaluated once; what is beyond is computed again.  vec:
-// rows of dY and Z allow 16-byte accesses.
-constexpr int GRAD_KEPT = 3;
-template <bool BF, int ACT>
+// Rows of ldz (a multiple of 8) elements.  A thread keeps its first KEPT eights of dz in registers: 1 for
+// rows of up to 4096 values, else 3, where 12288 are read and act' evaluated once; what is beyond is
+// computed again.  vec: rows of dY and Z allow 16-byte accesses.
+template <bool BF, int ACT, int KEPT>
 __global__ void __launch_bounds__(512) act_grad_kernel(const uint16_t* __restrict__ dY, int64_t ld_dy,
                                                        const uint16_t* __restrict__ Z, int m, int vec,
                                                        uint16_t* __restrict__ hi, uint16_t* __restrict__ lo,
-                                                       int64_t ldz, float* __restrict__ token_scale) {
+                                                       int64_t ldz, float* __restrict__ token_scale,
+                                                       const ColumnArgs cols) {
   __shared__ float wmax[16];
   griddep_wait();
   griddep_launch_dependents();
-  const size_t t = blockIdx.x;
+  if (static_cast<int>(blockIdx.x) < cols.chunks) {
+    column_exponent(cols.scales, m, cols.G, cols.gi, cols.per, cols.bits, static_cast<int>(blockIdx.x), cols.exponent);
+    return;
+  }
+  const size_t t = blockIdx.x - cols.chunks;
   const uint16_t* dy = dY + t * ld_dy;
   const uint16_t* z = Z + t * m;
   // eight values of dz from column r
@@ -70,16 +109,16 @@ __global__ void __launch_bounds__(512) act_grad_kernel(const uint16_t* __restric
       mx = fmaxf(mx, a < INFINITY ? a : 0.0f);
     }
   };
-  float kept[GRAD_KEPT][8];
+  float kept[KEPT][8];
 #pragma unroll
-  for (int k = 0; k < GRAD_KEPT; ++k) {
+  for (int k = 0; k < KEPT; ++k) {
     const int r = static_cast<int>(threadIdx.x) * 8 + k * 4096;
     if (r < m) {
       eight(r, kept[k]);
       largest(kept[k]);
     }
   }
-  for (int r = threadIdx.x * 8 + GRAD_KEPT * 4096; r < m; r += 4096) {
+  for (int r = threadIdx.x * 8 + KEPT * 4096; r < m; r += 4096) {
     float x[8];
     eight(r, x);
     largest(x);
@@ -109,11 +148,11 @@ __global__ void __launch_bounds__(512) act_grad_kernel(const uint16_t* __restric
     }
   };
 #pragma unroll
-  for (int k = 0; k < GRAD_KEPT; ++k) {
+  for (int k = 0; k < KEPT; ++k) {
     const int r = static_cast<int>(threadIdx.x) * 8 + k * 4096;
     if (r < m) store(r, kept[k]);
   }
-  for (int r = threadIdx.x * 8 + GRAD_KEPT * 4096; r < m; r += 4096) {
+  for (int r = threadIdx.x * 8 + KEPT * 4096; r < m; r += 4096) {
     float x[8];
     eight(r, x);
     store(r, x);

@@ -261,6 +261,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PR_THREADS, 1)
     for (int tile = cluster; tile < ntiles && ok; tile += clusters) {
       const int mt = tile % p.tiles_m * 2 + static_cast<int>(rank);
       // row of W and its groups: forward row mt * 128 + r in chunk i; gradient row i * 128 + r in chunk mt
+      const float up = BWD ? pow2(p.go.exponent[min(mt, p.go.n / 128 - 1)]) : 1.0f;
       float ns[ZN], nz[ZN];
       auto load_sz = [&](int i) {
         const int gr = (BWD ? i : mt) * 128 + r;
@@ -280,7 +281,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PR_THREADS, 1)
 #pragma unroll
         for (int j = 0; j < ZN; ++j) {
           cz[j] = nz[j];
-          cs[j] = BWD ? ns[j] : 0.0f;
+          cs[j] = BWD ? ns[j] * up : 0.0f;
         }
         if (i + 1 < p.steps) load_sz((BWD && i + 1 >= p.chunks) ? i + 1 - p.chunks : i + 1);
         if (!warp_wait_uniform_cl(bar_empty + 8 * as, aph ^ 1u, abort_flag)) {
@@ -380,6 +381,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PR_THREADS, 1)
           break;
         }
         tc_fence_after();
+        const int e = p.go.exponent[min(mt, p.go.n / 128 - 1)];
 #pragma unroll 1
         for (int cc = 0; cc < 8; ++cc) {
           uint32_t v[16];
@@ -390,8 +392,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PR_THREADS, 1)
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               const int t = tok0 + cc * 16 + 8 * g + j;
-              const float ts = p.go.token_scale && t < p.lin.T ? __ldg(p.go.token_scale + t) : 1.0f;
-              stage[j * 32 + lane] = __uint_as_float(v[8 * g + j]) * ts;
+              const Unscale s(p.go.token_scale && t < p.lin.T ? __ldg(p.go.token_scale + t) : 1.0f, e);
+              stage[j * 32 + lane] = s(__uint_as_float(v[8 * g + j]));
             }
             put8(cc * 16 + 8 * g, p.go.dX, p.go.lddx, false, nullptr);
           }

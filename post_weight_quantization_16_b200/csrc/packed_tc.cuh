@@ -25,11 +25,12 @@
 // one behind the other in 86 blocks; 500 tokens' gradient through 4096 x 4096 39 us.
 //
 // Gradient: dX[t][perm[k]] = scale_t * sum over rows r of W16[r][k] * dz[t][r],
-//     W16 = fp16( fp32(u - z) * s ),   dz[t][r] = dY[t][r] act'(Z[t][r]) / scale_t  in fp16
-// The sum runs over the rows, across which the scale varies, so the weights enter as their fp16
-// values (the library's dequantized weight) and both operands are fp16 whatever the type of the
-// activations: bf16 operands would lose three more bits of each.  scale_t is a power of two per
-// token that puts the token's largest dY at 2^13 or above, so the range of bf16 gradients fits.
+//     W16 = fp16( fp32(u - z) * s * 2^e ) / 2^e,   dz[t][r] = dY[t][r] act'(Z[t][r]) / scale_t  in fp16
+// The sum runs over the rows, across which the scale varies, so the weights enter as rounded to fp16's 11
+// significant bits, and both operands are fp16 whatever the type of the activations: bf16 operands
+// would lose three more bits of each.  e is one exponent per 128 columns, from their largest scale
+// (packed_grad.cuh), and scale_t a power of two per token that puts the token's largest dz at 2^13 or
+// above, so layers of any scale and the range of bf16 gradients fit; both are undone in fp32.
 // With fp16 activations and a smooth act' the rounding of dz would be as large as that of dX
 // itself: dz then comes as a sum of two fp16 values and the rows are gone through twice.  A block
 // owns 128 columns of W: its operand is read transposed (MN-major) straight from the row-wise
@@ -239,10 +240,24 @@ struct RingAt {
 };
 
 struct GradOut {
-  const float* token_scale;  // [T] or null (1)
+  const float* token_scale;  // [T], powers of two, or null (1)
+  const int* exponent;       // [n / 128]: the weights of these columns are multiplied by 2^exponent
   uint16_t* dX;              // [T x n], sweep order
   int64_t lddx;
   int n, vec;  // vec: dX allows 8-byte accesses
+};
+
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }  // |e| <= 126
+// v times the token's scale over the weights' 2^e: in two steps, as the two together may lie past the
+// exponents of fp32 while the result does not.
+struct Unscale {
+  float a, b;
+  __device__ __forceinline__ Unscale(float token_scale, int e) {
+    const int x = static_cast<int>(__float_as_uint(token_scale) >> 23) - 127 - e;
+    a = pow2(x / 2);
+    b = pow2(x - x / 2);
+  }
+  __device__ __forceinline__ float operator()(float v) const { return v * a * b; }
 };
 
 // Forward: lin holds everything, `chunks` are 128-column chunks of k.  Gradient: lin holds T, m, G,
@@ -403,6 +418,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     const uint32_t dst0 = a_base + (BWD ? h * (TC_STEP_A / 2) + (r & 63) * 128 : r * 128);
     constexpr int ZN = GU == 32 ? 2 : 1;  // groups of a half row
     float ns[ZN], nz[ZN];
+    const float up = BWD ? pow2(go.exponent[mt]) : 1.0f;
     auto load_sz = [&](int i) {
       const int c = ch0 + (BWD && i >= nch ? i - nch : i);
       const int gr = (BWD ? c : mt) * 128 + r;
@@ -437,7 +453,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
 #pragma unroll
       for (int j = 0; j < ZN; ++j) {
         cz[j] = nz[j];
-        cs_[j] = BWD ? ns[j] : 0.0f;
+        cs_[j] = BWD ? ns[j] * up : 0.0f;
       }
       if (i + 2 < nk) load_sz(i + 2);
       if (!warp_wait_uniform(bar_empty + 8 * as, aph ^ 1u, abort_flag)) break;
@@ -527,6 +543,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   if (cs > 1) cluster_sync();
   // tokens rank, rank + cs, ... of the tile: a warp takes a token, a lane four rows (columns of dX)
   if (!*abort_flag) {
+    const int e = BWD ? go.exponent[mt] : 0;
     for (int t = rank + cs * warp; t < tn; t += cs * (TC_THREADS / 32)) {
       const int tok = t0 + t, row = mt * TC_BM + 4 * lane;
       if (tok >= p.T || (!BWD && row >= p.m)) continue;
@@ -540,9 +557,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         v.w += w.w;
       }
       if (BWD) {
-        const float s = go.token_scale ? go.token_scale[tok] : 1.0f;
+        const Unscale s(go.token_scale ? go.token_scale[tok] : 1.0f, e);
         uint16_t* o = go.dX + static_cast<size_t>(tok) * go.lddx + row;
-        const uint32_t lo = pack2<BF>(v.x * s, v.y * s), hi = pack2<BF>(v.z * s, v.w * s);
+        const uint32_t lo = pack2<BF>(s(v.x), s(v.y)), hi = pack2<BF>(s(v.z), s(v.w));
         if (go.vec) {
           *reinterpret_cast<uint2*>(o) = make_uint2(lo, hi);
         } else {

@@ -20,8 +20,12 @@ def gradient_close(c, got, dY, Z, dtype):
     W = np.zeros_like(c.W)
     W[:, c.perm_np] = c.W
     want = dz @ W
-    tol = (2.0 ** -10 + 2.0 ** -21) * (np.abs(dz) @ np.abs(W)) + H.product_tol(dz, W.T)
+    tol = (2.0 ** -10 + 2.0 ** -21) * (np.abs(dz) @ np.abs(W)) + H.product_tol(dz, W.T) - 1e-30   # (no absolute part: the layers' scales vary)
     tol += np.abs(dz).max(1, keepdims=True) * 2.0 ** (-13 - 25) * np.abs(W).sum(0)
+    # a weight is off by 2^-39 of the largest that its 128 columns' scales allow where it is that small
+    largest = np.zeros(c.n)
+    largest[c.perm_np] = np.repeat(np.repeat(c.s.max(0), c.n // c.s.shape[1]).reshape(-1, 128).max(1), 128) * 2.0 ** c.bits
+    tol += 2.0 ** -39 * np.abs(dz).sum(1, keepdims=True) * largest
     # (act' itself is good to 2^-19 of its largest value, 1.13)
     if c.act != "relu":
         tol += 2.0 ** -19 * 1.13 * (np.abs(np.where(np.abs(H.to64(Z)) > 50, 0, H.to64(dY))) @ np.abs(W))
@@ -60,3 +64,43 @@ def test_a_token_with_one_infinity(T, n):
     keep = c.W[r] != 0
     assert keep.mean() > 0.8
     assert np.array_equal(got[:, keep], np.broadcast_to(np.sign(c.W[r][keep]) * np.inf, (T, keep.sum())))
+
+
+def rescaled(c, factor):
+    """The case with its scales multiplied (factor: a number or an [m, groups] array)."""
+    c.s = (c.s.astype(np.float64) * factor).astype(np.float32)
+    c.layer[1] = torch.from_numpy(c.s).to(DEV)
+    c.W = H.weights64(c.codes, c.s, c.z)
+    return c
+
+
+@pytest.mark.parametrize("T,n", KERNELS + [(40, 384)])
+@pytest.mark.parametrize("bits,g,dtype,act,dy,factor", [
+    (8, 128, "bf16", "none", 1.0, 1e-3), (8, 32, "bf16", "silu", 1.0, 1e-6), (4, 64, "fp16", "none", 100.0, 1e-4),
+    (4, -1, "bf16", "none", 1.0, 1e7), (2, 32, "fp16", "relu", 1e-3, 1e5), (3, 64, "bf16", "gelu", 1.0, 1e30),
+    (4, 128, "bf16", "none", 1.0, 1e-30)])
+def test_gradient_of_layers_of_any_scale(T, n, bits, g, dtype, act, dy, factor):
+    """The forward pass holds its scales in fp32; the gradient's fp16 weights reach as far."""
+    c = rescaled(Case(T, 200, n, bits, g, dtype, act, True), factor)
+    dY = c.dev(c.rng.normal(0, dy, (T, 200)))
+    Z = c.dev(c.rng.normal(0, 1, (T, 200)))
+    gradient_close(c, G.dequant_linear_backward(dY, *c.layer, act=H.ACTS[act], preact=Z), dY, Z, c.dt)
+
+
+@pytest.mark.parametrize("T,n", KERNELS)
+@pytest.mark.parametrize("bits,g", [(4, 128), (8, 64), (3, 32), (2, 256)])
+def test_gradient_of_columns_and_rows_of_different_scales(T, n, bits, g):
+    """Blocks of 128 columns a factor of up to 2^60 apart do not touch one another's bits; rows inside a
+    block may be 2^20 apart, or zero."""
+    m = 200
+    c = Case(T, m, n, bits, g, "bf16", "none", True)
+    per = max(1, g // 128)                                             # blocks of 128 columns that share a group
+    blocks = np.repeat(c.rng.integers(-30, 31, -(-n // 128 // per)), per)[: n // 128].astype(float)
+    f = 2.0 ** np.repeat(blocks, 128)[:: g] * 2.0 ** c.rng.integers(-20, 1, (m, 1))
+    f[:, :: 5] *= (c.rng.random((m, 1)) < 0.9)
+    if f.shape[1] >= 8:
+        f[:, 0] = 0.0
+    rescaled(c, f)
+    dY = c.dev(c.rng.normal(0, 1, (T, m)))
+    Z = c.dev(np.ones((T, m)))
+    gradient_close(c, G.dequant_linear_backward(dY, *c.layer), dY, Z, c.dt)
