@@ -428,7 +428,9 @@ gptq_status gptq_dequant_linear_backward(const gptq_linear_grad_args* args, int 
  *   p = softmax(X R^T) over the experts (64-bit); a token's top_k experts are those of the largest
  *   p, in descending order, ties to the lower expert (a NaN is chosen last); their weights are p,
  *   divided by their sum when renormalize is 1
- *   h = act(x Wg_e^T) * (x Wu_e^T)     rounded to dtype (the second product's operand)
+ *   h = act(x Wg_e^T) * (x Wu_e^T)     rounded to dtype's significant bits (the second product's
+ *                                      operand); |h| up to 1.7e13 in fp16, where it has a step of 2^-24
+ *                                      below 2^-14
  *   Y = sum over the token's experts of weight * h Wd_e^T, + residual
  *   X         : device, dtype, [T x H], row stride ld_x (as gptq_dequant_linear); 0 <= T <= 128
  *   router    : device, dtype, [E x H], 16-byte aligned; 1 <= E <= 256, 1 <= top_k <= min(E, 16)

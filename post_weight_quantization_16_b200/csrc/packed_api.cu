@@ -274,7 +274,8 @@ DownSplit down_split(int64_t H, int64_t I, int64_t experts) {
 struct MoeLayout {
   int max_segments, max_tiles;
   DownSplit down;
-  size_t logits, ids, weights, segments, tiles, expert, begin, count, tile0, tile_seg, pair, pweight, x, h, partial, tickets, total;
+  size_t logits, ids, weights, segments, tiles, expert, begin, count, tile0, high, tile_seg, pair, pweight, x, h, h_high,
+      partial, tickets, total;
 };
 bool moe_layout(int64_t T, int64_t E, int64_t top_k, int64_t H, int64_t I, MoeLayout* l) {
   if (T < 0 || T > MOE_MAX_T || E < 1 || E > MOE_MAX_E || top_k < 1 || top_k > E || top_k > MOE_MAX_TOPK ||
@@ -299,11 +300,13 @@ bool moe_layout(int64_t T, int64_t E, int64_t top_k, int64_t H, int64_t I, MoeLa
   l->begin = take(l->max_segments * 4);
   l->count = take(l->max_segments * 4);
   l->tile0 = take(l->max_segments * 4);
+  l->high = take(l->max_segments * 4);
   l->tile_seg = take(l->max_tiles * 4);
   l->pair = take(pairs * 4);
   l->pweight = take(pairs * 4);
   l->x = take(static_cast<size_t>(l->max_tiles) * (H / 128) * FRAG_BYTES);
   l->h = take(static_cast<size_t>(l->max_tiles) * (I / 128) * FRAG_BYTES);
+  l->h_high = take(static_cast<size_t>(l->max_tiles) * (I / 128) * FRAG_BYTES);
   l->down = down_split(H, I, std::max<int64_t>(1, std::min(E, pairs)));
   l->partial = take(l->down.splits > 1 ? static_cast<size_t>(l->down.splits) * T * H * 4 : 0);
   l->tickets = take(l->down.splits > 1 ? static_cast<size_t>(H / DEC_ROWS) * l->down.cluster * 4 : 0);
@@ -601,6 +604,7 @@ extern "C" gptq_status gptq_dequant_moe(const gptq_moe_args* args, int device, v
   r.plan.begin = reinterpret_cast<int*>(ws + lay.begin);
   r.plan.count = reinterpret_cast<int*>(ws + lay.count);
   r.plan.tile0 = reinterpret_cast<int*>(ws + lay.tile0);
+  r.plan.high = reinterpret_cast<int*>(ws + lay.high);
   r.plan.tile_seg = reinterpret_cast<int*>(ws + lay.tile_seg);
   r.plan.pair = reinterpret_cast<int*>(ws + lay.pair);
   r.plan.weight = reinterpret_cast<float*>(ws + lay.pweight);
@@ -654,6 +658,7 @@ extern "C" gptq_status gptq_dequant_moe(const gptq_moe_args* args, int device, v
   m.act = a.act;
   m.dn_unit = std::min(gd, 128);
   m.h = ws + lay.h;
+  m.h_high = ws + lay.h_high;
   m.status = r.status;
   m.splits = lay.down.splits;
   m.partial = reinterpret_cast<float*>(ws + lay.partial);

@@ -791,6 +791,7 @@ __global__ void __launch_bounds__(DEC_THREADS)
 constexpr int MOE_MAX_T = 128;      // "few tokens": the down product keeps a row of sums per token in shared memory
 constexpr int MOE_MAX_E = 256;
 constexpr int MOE_MAX_TOPK = 16;
+constexpr float MOE_HIGH_UP = 268435456.0f, MOE_HIGH_DOWN = 1.0f / MOE_HIGH_UP;  // 2^28
 
 // The routing of one call (workspace).  The (token, choice) pairs are listed by expert, ascending
 // inside an expert; a segment is up to 8 NT consecutive pairs of one expert.  Its tiles of eight
@@ -801,6 +802,7 @@ struct MoePlan {
   int* begin;      // [segments] first list position
   int* count;      // [segments] pairs
   int* tile0;      // [segments] tiles of the segments before it
+  int* high;       // [segments] 1: some h of the segment is past fp16 and lies in h_high
   int* tiles;      // [1] all tiles
   int* tile_seg;   // [tiles] segment of a tile
   int* pair;       // [T * top_k] pair (token * top_k + choice) at a list position
@@ -820,6 +822,7 @@ struct MoeArgs {
   GroupIndex gu_gi, dn_gi;
   int act, dn_unit;
   uint8_t* h;  // fragment order, as x with I / 128 chunks
+  uint8_t* h_high;  // fp16: h 2^-28 of the values that are past fp16's largest, 0 for the others
   int splits;      // of the down product's list, beyond the cluster's
   float* partial;  // splits > 1: [splits][T][H]
   int* tickets;    // and a count per block of a split, zero before the call's down product
@@ -830,7 +833,10 @@ struct MoeArgs {
 };
 
 // h = act(x Wg^T) * (x Wu^T), rounded to the activations' type (the operand type of the second
-// product).  Grid (I / 64 * cluster, segments): a block's stage holds 64 gate rows and the same 64
+// product).  In fp16 a value that would round to infinity (65520 and above: a gated product has such
+// outliers, while Y, after the down weights, is small) goes into a second operand times 2^-28, which holds
+// up to 1.7e13 with all its 11 bits; the down product takes that operand too for segments that have one.
+// Grid (I / 64 * cluster, segments): a block's stage holds 64 gate rows and the same 64
 // up rows; a warp takes eight of each as rows 0-7 and 8-15 of its MMA, so both halves of an h value
 // end up in one lane.  Measured: 48 tokens, two of eight experts of 4096 x 11008, 139 us (2.6 TB/s);
 // 33 tokens, 8 of 64 experts of 2048 x 768 with 3 bits, 56 us.  The stream alone takes 67 and 25 us,
@@ -898,7 +904,8 @@ __global__ void __launch_bounds__(DEC_THREADS)
     __syncthreads();
   }
   constexpr int ITEMS = DEC_WARPS * NT * 32;
-  uint16_t* h = reinterpret_cast<uint16_t*>(p.h + static_cast<size_t>(tile0) * (p.I / 128) * FRAG_BYTES);
+  const size_t h_at = static_cast<size_t>(tile0) * (p.I / 128) * FRAG_BYTES;
+  uint16_t *h = reinterpret_cast<uint16_t*>(p.h + h_at), *h_high = reinterpret_cast<uint16_t*>(p.h_high + h_at);
   for (int i = rank * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x); i < ITEMS && !abort_flag;
        i += cs * static_cast<int>(blockDim.x)) {
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -912,9 +919,18 @@ __global__ void __launch_bounds__(DEC_THREADS)
     const int l = i & 31, t = (i >> 5) % NT, w = (i >> 5) / NT;
     const int col = i0 + 8 * w + (l >> 2), n = 2 * (l & 3);
     if (t < sg.tiles) {
-      uint16_t* d = h + (static_cast<size_t>(col >> 7) * sg.tiles + t) * (FRAG_BYTES / 2);
-      d[frag_offset(p.dn_unit, n, col & 127)] = f2h<BF>(act_apply(v.x, p.act) * v.z);
-      d[frag_offset(p.dn_unit, n + 1, col & 127)] = f2h<BF>(act_apply(v.y, p.act) * v.w);
+      const size_t at = (static_cast<size_t>(col >> 7) * sg.tiles + t) * (FRAG_BYTES / 2);
+      const float hv[2] = {act_apply(v.x, p.act) * v.z, act_apply(v.y, p.act) * v.w};
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const size_t o = at + frag_offset(p.dn_unit, n + j, col & 127);
+        const bool high = !BF && fabsf(hv[j]) >= 65520.0f;
+        h[o] = f2h<BF>(high ? 0.0f : hv[j]);
+        if (!BF) {
+          h_high[o] = f2h<BF>(high ? hv[j] * MOE_HIGH_DOWN : 0.0f);
+          if (high) p.plan.high[seg] = 1;
+        }
+      }
     }
   }
   if (cs > 1) cluster_sync();
@@ -967,13 +983,17 @@ __global__ void __launch_bounds__(DEC_THREADS)
       bool ok = true;
       for (int w = w0; w < w1 && ok;) {
         int seg;
-        const Segment sg = segment_at(w, seg);
-        for (int c = sg.c0; c < sg.c1; ++c, ++it) {
-          if (!r.codes(&codes_map, sg, c, it)) {
-            ok = false;
-            break;
+        Segment sg = segment_at(w, seg);
+        for (int high = BF ? 0 : p.plan.high[seg]; high >= 0 && ok; --high) {
+          if (high) sg.x += p.h_high - p.h;
+          for (int c = sg.c0; c < sg.c1; ++c, ++it) {
+            if (!r.codes(&codes_map, sg, c, it)) {
+              ok = false;
+              break;
+            }
+            r.acts(sg, c, it);
           }
-          r.acts(sg, c, it);
+          if (high) sg.x -= p.h_high - p.h;
         }
         w += sg.c1 - sg.c0;
       }
@@ -985,10 +1005,11 @@ __global__ void __launch_bounds__(DEC_THREADS)
     r.vec = p.dn_vec;
     r.gi = p.dn_gi;
     const int ra = warp * 16 + g, rb = ra + 8;
+    int high = -1;  // 1 while a segment's high operand comes, 0 for h itself, -1 before a segment
     for (int w = w0; w < w1;) {
       int seg;
       const Segment sg = segment_at(w, seg);
-      w += sg.c1 - sg.c0;
+      if (high < 0) high = BF ? 0 : p.plan.high[seg];
       float acc[NT][4];
 #pragma unroll
       for (int t = 0; t < NT; ++t)
@@ -1003,13 +1024,14 @@ __global__ void __launch_bounds__(DEC_THREADS)
         for (int j = 0; j < 2; ++j) {
           const int i = 8 * t + 2 * q + j;
           if (i < count) {
-            const float wt = p.plan.weight[begin + i];
+            const float wt = p.plan.weight[begin + i] * (high ? MOE_HIGH_UP : 1.0f);
             float* y = ysum + p.plan.pair[begin + i] / p.top_k * DEC_ROWS + ra;
             y[0] = fmaf(wt, acc[t][j], y[0]);
             y[8] = fmaf(wt, acc[t][2 + j], y[8]);
           }
         }
       __syncwarp();
+      if (--high < 0) w += sg.c1 - sg.c0;
     }
   }
   if (cs > 1) {

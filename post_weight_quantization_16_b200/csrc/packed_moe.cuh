@@ -356,6 +356,7 @@ __global__ void __launch_bounds__(ROUTER_WARPS * 32) moe_router_kernel(const Rou
       p.plan.begin[s] = begins[e] + k * per;
       p.plan.count[s] = min(per, n - k * per);
       p.plan.tile0[s] = tiles[e] + k * (per / 8);
+      p.plan.high[s] = 0;
     }
     for (int k = lane; k * 8 < n; k += 32) p.plan.tile_seg[tiles[e] + k] = slots[e] + k * 8 / per;
   }

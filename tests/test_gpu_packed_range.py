@@ -7,6 +7,7 @@ import torch
 from post_weight_quantization_16_b200 import gptq as G
 from tests import packed_helpers as H
 from tests.test_gpu_packed_linear import DEV, Case
+from tests.test_gpu_packed_moe import Moe
 
 pytestmark = pytest.mark.gpu
 KERNELS = [(20, 256), (300, 9472)]                    # tokens and columns of the single-block and of the pair kernel
@@ -104,3 +105,25 @@ def test_gradient_of_columns_and_rows_of_different_scales(T, n, bits, g):
     dY = c.dev(c.rng.normal(0, 1, (T, m)))
     Z = c.dev(np.ones((T, m)))
     gradient_close(c, G.dequant_linear_backward(dY, *c.layer), dY, Z, c.dt)
+
+
+@pytest.mark.parametrize("T,E,k,h,i,g,dg,dtype,perm", [
+    (1, 4, 2, 256, 256, 64, 128, "fp16", True), (6, 8, 3, 384, 128, 32, 32, "fp16", False),
+    (12, 2, 1, 256, 640, 128, 128, "fp16", True), (33, 4, 2, 256, 384, 64, 64, "fp16", True),
+    (128, 2, 2, 256, 256, 128, 128, "fp16", False), (33, 4, 2, 256, 384, 64, 64, "bf16", True)])
+@pytest.mark.parametrize("factor", [2.0 ** 9, 2.0 ** 17])
+def test_experts_gated_values_past_fp16(T, E, k, h, i, g, dg, dtype, perm, factor):
+    """A twentieth of the gate and up rows with |h| of up to 1e7 or 1e12 in every other expert, and down
+    weights there that bring Y back: finite, and as exact as without them."""
+    c = Moe(T, E, k, h, i, 4, g, dg, dtype, perm=perm, seed=3)
+    for e in range(0, E, 2):
+        rows = c.rng.choice(i, i // 20, replace=False)
+        for r in (rows, rows + i):
+            c.gate_up[1][e, torch.from_numpy(r).to(DEV)] *= factor
+            c.Wgu[e][r] *= factor
+        c.down[1][e] *= 2.0 ** -2 / factor ** 2
+        c.Wd[e] *= 2.0 ** -2 / factor ** 2
+    got = c.run()
+    assert got[0].isfinite().all()
+    c.check(got)
+    assert torch.equal(c.run()[0], got[0])
