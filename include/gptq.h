@@ -425,9 +425,11 @@ size_t gptq_dequant_linear_backward_workspace_bytes(int64_t T, int64_t m, int64_
 gptq_status gptq_dequant_linear_backward(const gptq_linear_grad_args* args, int device, void* cuda_stream);
 
 /* The mixture-of-experts layer for a few tokens, experts packed:
- *   p = softmax(X R^T) over the experts (64-bit); a token's top_k experts are those of the largest
- *   p, in descending order, ties to the lower expert (a NaN is chosen last); their weights are p,
- *   divided by their sum when renormalize is 1
+ *   p = softmax(X R^T) over the experts; a token's top_k experts are those of the largest p, in
+ *   descending order, ties to the lower expert (a NaN is chosen last), as 64-bit logits give them;
+ *   their weights are p, divided by their sum when renormalize is 1.  (A logit is summed in fp32 over
+ *   128 columns and in 64 bits beyond, off by at most 2^-16 of the sum of its products' magnitudes;
+ *   where that could change a choice or its place, the logits at stake are formed anew in 64 bits.)
  *   h = act(x Wg_e^T) * (x Wu_e^T)     rounded to dtype's significant bits (the second product's
  *                                      operand); |h| up to 1.7e13 in fp16, where it has a step of 2^-24
  *                                      below 2^-14

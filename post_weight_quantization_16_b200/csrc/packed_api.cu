@@ -274,7 +274,7 @@ DownSplit down_split(int64_t H, int64_t I, int64_t experts) {
 struct MoeLayout {
   int max_segments, max_tiles;
   DownSplit down;
-  size_t logits, ids, weights, segments, tiles, expert, begin, count, tile0, high, tile_seg, pair, pweight, x, h, h_high,
+  size_t logits, bounds, ids, weights, segments, tiles, expert, begin, count, tile0, high, tile_seg, pair, pweight, x, h, h_high,
       partial, tickets, total;
 };
 bool moe_layout(int64_t T, int64_t E, int64_t top_k, int64_t H, int64_t I, MoeLayout* l) {
@@ -292,6 +292,7 @@ bool moe_layout(int64_t T, int64_t E, int64_t top_k, int64_t H, int64_t I, MoeLa
   l->max_segments = static_cast<int>(std::min(pairs, std::min(E, pairs) + pairs / (8 * moe_nt(T, E, top_k))));
   l->max_tiles = static_cast<int>(std::min(pairs, std::min(E, pairs) + pairs / 8));
   l->logits = take(static_cast<size_t>(T) * E * 8);
+  l->bounds = take(static_cast<size_t>(T) * E * 4);
   l->ids = take(pairs * 4);
   l->weights = take(pairs * 4);
   l->segments = take(4);
@@ -594,6 +595,7 @@ extern "C" gptq_status gptq_dequant_moe(const gptq_moe_args* args, int device, v
   r.renorm = a.renormalize;
   r.seg_pairs = 8 * moe_nt(a.T, a.E, a.top_k);
   r.logits = reinterpret_cast<double*>(ws + lay.logits);
+  r.bounds = reinterpret_cast<float*>(ws + lay.bounds);
   r.ids = reinterpret_cast<int32_t*>(ws + lay.ids);
   r.weights = reinterpret_cast<float*>(ws + lay.weights);
   r.ids_out = a.ids_out;

@@ -103,6 +103,7 @@ struct RouterArgs {
   int T, E, H, top_k, renorm;
   int seg_pairs;       // pairs of a segment at most
   double* logits;      // [T x E] (workspace)
+  float* bounds;       // [T x E] of their errors (workspace)
   int32_t* ids;        // [T x top_k] (workspace)
   float* weights;      // [T x top_k] (workspace)
   int32_t* ids_out;    // the caller's copies, or null
@@ -113,21 +114,52 @@ struct RouterArgs {
   int* status;
 };
 
+// Bound of a logit's error by the sum S of its products' magnitudes: an MMA adds 16 products, exact in
+// fp32, to its addend with at least single precision, at most 16 roundings or truncations of 2^-23 of the
+// partial sum, and eight follow one another before fp64 takes over: 2^-16 S; 1.01 for S's own rounding.
+// (The largest seen is 2^-20.5 S, of tokens with outliers and of logits whose products are all positive.)
+constexpr float ROUTER_ERROR = 1.01f / 65536.0f;
+
+// The logit of one expert in fp64, by a warp: products, exact in fp32, are added in 64 bits in a fixed order.
+template <bool BF>
+__device__ __noinline__ double exact_logit(const uint16_t* __restrict__ x, const uint16_t* __restrict__ r, int H, int lane) {
+  double sum[4] = {0.0, 0.0, 0.0, 0.0};
+#pragma unroll 4
+  for (int c = lane * 8; c < H; c += 256) {
+    const uint4 a = *reinterpret_cast<const uint4*>(x + c), b = *reinterpret_cast<const uint4*>(r + c);
+    const uint32_t u[4] = {a.x, a.y, a.z, a.w}, v[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      sum[j] += static_cast<double>(h2f<BF>(u[j] & 0xFFFFu) * h2f<BF>(v[j] & 0xFFFFu));
+      sum[j] += static_cast<double>(h2f<BF>(u[j] >> 16) * h2f<BF>(v[j] >> 16));
+    }
+  }
+  double s = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return s;
+}
+
 // One cluster.  (1) Logits: tiles of 16 experts x 8 tokens go round the blocks, as many at a time as a
 // round of all needs; a tile's warps split H; products of 16-bit values are exact in fp32, 128 columns
-// are summed on the tensor cores and the partial sums of those in fp64, so the order of the choices is
-// that of the 64-bit logits but for logits that agree to about 1e-7.  (2) Softmax and top-k: a warp per
-// token, in fp64; equal values go to the lower expert; a NaN logit is chosen last (its weights are
-// NaN).  (3) The lists, in block 0: a thread per choice, whose place is what its expert has before its
+// are summed on the tensor cores and the partial sums of those in fp64; the same MMAs on the magnitudes
+// bound the error.  (2) Softmax and top-k: a warp per token, in fp64; equal values go to the lower expert;
+// a NaN logit is chosen last (its weights are NaN).  Where two of the largest top_k + 1 logits stand so
+// close that their errors could swap them, all logits at stake are formed again in fp64: the choices are
+// those of the 64-bit logits.  (3) The lists, in block 0: a thread per choice, whose place is what its expert has before its
 // group of 32 choices and its rank inside it, so positions are deterministic.
 // By its own clock: 7 us for two tokens over 32 experts (2048 wide), 18 for 33 over 64, of which 9 are the
 // logits (eight SMs fetch R and X, four trips to memory each), 5 the softmax and the choices, 4 the
-// lists and barriers (lists by a warp per expert took 7 more).
+// lists and barriers (lists by a warp per expert took 7 more); 1 for the errors' bounds and, where a
+// token's choices are formed again (one token in 15 there), 4.
 template <bool BF>
 __global__ void __launch_bounds__(ROUTER_WARPS * 32) moe_router_kernel(const RouterArgs p) {
   constexpr int CHOICES = MOE_MAX_T * MOE_MAX_TOPK, MINE = CHOICES / (ROUTER_WARPS * 32);
   __shared__ union {
-    double red[ROUTER_WARPS][128];             // (1)
+    struct {
+      double red[ROUTER_WARPS][128];
+      float mag[ROUTER_WARPS][128];
+    } l;                                        // (1)
     uint16_t before[CHOICES / 32 * MOE_MAX_E];  // (3) [group of choices][expert]
   } sh;
   __shared__ int counts[MOE_MAX_E];
@@ -152,6 +184,7 @@ __global__ void __launch_bounds__(ROUTER_WARPS * 32) moe_router_kernel(const Rou
     const uint16_t* rb = p.R + static_cast<size_t>(min(e0 + g + 8, p.E - 1)) * p.H + q * 8;
     const uint16_t* x = p.X + static_cast<size_t>(min(t0 + g, p.T - 1)) * p.ldx + q * 8;
     double acc[4] = {0.0, 0.0, 0.0, 0.0};
+    float mag[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     const int b0 = blocks * kw / KW, b1 = blocks * (kw + 1) / KW;
     uint4 na[4], nb[4], nx[4];
     auto load = [&](int b) {
@@ -179,21 +212,34 @@ __global__ void __launch_bounds__(ROUTER_WARPS * 32) moe_router_kernel(const Rou
         if (b + j < b1) {
           mma_16816<BF>(d, va[j].x, vb[j].x, va[j].y, vb[j].y, vx[j].x, vx[j].y);
           mma_16816<BF>(d, va[j].z, vb[j].z, va[j].w, vb[j].w, vx[j].z, vx[j].w);
+          constexpr uint32_t M = 0x7FFF7FFFu;
+          mma_16816<BF>(mag, va[j].x & M, vb[j].x & M, va[j].y & M, vb[j].y & M, vx[j].x & M, vx[j].y & M);
+          mma_16816<BF>(mag, va[j].z & M, vb[j].z & M, va[j].w & M, vb[j].w & M, vx[j].z & M, vx[j].w & M);
         }
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[j] += static_cast<double>(d[j]);
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) sh.red[warp][lane * 4 + j] = acc[j];
+    for (int j = 0; j < 4; ++j) {
+      sh.l.red[warp][lane * 4 + j] = acc[j];
+      sh.l.mag[warp][lane * 4 + j] = mag[j];
+    }
     __syncthreads();
     for (int k = threadIdx.x; k < at_once * 128; k += ROUTER_WARPS * 32) {
       const int mine = first + (k >> 7), i = k & 127;
       double v = 0.0;
-      for (int w = 0; w < KW; ++w) v += sh.red[(k >> 7) * KW + w][i];
+      float s = 0.0f;
+      for (int w = 0; w < KW; ++w) {
+        v += sh.l.red[(k >> 7) * KW + w][i];
+        s += sh.l.mag[(k >> 7) * KW + w][i];
+      }
       const int l = i >> 2, j = i & 3;
       const int e = (mine % et) * 16 + (l >> 2) + 8 * (j >> 1), t = (mine / et) * 8 + 2 * (l & 3) + (j & 1);
-      if (mine < ntiles && e < p.E && t < p.T) p.logits[static_cast<size_t>(t) * p.E + e] = v;
+      if (mine < ntiles && e < p.E && t < p.T) {
+        p.logits[static_cast<size_t>(t) * p.E + e] = v;
+        p.bounds[static_cast<size_t>(t) * p.E + e] = ROUTER_ERROR * s;
+      }
     }
     __syncthreads();
   }
@@ -202,57 +248,100 @@ __global__ void __launch_bounds__(ROUTER_WARPS * 32) moe_router_kernel(const Rou
   constexpr int PER = MOE_MAX_E / 32;
   const int per = (p.E + 31) / 32;
   for (int t = rank * ROUTER_WARPS + warp; t < p.T; t += ROUTER_CLUSTER * ROUTER_WARPS) {
-    // logits as keys whose unsigned order is theirs; a NaN comes after every number, a place past E
-    // is never taken (key 0)
     double v[PER], best = -INFINITY;
-    unsigned long long key[PER];
+    float bound = 0.0f;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      key[i] = 0;
       v[i] = 0.0;
       if (i < per && lane + 32 * i < p.E) {
         v[i] = __ldcg(p.logits + static_cast<size_t>(t) * p.E + lane + 32 * i);
-        const unsigned long long u = static_cast<unsigned long long>(__double_as_longlong(v[i] + 0.0));
-        key[i] = v[i] != v[i] ? 1ull : ((u >> 63) ? ~u : (u | 0x8000000000000000ull));
+        bound = fmaxf(bound, __ldcg(p.bounds + static_cast<size_t>(t) * p.E + lane + 32 * i));
         best = fmax(best, v[i]);
       }
     }
 #pragma unroll
-    for (int o = 16; o; o >>= 1) best = fmax(best, __shfl_xor_sync(0xffffffffu, best, o));
+    for (int o = 16; o; o >>= 1) {
+      best = fmax(best, __shfl_xor_sync(0xffffffffu, best, o));
+      bound = fmaxf(bound, __shfl_xor_sync(0xffffffffu, bound, o));
+    }
+    auto value = [](unsigned long long key) {
+      const unsigned long long u = (key >> 63) ? key & 0x7FFFFFFFFFFFFFFFull : ~key;
+      return __longlong_as_double(key == 1ull ? 0x7FF8000000000000ll : static_cast<long long>(u));
+    };
+    int my_id = 0;
+    unsigned long long my_key = 0;
+    const double apart = 2.0 * bound;
+    for (bool again = false;; again = true) {
+      // The largest logits in order, the k-th left to lane k.  As keys whose unsigned order is theirs: a
+      // NaN comes after every number, a place past E is never taken (key 0)
+      unsigned long long key[PER];
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const unsigned long long u = static_cast<unsigned long long>(__double_as_longlong(v[i] + 0.0));
+        key[i] = i < per && lane + 32 * i < p.E
+                     ? (v[i] != v[i] ? 1ull : ((u >> 63) ? ~u : (u | 0x8000000000000000ull)))
+                     : 0ull;
+      }
+      const int rounds = again ? p.top_k : min(p.top_k + 1, p.E);
+      for (int k = 0; k < rounds; ++k) {
+        unsigned long long bk = 0;
+        unsigned bi = 0xffffffffu;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+          if (i < per && key[i] > bk) {  // (equal keys: the lower expert stands first)
+            bk = key[i];
+            bi = lane + 32 * i;
+          }
+        const unsigned hi = __reduce_max_sync(0xffffffffu, static_cast<unsigned>(bk >> 32));
+        const bool top = static_cast<unsigned>(bk >> 32) == hi;
+        const unsigned lo = __reduce_max_sync(0xffffffffu, top ? static_cast<unsigned>(bk) : 0u);
+        const unsigned id = __reduce_min_sync(0xffffffffu, top && static_cast<unsigned>(bk) == lo ? bi : 0xffffffffu);
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+          if (static_cast<unsigned>(lane + 32 * i) == id) key[i] = 0;
+        if (lane == k) {
+          my_id = static_cast<int>(id);
+          my_key = (static_cast<unsigned long long>(hi) << 32) | lo;
+        }
+      }
+      if (again) break;
+      // bit k: the next one is less than `apart` below the k-th (a NaN is not)
+      const double mine = value(my_key), next = __shfl_down_sync(0xffffffffu, mine, 1);
+      const unsigned close = __ballot_sync(0xffffffffu, lane + 1 < rounds && mine - next < apart);
+      if (close == 0) break;
+      const uint16_t* x = p.X + static_cast<size_t>(t) * p.ldx;
+      const double least = __shfl_sync(0xffffffffu, mine, p.top_k - 1) - apart;
+      const bool border = (close >> (p.top_k - 1)) & 1u;
+      // These are formed again; and where the border of the choices is one of them, so is every other expert
+      // less than `apart` below the last choice (one further below is below all true choices).
+      unsigned picks = close | (close << 1);
+      for (int i = -1; i < (border ? per : 0); ++i) {
+        unsigned at = picks;
+        if (i >= 0) {
+          bool mine_too = false;
+#pragma unroll
+          for (int j = 0; j < PER; ++j) mine_too |= j == i && key[j] != 0 && v[j] >= least;
+          at = __ballot_sync(0xffffffffu, mine_too);
+        }
+        for (; at; at &= at - 1) {
+          const int l = __ffs(at) - 1, e = i < 0 ? __shfl_sync(0xffffffffu, my_id, l) : l + 32 * i;
+          const double d = exact_logit<BF>(x, p.R + static_cast<size_t>(e) * p.H, p.H, lane);
+#pragma unroll
+          for (int j = 0; j < PER; ++j)
+            if (lane + 32 * j == e) v[j] = d;
+        }
+      }
+    }
     double sum = 0.0;
 #pragma unroll
     for (int i = 0; i < PER; ++i)
       if (i < per && lane + 32 * i < p.E) sum += exp(v[i] - best);
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    int my_id = 0;
-    unsigned long long my_key = 0;
-    for (int k = 0; k < p.top_k; ++k) {
-      unsigned long long bk = 0;
-      unsigned bi = 0xffffffffu;
-#pragma unroll
-      for (int i = 0; i < PER; ++i)
-        if (i < per && key[i] > bk) {  // (equal keys: the lower expert stands first)
-          bk = key[i];
-          bi = lane + 32 * i;
-        }
-      const unsigned hi = __reduce_max_sync(0xffffffffu, static_cast<unsigned>(bk >> 32));
-      const bool top = static_cast<unsigned>(bk >> 32) == hi;
-      const unsigned lo = __reduce_max_sync(0xffffffffu, top ? static_cast<unsigned>(bk) : 0u);
-      const unsigned id = __reduce_min_sync(0xffffffffu, top && static_cast<unsigned>(bk) == lo ? bi : 0xffffffffu);
-#pragma unroll
-      for (int i = 0; i < PER; ++i)
-        if (static_cast<unsigned>(lane + 32 * i) == id) key[i] = 0;
-      if (lane == k) {
-        my_id = static_cast<int>(id);
-        my_key = (static_cast<unsigned long long>(hi) << 32) | lo;
-      }
-    }
     // (top_k <= E: every round finds an expert)
     double mine = 0.0;
     if (lane < p.top_k) {
-      const unsigned long long u = (my_key >> 63) ? my_key & 0x7FFFFFFFFFFFFFFFull : ~my_key;
-      mine = my_key == 1ull ? __longlong_as_double(0x7FF8000000000000ll) : exp(__longlong_as_double(static_cast<long long>(u)) - best);
+      mine = exp(value(my_key) - best);
     }
     if (p.renorm) {
       sum = mine;

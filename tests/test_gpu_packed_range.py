@@ -127,3 +127,56 @@ def test_experts_gated_values_past_fp16(T, E, k, h, i, g, dg, dtype, perm, facto
     assert got[0].isfinite().all()
     c.check(got)
     assert torch.equal(c.run()[0], got[0])
+
+
+def choices64(x, r, k):
+    """The k largest logits of 64 bits, descending, ties to the lower expert; no two of x r^T that the
+    choices hang on are closer than 64 bits can tell."""
+    logits = x @ r.T
+    ids = np.argsort(-logits, axis=1, kind="stable")
+    s = np.take_along_axis(logits, ids, 1)
+    gap = np.abs(np.diff(s, axis=1))[:, : k]
+    noise = 2.0 ** -53 * x.shape[1] ** 0.5 * (np.abs(x) @ np.abs(r).T).max()
+    assert (gap > 100 * noise).all()
+    return ids[:, :k], logits
+
+
+@pytest.mark.parametrize("T,E,k,h,dtype", [(1, 64, 8, 2048, "fp16"), (33, 64, 8, 2048, "bf16"), (128, 256, 16, 512, "fp16"),
+                                           (17, 34, 5, 4096, "bf16"), (9, 6, 6, 1152, "fp16")])
+@pytest.mark.parametrize("outlier", [1.0, 1000.0])
+def test_choices_are_those_of_64_bit_logits(T, E, k, h, dtype, outlier):
+    """Pairs of experts whose logits agree to far fewer bits than fp32 holds of their sums: half of the
+    rows are the others with one entry a step away, and a few channels of X are large."""
+    c = Moe(T, E, k, h, 128, 4, 128, 128, dtype, perm=False, seed=5)
+    X = c.X.double()
+    X[:, torch.from_numpy(c.rng.choice(h, 4, replace=False)).to(DEV)] *= outlier
+    X = X.to(c.dt)
+    r = c.router.clone()
+    for e in range(E // 2):
+        r[e + E // 2] = r[e]
+        at = int(c.rng.integers(h))
+        r[e + E // 2, at] *= 1 + 4 * H.EPS[c.dt]
+    x, rr = H.to64(X), H.to64(r)
+    near = (rr[: E // 2] != rr[E // 2: 2 * (E // 2)]).sum(1)
+    assert (near == 1).all()
+    want, logits = choices64(x, rr, k)
+    y, ids, w = c.run(X=X, router=r)
+    assert np.array_equal(ids.cpu().numpy(), want)
+    p = np.exp(logits - logits.max(1, keepdims=True))
+    p = np.take_along_axis(p, want, 1)
+    p /= p.sum(1, keepdims=True)
+    # the chosen weights: fp32 after logits that are off by at most 2^-16 of their products' magnitudes
+    b = 2.0 ** -16 * (np.abs(x) @ np.abs(rr).T).max(1, keepdims=True)
+    assert (np.abs(H.to64(w) - p) <= p * (4 * np.minimum(b, 1) + 2.0 ** -22) + 1e-30).all()
+
+
+def test_tokens_of_zeros_and_equal_experts():
+    """Padding rows (every logit 0) and routers of equal rows: the lowest experts, in order."""
+    c = Moe(20, 40, 4, 256, 128, 4, 64, 64, "bf16")
+    X = c.X.clone()
+    X[::2] = 0
+    y, ids, w = c.run(X=X)
+    assert (ids[::2].cpu().numpy() == np.arange(4)).all() and (w[::2] == 0.25).all() and (y[::2] == 0).all()
+    r = c.router[:1].expand(40, -1).contiguous()
+    y, ids, w = c.run(router=r)
+    assert (ids.cpu().numpy() == np.arange(4)).all() and (w == 0.25).all()
