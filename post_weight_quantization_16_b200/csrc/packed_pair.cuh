@@ -449,10 +449,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PR_THREADS, 1)
             for (int j = 0; j < 128; ++j) acc[j] = acc[j] > 0.0f ? acc[j] : 0.0f;
           } else if (p.lin.act == ACT_SILU) {
 #pragma unroll
-            for (int j = 0; j < 128; ++j) acc[j] = silu_fast(acc[j]);
+            for (int j = 0; j < 128; ++j) acc[j] = silu(acc[j]);
           } else if (p.lin.act == ACT_GELU) {
 #pragma unroll
-            for (int j = 0; j < 128; ++j) acc[j] = gelu_fast(acc[j]);
+            for (int j = 0; j < 128; ++j) acc[j] = gelu(acc[j]);
           }
 #pragma unroll
           for (int cc = 0; cc < 16; ++cc) {
