@@ -100,3 +100,27 @@ def test_the_largest_values_and_infinity():
             z = X[:, :1].float().expand(-1, m)
             low = z == float("-inf")
             assert y[low].isnan().all() and torch.equal(y[~low], z[~low].clamp(min=0))
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_gradient_by_the_bias_sum(dtype, act):
+    """dbias of one token with dY = 1 is act'(Z) itself, in fp32: off by less than 2^-20 of its largest value,
+    1.13, and, where it is a single product far from its zero, by 2^-18 of itself."""
+    m, n = 8192, 128
+    w = layer(m, n, np.ones(m, dtype=np.float32))
+    z = np.concatenate([np.linspace(-60, 60, m // 2), np.linspace(-4, 4, m // 2)])
+    Z = torch.from_numpy(z).to(DEV).to(dtype)[None].contiguous()
+    one = torch.ones_like(Z)
+    k = G.ACT_SILU if act == "silu" else G.ACT_GELU
+    got = G.dequant_linear_backward(one, *w, None, 4, -1, act=k, preact=Z, want_dx=False, want_dbias=True)[1]
+    got, z = got.double().cpu().numpy(), Z.double().cpu().numpy()[0]
+    if act == "silu":
+        want = expit(z) * (1 + z * expit(-z))
+        far = z < -2
+    else:
+        want = ndtr(z) + z * np.exp(-z * z / 2) / np.sqrt(2 * np.pi)
+        far = (z < -2) & (z > -12.5)
+    d = np.abs(got - want)
+    assert (d <= 1.13 * 2.0 ** -20).all(), np.log2(d.max())
+    assert (d[far] <= 2.0 ** -18 * np.abs(want[far])).all(), np.log2((d[far] / np.abs(want[far])).max())
