@@ -406,7 +406,7 @@ gptq_status gptq_dequant_linear(const gptq_linear_args* args, int device, void* 
  *              neither dY nor preact; or NULL
  *   dbias    : device fp32 [m], or NULL (zeros when T is 0)
  *   workspace: as above, gptq_dequant_linear_backward_workspace_bytes
- * At least one output.  Asynchronous on cuda_stream, capturable, deterministic. */
+ * At least one output when T > 0.  Asynchronous on cuda_stream, capturable, deterministic. */
 typedef struct {
   const void* dY;
   int64_t T, ld_dy;

@@ -428,7 +428,7 @@ extern "C" gptq_status gptq_dequant_linear_backward(const gptq_linear_grad_args*
   GradLayout need, lay;
   if (!valid_packed(a.W) || !grad_layout(a.T, a.W.m, a.W.n, a.W.perm ? 1 : 0, a.dtype, a.act, false, &need))
     return GPTQ_ERR_ARG;
-  if (!a.dX && !a.dbias) return GPTQ_ERR_ARG;
+  if (a.T > 0 && !a.dX && !a.dbias) return GPTQ_ERR_ARG;  // (an empty dX may have no address)
   if (!aligned_to(a.dbias, 4) || (a.T > 0 && a.ld_dy < a.W.m) || (a.T > 0 && a.dX && a.ld_dx < a.W.n) ||
       !aligned_to(a.dX, 2))
     return GPTQ_ERR_ARG;

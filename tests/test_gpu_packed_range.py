@@ -180,3 +180,11 @@ def test_tokens_of_zeros_and_equal_experts():
     r = c.router[:1].expand(40, -1).contiguous()
     y, ids, w = c.run(router=r)
     assert (ids.cpu().numpy() == np.arange(4)).all() and (w == 0.25).all()
+
+
+@pytest.mark.parametrize("act", ["none", "silu"])
+def test_gradient_of_no_tokens(act):
+    c = Case(4, 33, 256, 4, 64, "fp16", act, True)
+    e = torch.empty(0, 33, dtype=c.dt, device=DEV)
+    dx = G.dequant_linear_backward(e, *c.layer, act=H.ACTS[act], preact=e)
+    assert dx.shape == (0, 256) and dx.dtype == c.dt

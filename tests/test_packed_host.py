@@ -238,3 +238,10 @@ def test_stack_experts_refuses_layers_with_a_channel_scale():
             parts[at][e] = scaled
             with pytest.raises(ValueError, match=f"expert {e}: {name} has a channel_scale"):
                 G.stack_experts(*parts)
+
+
+def test_gradient_of_no_tokens_without_an_address(L):
+    """An empty dX, as an allocator hands it out, has no address: nothing to do, not a missing output."""
+    assert backward(L, T=0, dY=0, dX=0, ws=0) == G.OK
+    assert backward(L, T=0, dY=0, dX=0, ws=0, act=3, dtype=1) == G.OK
+    assert backward(L, T=1, dX=0) == G.ERR_ARG
