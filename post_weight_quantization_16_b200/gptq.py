@@ -417,11 +417,23 @@ def _workspace(need: int, workspace: torch.Tensor | None, like: torch.Tensor) ->
     return workspace
 
 
+def check_workspace(workspace: torch.Tensor, stream: torch.cuda.Stream | None = None):
+    """Wait (bounded) for `stream` (default: the workspace's device's current one) and raise GPTQError with
+    status ERR_TIMEOUT if a bounded wait of the last dequant_matmul, dequant_linear, dequant_linear_backward
+    or dequant_moe on this workspace ran out: its outputs are then not to be used.  (A call without tokens
+    leaves the workspace as it was.)  Not while a graph is captured; after a replay it tells of that."""
+    index = workspace.get_device()
+    if index < 0 or workspace.dtype != torch.uint8 or workspace.numel() < 256:
+        raise ValueError("workspace must be a uint8 device tensor that a call was given")
+    handle = _raw_stream(index) if stream is None else stream.cuda_stream
+    _check(lib().gptq_dequant_matmul_check(workspace.data_ptr(), index, handle), "a call on this workspace")
+
+
 def dequant_linear(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor,
                    perm: torch.Tensor | None, bits: int, group_size: int, bias: torch.Tensor | None = None,
                    act: int = ACT_NONE, residual: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
                    want_preact: bool = False, out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
-                   stream: torch.cuda.Stream | None = None):
+                   stream: torch.cuda.Stream | None = None, check: bool = False):
     """Y = act(X[:, perm] W^T + bias) + residual with a packed W (gptq_dequant_linear).  X: fp16 or
     bf16 [T, n] device tensor in original column order (row stride a multiple of 8); codes, scales,
     zeros, perm as quantize_layer (or rtn_quantize: perm None) wrote them (the product is with the scaled
@@ -431,11 +443,13 @@ def dequant_linear(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, z
     activation was applied to, which dequant_linear_backward takes.  `out` may be `residual`,
     but not share memory with X.
     Asynchronous on `stream` (default: the device's current one; another stream's allocations are made
-    on it); can be captured into a graph."""
+    on it); can be captured into a graph.  check: wait for the call and raise if one of its bounded waits
+    ran out (check_workspace does that for a caller's workspace, later or after a graph's replay).  Records
+    no autograd graph: Y does not require a gradient, dequant_linear_backward is the call for it."""
     if _elsewhere(stream, X):
         with _On(stream):
             return dequant_linear(X, codes, scales, zeros, perm, bits, group_size, bias, act, residual, out_dtype,
-                                  want_preact, out, workspace)
+                                  want_preact, out, workspace, check=check)
     index = X.get_device()
     W = _packed(codes, scales, zeros, perm, bits, group_size, index)
     m, n = W[4], W[5]
@@ -466,6 +480,8 @@ def dequant_linear(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, z
     st = L.gptq_dequant_linear(a, index, _raw_stream(index))
     if st != OK:
         raise GPTQError(st, "gptq_dequant_linear")
+    if check and T:
+        check_workspace(ws)
     return (out, z) if want_preact else out
 
 
@@ -473,15 +489,16 @@ def dequant_linear_backward(dY: torch.Tensor, codes: torch.Tensor, scales: torch
                             perm: torch.Tensor | None, bits: int, group_size: int, act: int = ACT_NONE,
                             preact: torch.Tensor | None = None, want_dx: bool = True, want_dbias: bool = False,
                             out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
-                            stream: torch.cuda.Stream | None = None):
+                            stream: torch.cuda.Stream | None = None, check: bool = False):
     """The gradient of dequant_linear with W frozen (gptq_dequant_linear_backward).  dY: fp16 or bf16
     [T, m]; preact: the Z that dequant_linear(want_preact=True) gave (needed unless act is ACT_NONE).
     Returns dX [T, n] in dY's type, or (dX, dbias) with want_dbias (dbias fp32 [m]; dX is None with
-    want_dx=False).  The residual's gradient is dY itself.  Asynchronous on `stream`."""
+    want_dx=False).  The residual's gradient is dY itself.  Asynchronous on `stream`; check as in
+    dequant_linear."""
     if _elsewhere(stream, dY):
         with _On(stream):
             return dequant_linear_backward(dY, codes, scales, zeros, perm, bits, group_size, act, preact, want_dx,
-                                           want_dbias, out, workspace)
+                                           want_dbias, out, workspace, check=check)
     index = dY.get_device()
     W = _packed(codes, scales, zeros, perm, bits, group_size, index)
     m, n = W[4], W[5]
@@ -508,6 +525,8 @@ def dequant_linear_backward(dY: torch.Tensor, codes: torch.Tensor, scales: torch
     st = L.gptq_dequant_linear_backward(a, index, _raw_stream(index))
     if st != OK:
         raise GPTQError(st, "gptq_dequant_linear_backward")
+    if check and T:
+        check_workspace(ws)
     return (dx, db) if want_dbias else dx
 
 
@@ -515,17 +534,18 @@ def dequant_moe(X: torch.Tensor, router: torch.Tensor, gate_up: tuple, down: tup
                 bits: int, group_size: int, top_k: int, renormalize: bool = True, act: int = ACT_SILU,
                 residual: torch.Tensor | None = None, down_group_size: int | None = None,
                 out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
-                stream: torch.cuda.Stream | None = None):
+                stream: torch.cuda.Stream | None = None, check: bool = False):
     """The mixture-of-experts layer for at most 128 tokens on packed experts (gptq_dequant_moe).
     X: fp16 or bf16 [T, H]; router [E, H] in X's type; gate_up = (codes [E, 2 I, words], scales, zeros)
     with the gate rows first; down = (codes [E, H, words], scales, zeros); perm: int32 [E, H], the
     act-order of each expert's gate and up, or None (stack_experts builds these from quantized
     layers).  Returns Y [T, H], the chosen experts [T, top_k] (int32, by descending probability) and
-    their weights [T, top_k] (fp32).  `out` may be X or `residual`.  Asynchronous on `stream`."""
+    their weights [T, top_k] (fp32).  `out` may be X or `residual`.  Asynchronous on `stream`; check as in
+    dequant_linear."""
     if _elsewhere(stream, X):
         with _On(stream):
             return dequant_moe(X, router, gate_up, down, perm, bits, group_size, top_k, renormalize, act, residual,
-                               down_group_size, out, workspace)
+                               down_group_size, out, workspace, check=check)
     index = X.get_device()
     E = router.shape[0] if router.dim() == 2 else 0
     if E == 0:
@@ -551,6 +571,8 @@ def dequant_moe(X: torch.Tensor, router: torch.Tensor, gate_up: tuple, down: tup
     st = L.gptq_dequant_moe(a, index, _raw_stream(index))
     if st != OK:
         raise GPTQError(st, "gptq_dequant_moe")
+    if check and T:
+        check_workspace(ws)
     return out, ids, weights
 
 
