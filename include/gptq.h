@@ -368,8 +368,8 @@ enum { GPTQ_ACT_NONE = 0, GPTQ_ACT_RELU = 1, GPTQ_ACT_GELU = 2, GPTQ_ACT_SILU = 
  *   preact   : device, dtype, [T x m] contiguous, receives Z (the backward pass's input), or NULL
  *   workspace: device, 256-byte aligned, at least gptq_dequant_linear_workspace_bytes (a status
  *              word for gptq_dequant_matmul_check, which each call with T > 0 sets, and, with a perm
- *              or at most 16 tokens, X in the kernels' order); owned by the caller, may be reused by later calls on the same stream; calls that can run at the
- *              same time need one each
+ *              or at most 16 tokens, X in the kernels' order); owned by the caller, may be reused by
+ *              later calls on the same stream; calls that can run at the same time need one each
  * Asynchronous on cuda_stream; no allocation and no synchronization, so a call can be captured
  * into a graph; arguments are checked before any launch; the result is deterministic. */
 typedef struct {

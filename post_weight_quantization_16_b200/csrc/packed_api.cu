@@ -1,5 +1,5 @@
 // packed_api.cu — the C ABI of the products on packed layers (include/gptq.h: gptq_dequant_linear,
-// gptq_dequant_moe): argument checks, workspace layout and launches.
+// gptq_dequant_linear_backward, gptq_dequant_moe): argument checks, workspace layout and launches.
 #include <algorithm>
 #include <utility>
 
@@ -485,8 +485,8 @@ extern "C" gptq_status gptq_dequant_linear_backward(const gptq_linear_grad_args*
       constexpr int A = decltype(k)::value;
       const auto kernel = bf ? (m <= 4096 ? act_grad_kernel<true, A, 1> : act_grad_kernel<true, A, 3>)
                              : (m <= 4096 ? act_grad_kernel<false, A, 1> : act_grad_kernel<false, A, 3>);
-      return launch_pdl(kernel, dim3(cols.chunks + (h ? T : 0)), dim3(512), 0, 1, st, dY, a.ld_dy, Z, m, vec, h, o, lay.ldz,
-                        reinterpret_cast<float*>(ws + lay.scale), cols);
+      return launch_pdl(kernel, dim3(cols.chunks + (h ? T : 0)), dim3(512), 0, 1, st, dY, a.ld_dy, Z, m, vec, h, o,
+                        lay.ldz, reinterpret_cast<float*>(ws + lay.scale), cols);
     }));
     if (h) {
       ldz = lay.ldz;

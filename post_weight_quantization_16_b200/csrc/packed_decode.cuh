@@ -152,17 +152,8 @@ __device__ __forceinline__ uint32_t fma2_f16(uint32_t a, uint32_t b, uint32_t c)
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// Wait of a whole warp: one lane polls, so that the warp stays converged (the MMAs and tensor-memory
-// loads that follow are warp-wide instructions; lanes that each leave a polling loop on their own
-// need not run together afterwards), then the barrier's completion is made known to the others.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int lane) {
-  int ok = 1;
-  if (lane == 0) ok = mbar_wait_bounded(bar, parity, abort_flag) ? 1 : 0;
-  __syncwarp();
-  return __shfl_sync(0xffffffffu, ok, 0) != 0;
-}
-
-// The same with all lanes testing the barrier together and one decision for the warp: no branch by lane.
+// Bounded wait of a whole warp: all lanes test the barrier together and take one decision, so that the warp
+// stays converged (the MMAs and tensor-memory loads that follow are warp-wide instructions).
 __device__ __forceinline__ bool warp_wait_uniform(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   uint64_t t0 = 0;
@@ -706,7 +697,6 @@ __device__ __forceinline__ float ld_dsmem_f(uint32_t addr) {
 // 4096 x 11008 22 us (1.2 TB/s).  The first is a launch, one trip to memory, a few chunks and the
 // cluster's sums, one after the other; the stream alone of the second (no unpacking, no products)
 // takes 12 us, and the rest is the instructions of 16 tokens' products with 16 warps an SM.
-constexpr int DEC_MAX_TILES = 4;
 constexpr int DEC_LOCAL_BYTES = 32 * 1024;  // local activations of a block at most
 
 struct LinearDecodeArgs {

@@ -45,7 +45,7 @@ __device__ __forceinline__ float at8(const uint4& v, int j) {
 __device__ __forceinline__ void column_exponent(const float* __restrict__ scales, int m, int G, GroupIndex gi, int per,
                                                 int bits, int chunk, int* __restrict__ out) {
   __shared__ float wmax[16];
-  const float* first = scales + (per > 1 ? chunk * per : gi.div == 1 ? chunk : static_cast<int>(__umulhi(static_cast<uint32_t>(chunk), gi.magic)));
+  const float* first = scales + (per > 1 ? chunk * per : group_of<128>(gi, chunk, 0));
   const int shift = per == 4 ? 2 : per - 1;  // per: groups of the block, 1, 2 or 4
   float mx = 0.0f;
 #pragma unroll 8

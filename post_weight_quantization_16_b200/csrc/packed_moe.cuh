@@ -10,8 +10,8 @@ namespace gptq {
 // out[t][k] = X[t][perm[k]] in rows of n: rows pass through shared memory, so that global reads and
 // writes are whole lines, the gather itself is from shared memory and a block reads the order once.
 // PAIR: two rows at a time, interleaved as 32-bit words there, so that one 32-bit gather (conflicts
-// of random banks are its cost) serves both: 4096 x 28672 values in 108 us (4.4 TB/s).  Grid (tokens / rows rounded up), dynamic shared memory
-// rows * n * 2 bytes, rows even with PAIR.
+// of random banks are its cost) serves both: 4096 x 28672 values in 108 us (4.4 TB/s).  Grid (tokens /
+// rows rounded up), dynamic shared memory rows * n * 2 bytes, rows even with PAIR.
 template <bool PAIR>
 __global__ void __launch_bounds__(512) gather_x_kernel(const uint16_t* __restrict__ X, int64_t ldx, int T, int n,
                                                        const int32_t* __restrict__ perm, int rows,

@@ -245,3 +245,36 @@ def test_gradient_of_no_tokens_without_an_address(L):
     assert backward(L, T=0, dY=0, dX=0, ws=0) == G.OK
     assert backward(L, T=0, dY=0, dX=0, ws=0, act=3, dtype=1) == G.OK
     assert backward(L, T=1, dX=0) == G.ERR_ARG
+
+
+def test_argument_blocks_hold_every_field_where_c_does():
+    """A distinct value for each field of the binding's argument blocks, read back at the offset and with the
+    type that the header's declaration gives it."""
+    text = re.sub(r"/\*.*?\*/", "", open(G.HEADER).read(), flags=re.S)
+    scalars = {"int64_t": "q", "size_t": "Q", "int": "i", "double": "d"}
+
+    def fields(name):
+        """[(member, offset, format)] of the flattened structure, its size and its alignment"""
+        out, off, most = [], 0, 1
+        for decl in re.search(r"typedef struct \{([^}]*)\} %s;" % name, text).group(1).split(";"):
+            if not decl.split():
+                continue
+            base, rest = re.match(r"\s*(?:const\s+)?(\w+)(.*)", decl, re.S).groups()
+            for var in rest.split(","):
+                if "*" in var or base in scalars:
+                    kind = "Q" if "*" in var else scalars[base]
+                    sub, size, al = [("", 0, kind)], struct.calcsize(kind), struct.calcsize(kind)
+                else:
+                    sub, size, al = fields(base)
+                off = -(-off // al) * al
+                out += [(var.strip(" *\n") + "." + n, off + o, k) for n, o, k in sub]
+                off, most = off + size, max(most, al)
+        return out, -(-off // most) * most, most
+
+    for name, fmt in (("gptq_linear_args", G._LINEAR_ARGS), ("gptq_linear_grad_args", G._LINEAR_GRAD_ARGS),
+                      ("gptq_moe_args", G._MOE_ARGS)):
+        want, size, _ = fields(name)
+        assert size == fmt.size, name
+        block = fmt.pack(*range(101, 101 + len(want)))                        # (as many values as C has members)
+        for value, (member, offset, kind) in enumerate(want, 101):
+            assert struct.unpack_from("@" + kind, block, offset)[0] == value, (name, member)
