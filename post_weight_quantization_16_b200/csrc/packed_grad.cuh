@@ -8,7 +8,7 @@ namespace gptq {
 
 // act'(z), off by less than 2^-20 of its largest value, 1.13, and far from its zero by less than 2^-18 of
 // itself: dz keeps 11 bits (22 in two parts), and what the bias's gradient sums is off by no more than the
-// rest of its terms.  (SiLU's power in the epilogue's form: 4096 x 11008 values in 61 us, not 58.)
+// rest of its terms.  (With the epilogue's form of SiLU's power the bias's pass takes 3 us more of 58.)
 template <int ACT>
 __device__ __forceinline__ float act_grad(float z) {
   if (ACT == ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
@@ -57,9 +57,11 @@ __device__ __forceinline__ void column_exponent(const float* __restrict__ scales
   for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   if ((threadIdx.x & 31) == 0) wmax[threadIdx.x >> 5] = mx;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < 16; ++w) mx = fmaxf(mx, wmax[w]);
-    out[chunk] = mx > 0.0f ? min(126, max(-126, 14 - bits - ilogbf(mx))) : 0;
+  if (threadIdx.x < 32) {
+    mx = wmax[threadIdx.x & 15];
+#pragma unroll
+    for (int o = 8; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    if (threadIdx.x == 0) out[chunk] = mx > 0.0f ? min(126, max(-126, 14 - bits - ilogbf(mx))) : 0;
   }
 }
 
@@ -78,7 +80,8 @@ struct ColumnArgs {
 // largest |dY| would not do: an outlier that act' masks would push what is left into fp16's subnormals.)
 // Rows of ldz (a multiple of 8) elements.  A thread keeps its first KEPT eights of dz in registers: 1 for
 // rows of up to 4096 values, else 3, where 12288 are read and act' evaluated once; what is beyond is
-// computed again.  vec: rows of dY and Z allow 16-byte accesses.
+// computed again.  vec: rows of dY and Z allow 16-byte accesses.  4096 x 11008 values with SiLU: 53 us
+// (5.1 TB/s; 67 where each load waited for the one before it).
 template <bool BF, int ACT, int KEPT>
 __global__ void __launch_bounds__(512) act_grad_kernel(const uint16_t* __restrict__ dY, int64_t ld_dy,
                                                        const uint16_t* __restrict__ Z, int m, int vec,
@@ -95,14 +98,14 @@ __global__ void __launch_bounds__(512) act_grad_kernel(const uint16_t* __restric
   const size_t t = blockIdx.x - cols.chunks;
   const uint16_t* dy = dY + t * ld_dy;
   const uint16_t* z = Z + t * m;
-  // eight values of dz from column r
-  auto eight = [&](int r, float (&x)[8]) {
-    const bool whole = vec && r + 8 <= m;
-    const uint4 v = load8(dy + r, whole, m - r);
-    uint4 zv = {};
-    if (ACT != ACT_NONE) zv = load8(z + r, whole, m - r);
+  // eight values of dz
+  auto eight = [&](const uint4& v, const uint4& zv, float (&x)[8]) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) x[j] = at8<BF>(v, j) * (ACT != ACT_NONE ? act_grad<ACT>(at8<BF>(zv, j)) : 1.0f);
+  };
+  auto load = [&](int r, bool whole, uint4& v, uint4& zv) {
+    v = load8(dy + r, whole, m - r);
+    if (ACT != ACT_NONE) zv = load8(z + r, whole, m - r);
   };
   float mx = 0.0f;
   auto largest = [&](const float (&x)[8]) {
@@ -113,17 +116,30 @@ __global__ void __launch_bounds__(512) act_grad_kernel(const uint16_t* __restric
     }
   };
   float kept[KEPT][8];
+  {
+    uint4 v[KEPT], zv[KEPT];
+    // (the wide loads first, all in flight together)
 #pragma unroll
-  for (int k = 0; k < KEPT; ++k) {
-    const int r = static_cast<int>(threadIdx.x) * 8 + k * 4096;
-    if (r < m) {
-      eight(r, kept[k]);
-      largest(kept[k]);
+    for (int k = 0; k < KEPT; ++k) {
+      const int r = static_cast<int>(threadIdx.x) * 8 + k * 4096;
+      v[k] = zv[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (vec && r + 8 <= m) load(r, true, v[k], zv[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < KEPT; ++k) {
+      const int r = static_cast<int>(threadIdx.x) * 8 + k * 4096;
+      if (r < m) {
+        if (!(vec && r + 8 <= m)) load(r, false, v[k], zv[k]);
+        eight(v[k], zv[k], kept[k]);
+        largest(kept[k]);
+      }
     }
   }
   for (int r = threadIdx.x * 8 + KEPT * 4096; r < m; r += 4096) {
+    uint4 v, zv = {};
     float x[8];
-    eight(r, x);
+    load(r, vec && r + 8 <= m, v, zv);
+    eight(v, zv, x);
     largest(x);
   }
 #pragma unroll
@@ -156,8 +172,10 @@ __global__ void __launch_bounds__(512) act_grad_kernel(const uint16_t* __restric
     if (r < m) store(r, kept[k]);
   }
   for (int r = threadIdx.x * 8 + KEPT * 4096; r < m; r += 4096) {
+    uint4 v, zv = {};
     float x[8];
-    eight(r, x);
+    load(r, vec && r + 8 <= m, v, zv);
+    eight(v, zv, x);
     store(r, x);
   }
 }
