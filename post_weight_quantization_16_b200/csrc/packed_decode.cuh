@@ -47,7 +47,8 @@ enum : int { ACT_NONE = 0, ACT_RELU = 1, ACT_GELU = 2, ACT_SILU = 3 };
 
 // One form each for all kernels, so that a value does not depend on the number of tokens, and short: the
 // CTA-pair kernel's epilogue holds 128 of them a thread, unrolled, and longer code costs it more than its
-// operations do (2048 tokens through 11008 x 4096: 294 us with expf, 256 with these).
+// operations do (2048 tokens through 11008 x 4096 with SiLU: 294 us with expf, 263 with these, 254 with a plain
+// __expf whose error grows with |z|).
 __device__ __forceinline__ float ex2_ftz(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -872,7 +873,7 @@ struct MoeArgs {
 // Grid (I / 64 * cluster, segments): a block's stage holds 64 gate rows and the same 64
 // up rows; a warp takes eight of each as rows 0-7 and 8-15 of its MMA, so both halves of an h value
 // end up in one lane.  Measured: 48 tokens, two of eight experts of 4096 x 11008, 139 us (2.6 TB/s);
-// 33 tokens, 8 of 64 experts of 2048 x 768 with 3 bits, 56 us.  The stream alone takes 67 and 25 us,
+// 33 tokens, 8 of 64 experts of 2048 x 768 with 3 bits, 57 us.  The stream alone takes 67 and 25 us,
 // without the unpacking and the products 108 and 41: instruction issue and latency with 16 to 24 warps
 // an SM, no single pipe (the fullest, the integer one, is busy for half of the time).
 template <int BITS, bool BF, int GU, int NT, bool XL>

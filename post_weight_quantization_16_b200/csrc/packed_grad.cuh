@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(512) act_grad_kernel(const uint16_t* __restric
 // dbias[r] = sum over tokens of dY act'(Z), in fp32.  A block takes 256 columns, a lane eight of them
 // and a warp every DBIAS_WARPS-th token of its block's stripe; the eight blocks of a cluster take the
 // stripes; sums meet in a fixed order.  (One pass that also writes dz, with the sums in registers, was
-// slower: 237 us against 88 + 84 on 4096 x 11008 values, too few loads in flight; 57 + 58 since, 3.1 TB/s
+// slower: 237 us against 88 + 84 on 4096 x 11008 values, too few loads in flight; 53 + 58 since, 3.1 TB/s
 // here: act' by the special functions.)
 constexpr int DBIAS_CLUSTER = 8, DBIAS_WARPS = 8, DBIAS_COLS = 256;
 template <bool BF, int ACT>

@@ -21,9 +21,10 @@
 // the sums live in the drain warps' registers (128 each, hence the register split), whose epilogue
 // overlaps the producers' next tile.  Gradient: they alternate by tile, so that a tile's epilogue
 // overlaps the next tile's MMAs.
-// Measured, 4 bits: 2048 tokens through 11008 x 4096 in 258 us (716 TFLOP/s, 0.44 of the library
-// product's burst rate), 4096 through 8192 x 28672 in 1.9 ms (1.0 PFLOP/s, 0.74 of its sustained rate),
-// the gradient of 4096 through 11008 x 4096 in 345 us (1.07 PFLOP/s).  The loss is in handing steps over
+// Measured, 4 bits: 2048 tokens through 11008 x 4096 in 260 to 269 us (the slower 687 TFLOP/s, 0.42 of the
+// library product's burst rate), 4096 through 8192 x 28672 in 1.7 ms cold and 2.0 ms in a row of them (1.1 and
+// 0.96 PFLOP/s, 0.70 of its sustained rate), the gradient of 4096 through 11008 x 4096 in 345 to 359 us (1.03
+// PFLOP/s).  The loss is in handing steps over
 // and, where a tile has few chunks, in the epilogues, during which one of two accumulators is waited for.
 #pragma once
 
