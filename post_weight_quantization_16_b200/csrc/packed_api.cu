@@ -221,6 +221,8 @@ gptq_status linear_many_tokens(const gptq_linear_args& a, const uint16_t* X, int
   return GPTQ_OK;
 }
 
+// Slabs of rows whose scales a block each looks at, eight a thread, at most.
+constexpr int kSlabs = 256;
 // What the gradient's product needs in the workspace.
 struct GradLayout {
   int parts;       // 0: dY itself is the operand, else fp16 values of dz (1, or 2: high and low)
@@ -242,7 +244,7 @@ bool grad_layout(int64_t T, int64_t m, int64_t n, int act_order, int dtype, int 
   };
   const size_t dz = static_cast<size_t>(T) * l->ldz * 2;
   l->scale = take(static_cast<size_t>(T) * 4);
-  l->exponent = take(static_cast<size_t>(n / 128) * 4);
+  l->exponent = take(static_cast<size_t>(n / 128) * kSlabs * 4);
   l->hi = take(l->parts >= 1 ? dz : 0);
   l->lo = take(l->parts == 2 ? dz : 0);
   l->dx = take(act_order ? static_cast<size_t>(T) * n * 2 : 0);
@@ -470,23 +472,24 @@ extern "C" gptq_status gptq_dequant_linear_backward(const gptq_linear_grad_args*
   const int g = group_width(a.W);
   const uint16_t *hi = dY, *lo = dY;
   int64_t ldz = a.ld_dy;
+  SlabArgs w;
+  w.scales = a.W.scales;
+  w.G = n / g;
+  w.per = g >= 128 ? 1 : 128 / g;
+  w.bits = a.W.qp.bits;
+  w.chunks = n / 128;
+  w.slabs = static_cast<int>(std::min<int64_t>({kSlabs, m, (a.W.m * w.G + 4095) / 4096}));
+  w.gi = group_index(g);
+  w.exponent = reinterpret_cast<int*>(ws + lay.exponent);
   {
     uint16_t* h = lay.parts >= 1 ? reinterpret_cast<uint16_t*>(ws + lay.hi) : nullptr;
     uint16_t* o = lay.parts == 2 ? reinterpret_cast<uint16_t*>(ws + lay.lo) : nullptr;
-    ColumnArgs cols;
-    cols.scales = a.W.scales;
-    cols.G = n / g;
-    cols.per = g >= 128 ? 1 : 128 / g;
-    cols.bits = a.W.qp.bits;
-    cols.chunks = n / 128;
-    cols.gi = group_index(g);
-    cols.exponent = reinterpret_cast<int*>(ws + lay.exponent);
     CK(by_act(a.act, [&](auto k) {
       constexpr int A = decltype(k)::value;
       const auto kernel = bf ? (m <= 4096 ? act_grad_kernel<true, A, 1> : act_grad_kernel<true, A, 3>)
                              : (m <= 4096 ? act_grad_kernel<false, A, 1> : act_grad_kernel<false, A, 3>);
-      return launch_pdl(kernel, dim3(cols.chunks + (h ? T : 0)), dim3(512), 0, 1, st, dY, a.ld_dy, Z, m, vec, h, o,
-                        lay.ldz, reinterpret_cast<float*>(ws + lay.scale), cols);
+      return launch_pdl(kernel, dim3(w.slabs + (h ? T : 0)), dim3(512), 0, 1, st, dY, a.ld_dy, Z, m, vec, h, o,
+                        lay.ldz, reinterpret_cast<float*>(ws + lay.scale), w);
     }));
     if (h) {
       ldz = lay.ldz;
@@ -511,6 +514,7 @@ extern "C" gptq_status gptq_dequant_linear_backward(const gptq_linear_grad_args*
   go.lddx = a.W.perm ? n : a.ld_dx;
   go.n = n;
   go.vec = go.lddx % 4 == 0 && aligned_to(go.dX, 8);
+  go.slabs = w.slabs;
   const int parts = std::max(1, lay.parts);
   CUtensorMap cmap, hmap, lmap;
   gptq_status s = encode_codes(&cmap, a.W, TC_BM);

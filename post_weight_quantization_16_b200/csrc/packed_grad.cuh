@@ -37,44 +37,54 @@ __device__ __forceinline__ float at8(const uint4& v, int j) {
   return h2f<BF>(static_cast<uint16_t>((j & 1) ? w >> 16 : w & 0xFFFFu));
 }
 
-// Exponent e[c] of a block of 128 columns of W: (u - z) s 2^e lies below 2^15 for every row, and the largest
+// Exponents of the blocks of 128 columns of W: (u - z) s 2^e lies below 2^15 for every row, and the largest
 // scale's weights near it, so that the product's fp16 weights keep 11 significant bits down to 2^-29 of
 // the block's largest, whatever the layer's scales are (a scale of 1e-7 would leave its codes in fp16's
-// subnormals, one of 1e4 above its largest value).  One block, 512 threads; scales that are not finite do
-// not count.  A row of every group is one 32-byte sector: 11008 rows take 2 us beside the tokens' blocks.
-__device__ __forceinline__ void column_exponent(const float* __restrict__ scales, int m, int G, GroupIndex gi, int per,
-                                                int bits, int chunk, int* __restrict__ out) {
-  __shared__ float wmax[16];
-  const float* first = scales + (per > 1 ? chunk * per : group_of<128>(gi, chunk, 0));
-  const int shift = per == 4 ? 2 : per - 1;  // per: groups of the block, 1, 2 or 4
-  float mx = 0.0f;
-#pragma unroll 8
-  for (int64_t i = threadIdx.x; i < static_cast<int64_t>(m) * per; i += 512) {
-    const float a = fabsf(__ldg(first + (i >> shift) * G + (i & (per - 1))));
-    mx = fmaxf(mx, a < INFINITY ? a : 0.0f);
-  }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  if ((threadIdx.x & 31) == 0) wmax[threadIdx.x >> 5] = mx;
+// subnormals, one of 1e4 above its largest value).  Slabs of rows, read as they lie, a block each, with some
+// eight scales a thread in flight; the product's kernel takes the least of a column block's `slabs`
+// exponents.  Scales that are not finite do not count.  (Where these blocks are a launch of their own, 17
+// tokens' fp16 gradient through 4096 x 4096 takes 15 us, 12 without exponents, and 32 tokens' of 152064 rows
+// 205, not 194.  By blocks of 128 columns, each row's groups another 32-byte sector, they took 17 and 274.)
+struct SlabArgs {
+  const float* scales;
+  int G, per, bits, chunks, slabs;  // per: groups of 128 columns, 1, 2 or 4
+  GroupIndex gi;
+  int* exponent;  // [chunks][slabs]
+};
+__device__ __forceinline__ void slab_exponents(const SlabArgs& p, int m, int slab) {
+  __shared__ unsigned largest[512];  // by column block, or by group where that is wider (bits of a float >= 0)
+  const int t = threadIdx.x, shift = p.per == 4 ? 2 : p.per - 1;
+  largest[t] = 0u;
   __syncthreads();
-  if (threadIdx.x < 32) {
-    mx = wmax[threadIdx.x & 15];
+  const int r0 = static_cast<int>(static_cast<int64_t>(m) * slab / p.slabs),
+            r1 = static_cast<int>(static_cast<int64_t>(m) * (slab + 1) / p.slabs);
+  const int width = min(p.G, 512), at_once = 512 / width, sub = t / width;  // rows at a time; this thread's
+  if (sub < at_once) {
+    for (int c = t % width; c < p.G; c += width) {
+      float mx = 0.0f;
+      for (int r = r0 + sub; r < r1; r += 8 * at_once) {
+        float a[8];
 #pragma unroll
-    for (int o = 8; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    if (threadIdx.x == 0) out[chunk] = mx > 0.0f ? min(126, max(-126, 14 - bits - ilogbf(mx))) : 0;
+        for (int j = 0; j < 8; ++j)
+          a[j] = r + j * at_once < r1 ? fabsf(__ldg(p.scales + static_cast<size_t>(r + j * at_once) * p.G + c)) : 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) mx = fmaxf(mx, a[j] < INFINITY ? a[j] : 0.0f);
+      }
+      unsigned bits = __float_as_uint(mx);
+      if (p.G == 1) bits = __reduce_max_sync(0xffffffffu, bits);
+      if (p.G > 1 || (t & 31) == 0) atomicMax(&largest[c >> shift], bits);
+    }
+  }
+  __syncthreads();
+  for (int k = t; k < p.chunks; k += 512) {
+    // (a subnormal scale counts as 2^-127)
+    const int ilog = static_cast<int>(largest[p.per > 1 ? k : group_of<128>(p.gi, k, 0)] >> 23) - 127;
+    p.exponent[k * p.slabs + slab] = min(126, 14 - p.bits - ilog);
   }
 }
 
-// What the blocks of act_grad_kernel before the tokens' take: one per 128 columns of W.
-struct ColumnArgs {
-  const float* scales;
-  int G, per, bits, chunks;
-  GroupIndex gi;
-  int* exponent;  // [chunks]
-};
-
-// Blocks 0 .. chunks - 1: the weights' exponents.  Then one block per token (the grid has none when dY itself
-// is the operand).  scale_t = 2^e with the largest finite |dz| of the token, dz = dY act'(Z), in
+// The first blocks: the weights' exponents.  Then one block per token (the grid has none when dY itself is
+// the operand).  scale_t = 2^e with the largest finite |dz| of the token, dz = dY act'(Z), in
 // [2^(e+13), 2^(e+14)) (e clamped to [-126, 126], where both scale_t and its inverse are normal; 1 for a
 // token without a finite, nonzero value), then hi + lo = dz / scale_t in fp16 (lo null: hi alone).  (The
 // largest |dY| would not do: an outlier that act' masks would push what is left into fp16's subnormals.)
@@ -87,15 +97,15 @@ __global__ void __launch_bounds__(512) act_grad_kernel(const uint16_t* __restric
                                                        const uint16_t* __restrict__ Z, int m, int vec,
                                                        uint16_t* __restrict__ hi, uint16_t* __restrict__ lo,
                                                        int64_t ldz, float* __restrict__ token_scale,
-                                                       const ColumnArgs cols) {
+                                                       const SlabArgs w) {
   __shared__ float wmax[16];
   griddep_wait();
   griddep_launch_dependents();
-  if (static_cast<int>(blockIdx.x) < cols.chunks) {
-    column_exponent(cols.scales, m, cols.G, cols.gi, cols.per, cols.bits, static_cast<int>(blockIdx.x), cols.exponent);
+  if (static_cast<int>(blockIdx.x) < w.slabs) {
+    slab_exponents(w, m, static_cast<int>(blockIdx.x));
     return;
   }
-  const size_t t = blockIdx.x - cols.chunks;
+  const size_t t = blockIdx.x - w.slabs;
   const uint16_t* dy = dY + t * ld_dy;
   const uint16_t* z = Z + t * m;
   // eight values of dz

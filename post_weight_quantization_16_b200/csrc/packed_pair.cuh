@@ -44,7 +44,8 @@ static_assert(PR_REGS_MISC + 2 * PR_REGS_UNPACK + 2 * PR_REGS_DRAIN <= 5 * 96, "
 __host__ __device__ constexpr int pr_steps(int bits) { return bits == 8 ? 4 : 6; }  // steps in flight (even)
 __host__ __device__ constexpr int pr_code_chunks(int bits) { return bits == 8 ? 4 : 3; }  // code chunks in flight
 __host__ __device__ constexpr int pr_smem_bytes(int bits) {
-  return 1024 + pr_steps(bits) * (PR_A_BYTES + PR_X_BYTES) + pr_code_chunks(bits) * tc_code_bytes(bits) + PR_EPI_BYTES + 512;
+  return 1024 + pr_steps(bits) * (PR_A_BYTES + PR_X_BYTES) + pr_code_chunks(bits) * tc_code_bytes(bits) + PR_EPI_BYTES + 512 +
+         256;
 }
 static_assert(pr_smem_bytes(4) <= 227 * 1024 && pr_smem_bytes(8) <= 227 * 1024, "shared memory");
 
@@ -90,6 +91,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PR_THREADS, 1)
                  bar_drain = bar_tempty + 16;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + (bar_drain + 8 - sbase));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  // gradient: the weights' exponents of this block's columns, [tiles_m]
+  int8_t* exponents = reinterpret_cast<int8_t*>(smem + (bar_full - sbase) + 512);
 
   // (a shuffled warp index is known to be uniform: operands of the MMAs stay in uniform registers)
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
@@ -258,11 +261,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PR_THREADS, 1)
     };
     int as = grp;  // slot of this group's next step
     uint32_t aph = 0;
+    if (BWD) {
+      for (int i = warp - 4; i < p.tiles_m; i += 8) {
+        const int e = column_exponent(p.go, min(2 * i + static_cast<int>(rank), p.go.n / 128 - 1), lane);
+        if (lane == 0) exponents[i] = static_cast<int8_t>(e);
+      }
+      asm volatile("bar.sync 1, 512;" ::: "memory");  // unpack and drain warps
+    }
     bool ok = cluster < ntiles && take();
     for (int tile = cluster; tile < ntiles && ok; tile += clusters) {
       const int mt = tile % p.tiles_m * 2 + static_cast<int>(rank);
       // row of W and its groups: forward row mt * 128 + r in chunk i; gradient row i * 128 + r in chunk mt
-      const float up = BWD ? pow2(p.go.exponent[min(mt, p.go.n / 128 - 1)]) : 1.0f;
+      const float up = BWD ? pow2(exponents[tile % p.tiles_m]) : 1.0f;
       float ns[ZN], nz[ZN];
       auto load_sz = [&](int i) {
         const int gr = (BWD ? i : mt) * 128 + r;
@@ -328,6 +338,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PR_THREADS, 1)
     const uint32_t lead_tempty = mapa_shared(bar_tempty, 0);
     const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(qd * 32) << 16) + static_cast<uint32_t>(half * 128);
     float* stage = reinterpret_cast<float*>(smem + (e_base - sbase)) + (warp - 12) * 256;  // [8 tokens][32 rows]
+    if (BWD) asm volatile("bar.sync 1, 512;" ::: "memory");  // the exponents are there
     RingPos<2> t;
     bool ok = true;
     for (int tile = cluster; tile < ntiles && ok; tile += clusters) {
@@ -377,12 +388,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PR_THREADS, 1)
         __syncwarp();
       };
       if (BWD) {
+        const int e = exponents[tile % p.tiles_m];
         if (!warp_wait_uniform_cl(bar_tfull + 8 * t.s, t.ph, abort_flag)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const int e = p.go.exponent[min(mt, p.go.n / 128 - 1)];
 #pragma unroll 1
         for (int cc = 0; cc < 8; ++cc) {
           uint32_t v[16];

@@ -242,21 +242,32 @@ struct RingAt {
 
 struct GradOut {
   const float* token_scale;  // [T], powers of two, or null (1)
-  const int* exponent;       // [n / 128]: the weights of these columns are multiplied by 2^exponent
+  const int* exponent;       // [n / 128][slabs]: the weights of these columns are multiplied by 2^(the least of them)
+  int slabs;
   uint16_t* dX;              // [T x n], sweep order
   int64_t lddx;
   int n, vec;  // vec: dX allows 8-byte accesses
 };
 
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }  // |e| <= 126
+// The exponent of 128 columns is the least of the warp's lanes' parts.
+__device__ __forceinline__ int exponent_part(const GradOut& go, int chunk, int lane) {
+  int e = 126;
+  if (lane < go.slabs) e = go.exponent[chunk * go.slabs + lane];
+  for (int i = lane + 32; i < go.slabs; i += 32) e = min(e, go.exponent[chunk * go.slabs + i]);
+  return e;
+}
+__device__ __forceinline__ int column_exponent(const GradOut& go, int chunk, int lane) {
+  return __reduce_min_sync(0xffffffffu, exponent_part(go, chunk, lane));
+}
 // v times the token's scale over the weights' 2^e: in two steps, as the two together may lie past the
 // exponents of fp32 while the result does not.
 struct Unscale {
   float a, b;
   __device__ __forceinline__ Unscale(float token_scale, int e) {
     const int x = static_cast<int>(__float_as_uint(token_scale) >> 23) - 127 - e;
-    a = pow2(x / 2);
-    b = pow2(x - x / 2);
+    a = pow2(x >> 1);
+    b = pow2(x - (x >> 1));
   }
   __device__ __forceinline__ float operator()(float v) const { return v * a * b; }
 };
@@ -419,7 +430,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     const uint32_t dst0 = a_base + (BWD ? h * (TC_STEP_A / 2) + (r & 63) * 128 : r * 128);
     constexpr int ZN = GU == 32 ? 2 : 1;  // groups of a half row
     float ns[ZN], nz[ZN];
-    const float up = BWD ? pow2(go.exponent[mt]) : 1.0f;
+    const int part = BWD ? exponent_part(go, mt, lane) : 0;
     auto load_sz = [&](int i) {
       const int c = ch0 + (BWD && i >= nch ? i - nch : i);
       const int gr = (BWD ? c : mt) * 128 + r;
@@ -449,6 +460,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       load_sz(par);
       ok = take();
     }
+    const float up = BWD ? pow2(__reduce_min_sync(0xffffffffu, part)) : 1.0f;  // (its load waited for beside theirs)
     for (int i = par; i < nk && ok; i += 2) {
       float cs_[ZN], cz[ZN];
 #pragma unroll
@@ -544,7 +556,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   if (cs > 1) cluster_sync();
   // tokens rank, rank + cs, ... of the tile: a warp takes a token, a lane four rows (columns of dX)
   if (!*abort_flag) {
-    const int e = BWD ? go.exponent[mt] : 0;
+    const int e = BWD ? column_exponent(go, mt, lane) : 0;
     for (int t = rank + cs * warp; t < tn; t += cs * (TC_THREADS / 32)) {
       const int tok = t0 + t, row = mt * TC_BM + 4 * lane;
       if (tok >= p.T || (!BWD && row >= p.m)) continue;

@@ -13,7 +13,7 @@ pytestmark = pytest.mark.gpu
 KERNELS = [(20, 256), (300, 9472)]                    # tokens and columns of the single-block and of the pair kernel
 
 
-def gradient_close(c, got, dY, Z, dtype):
+def gradient_close(c, got, dY, Z, dtype, sharp=True):
     """dX against the 64-bit formula with the exact weights: every product of dz and a weight is off by at
     most 2^-11 for each of them (2^-10 and the product of the two), a value of dz by 2^-25 of 2^13 times less
     than the token's largest |dz| where it is that small, the sum by its accumulation, dX by its rounding."""
@@ -33,8 +33,9 @@ def gradient_close(c, got, dY, Z, dtype):
     tol += H.EPS[dtype] * (np.abs(want) + tol) + H.TINY[dtype]
     d = np.abs(H.to64(got) - want)
     assert (d <= tol).all(), float((d / tol).max())
-    # the tolerance says something: it is far below the values
-    assert np.median(tol / np.abs(want).clip(1e-300)) < 0.1
+    # the tolerance says something: it is far below the values.  (Not with very many rows: the accumulation's
+    # bound grows with their number, 2^-8 of the sum of magnitudes at 270000, and the values with its root.)
+    assert not sharp or np.median(tol / np.abs(want).clip(1e-300)) < 0.1
 
 
 @pytest.mark.parametrize("T,n", KERNELS)
@@ -188,3 +189,21 @@ def test_gradient_of_no_tokens(act):
     e = torch.empty(0, 33, dtype=c.dt, device=DEV)
     dx = G.dequant_linear_backward(e, *c.layer, act=H.ACTS[act], preact=e)
     assert dx.shape == (0, 256) and dx.dtype == c.dt
+
+
+@pytest.mark.parametrize("T,m,n,bits,g", [(5, 40000, 256, 4, 64), (3, 270000, 128, 2, 32), (4, 50, 65536, 4, 32), (3, 30000, 128, 3, -1),
+                                          (20, 1100, 65536, 2, 64), (600, 9000, 1152, 4, 384)])
+def test_gradient_scales_are_looked_at_in_every_row_and_column(T, m, n, bits, g):
+    """One scale of each block of 128 columns, in a row of its own, is 2^14 times the others: fp16 would
+    overflow if its slab, or its group among many, were left out."""
+    c = Case(T, m, n, bits, g, "bf16", "none", True)
+    f = np.ones_like(c.s, dtype=np.float64)
+    G_ = f.shape[1]
+    per = max(1, 128 * G_ // n)
+    for b in range(0, G_, per):
+        f[c.rng.integers(m), b + c.rng.integers(per)] = 2.0 ** 14
+    f[m - 1, G_ - 1] = f[0, 0] = 2.0 ** 14
+    rescaled(c, 16 * f)
+    dY = c.dev(c.rng.normal(0, 1, (T, m)))
+    Z = c.dev(np.ones((T, m)))
+    gradient_close(c, G.dequant_linear_backward(dY, *c.layer), dY, Z, c.dt, sharp=m < 20000)
