@@ -243,7 +243,7 @@ bool grad_layout(int64_t T, int64_t m, int64_t n, int act_order, int dtype, int 
     return at;
   };
   const size_t dz = static_cast<size_t>(T) * l->ldz * 2;
-  l->scale = take(static_cast<size_t>(T) * 4);
+  l->scale = take(static_cast<size_t>(T) * 8);
   l->exponent = take(static_cast<size_t>(n / 128) * kSlabs * 4);
   l->hi = take(l->parts >= 1 ? dz : 0);
   l->lo = take(l->parts == 2 ? dz : 0);
@@ -489,7 +489,7 @@ extern "C" gptq_status gptq_dequant_linear_backward(const gptq_linear_grad_args*
       const auto kernel = bf ? (m <= 4096 ? act_grad_kernel<true, A, 1> : act_grad_kernel<true, A, 3>)
                              : (m <= 4096 ? act_grad_kernel<false, A, 1> : act_grad_kernel<false, A, 3>);
       return launch_pdl(kernel, dim3(w.slabs + (h ? T : 0)), dim3(512), 0, 1, st, dY, a.ld_dy, Z, m, vec, h, o,
-                        lay.ldz, reinterpret_cast<float*>(ws + lay.scale), w);
+                        lay.ldz, reinterpret_cast<float2*>(ws + lay.scale), w);
     }));
     if (h) {
       ldz = lay.ldz;
@@ -508,7 +508,7 @@ extern "C" gptq_status gptq_dequant_linear_backward(const gptq_linear_grad_args*
   d.zeros = a.W.zeros;
   d.status = reinterpret_cast<int*>(ws);
   GradOut go;
-  go.token_scale = lay.parts >= 1 ? reinterpret_cast<const float*>(ws + lay.scale) : nullptr;
+  go.token_scale = lay.parts >= 1 ? reinterpret_cast<const float2*>(ws + lay.scale) : nullptr;
   go.exponent = reinterpret_cast<const int*>(ws + lay.exponent);
   go.dX = a.W.perm ? reinterpret_cast<uint16_t*>(ws + lay.dx) : static_cast<uint16_t*>(a.dX);
   go.lddx = a.W.perm ? n : a.ld_dx;

@@ -96,7 +96,7 @@ template <bool BF, int ACT, int KEPT>
 __global__ void __launch_bounds__(512) act_grad_kernel(const uint16_t* __restrict__ dY, int64_t ld_dy,
                                                        const uint16_t* __restrict__ Z, int m, int vec,
                                                        uint16_t* __restrict__ hi, uint16_t* __restrict__ lo,
-                                                       int64_t ldz, float* __restrict__ token_scale,
+                                                       int64_t ldz, float2* __restrict__ token_scale,
                                                        const SlabArgs w) {
   __shared__ float wmax[16];
   griddep_wait();
@@ -160,8 +160,8 @@ __global__ void __launch_bounds__(512) act_grad_kernel(const uint16_t* __restric
   for (int w = 0; w < 16; ++w) mx = fmaxf(mx, wmax[w]);
   int e = 0;
   if (mx > 0.0f) e = min(126, max(-126, ilogbf(mx) - 13));
-  const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-  if (threadIdx.x == 0) token_scale[t] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+  const float inv = pow2(-e);
+  if (threadIdx.x == 0) token_scale[t] = pow2_halves(e);
   auto store = [&](int r, float (&x)[8]) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) x[j] *= inv;

@@ -262,9 +262,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PR_THREADS, 1)
     int as = grp;  // slot of this group's next step
     uint32_t aph = 0;
     if (BWD) {
-      for (int i = warp - 4; i < p.tiles_m; i += 8) {
-        const int e = column_exponent(p.go, min(2 * i + static_cast<int>(rank), p.go.n / 128 - 1), lane);
-        if (lane == 0) exponents[i] = static_cast<int8_t>(e);
+      for (int i0 = warp - 4; i0 < p.tiles_m; i0 += 32) {
+        int part[4];  // (four loads in flight)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          part[k] = exponent_part(p.go, min(2 * (i0 + 8 * k) + static_cast<int>(rank), p.go.n / 128 - 1), lane);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          part[k] = __reduce_min_sync(0xffffffffu, part[k]);
+          if (lane == 0 && i0 + 8 * k < p.tiles_m) exponents[i0 + 8 * k] = static_cast<int8_t>(part[k]);
+        }
       }
       asm volatile("bar.sync 1, 512;" ::: "memory");  // unpack and drain warps
     }
@@ -388,7 +395,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PR_THREADS, 1)
         __syncwarp();
       };
       if (BWD) {
-        const int e = exponents[tile % p.tiles_m];
+        const float2 back = pow2_halves(-exponents[tile % p.tiles_m]);
         if (!warp_wait_uniform_cl(bar_tfull + 8 * t.s, t.ph, abort_flag)) {
           ok = false;
           break;
@@ -404,7 +411,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PR_THREADS, 1)
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               const int t = tok0 + cc * 16 + 8 * g + j;
-              const Unscale s(p.go.token_scale && t < p.lin.T ? __ldg(p.go.token_scale + t) : 1.0f, e);
+              const Unscale s(p.go.token_scale && t < p.lin.T ? __ldg(p.go.token_scale + t) : make_float2(1.0f, 1.0f), back);
               stage[j * 32 + lane] = s(__uint_as_float(v[8 * g + j]));
             }
             put8(cc * 16 + 8 * g, p.go.dX, p.go.lddx, false, nullptr);

@@ -241,7 +241,7 @@ struct RingAt {
 };
 
 struct GradOut {
-  const float* token_scale;  // [T], powers of two, or null (1)
+  const float2* token_scale;  // [T], powers of two as products of two, or null (1)
   const int* exponent;       // [n / 128][slabs]: the weights of these columns are multiplied by 2^(the least of them)
   int slabs;
   uint16_t* dX;              // [T x n], sweep order
@@ -249,7 +249,6 @@ struct GradOut {
   int n, vec;  // vec: dX allows 8-byte accesses
 };
 
-__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }  // |e| <= 126
 // The exponent of 128 columns is the least of the warp's lanes' parts.
 __device__ __forceinline__ int exponent_part(const GradOut& go, int chunk, int lane) {
   int e = 126;
@@ -260,15 +259,12 @@ __device__ __forceinline__ int exponent_part(const GradOut& go, int chunk, int l
 __device__ __forceinline__ int column_exponent(const GradOut& go, int chunk, int lane) {
   return __reduce_min_sync(0xffffffffu, exponent_part(go, chunk, lane));
 }
-// v times the token's scale over the weights' 2^e: in two steps, as the two together may lie past the
+// v times the token's scale over the weights' 2^e: both in two halves, as the two together may lie past the
 // exponents of fp32 while the result does not.
 struct Unscale {
   float a, b;
-  __device__ __forceinline__ Unscale(float token_scale, int e) {
-    const int x = static_cast<int>(__float_as_uint(token_scale) >> 23) - 127 - e;
-    a = pow2(x >> 1);
-    b = pow2(x - (x >> 1));
-  }
+  __device__ __forceinline__ Unscale(float2 token_scale, float2 weights)
+      : a(token_scale.x * weights.x), b(token_scale.y * weights.y) {}
   __device__ __forceinline__ float operator()(float v) const { return v * a * b; }
 };
 
@@ -556,7 +552,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   if (cs > 1) cluster_sync();
   // tokens rank, rank + cs, ... of the tile: a warp takes a token, a lane four rows (columns of dX)
   if (!*abort_flag) {
-    const int e = BWD ? column_exponent(go, mt, lane) : 0;
+    const float2 back = pow2_halves(BWD ? -column_exponent(go, mt, lane) : 0);
     for (int t = rank + cs * warp; t < tn; t += cs * (TC_THREADS / 32)) {
       const int tok = t0 + t, row = mt * TC_BM + 4 * lane;
       if (tok >= p.T || (!BWD && row >= p.m)) continue;
@@ -570,7 +566,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         v.w += w.w;
       }
       if (BWD) {
-        const Unscale s(go.token_scale ? go.token_scale[tok] : 1.0f, e);
+        const Unscale s(go.token_scale ? go.token_scale[tok] : make_float2(1.0f, 1.0f), back);
         uint16_t* o = go.dX + static_cast<size_t>(tok) * go.lddx + row;
         const uint32_t lo = pack2<BF>(s(v.x), s(v.y)), hi = pack2<BF>(s(v.z), s(v.w));
         if (go.vec) {
