@@ -108,10 +108,14 @@ __global__ void __launch_bounds__(512) act_grad_kernel(const uint16_t* __restric
   const size_t t = blockIdx.x - w.slabs;
   const uint16_t* dy = dY + t * ld_dy;
   const uint16_t* z = Z + t * m;
-  // eight values of dz
+  // Eight values of dz; of bf16 and a slope that exceeds 1, halved: dz may lie above fp32's largest.
+  constexpr int HALVED = BF && (ACT == ACT_GELU || ACT == ACT_SILU) ? 1 : 0;
   auto eight = [&](const uint4& v, const uint4& zv, float (&x)[8]) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = at8<BF>(v, j) * (ACT != ACT_NONE ? act_grad<ACT>(at8<BF>(zv, j)) : 1.0f);
+    for (int j = 0; j < 8; ++j) {
+      const float d = HALVED ? 0.5f * at8<BF>(v, j) : at8<BF>(v, j);
+      x[j] = d * (ACT != ACT_NONE ? act_grad<ACT>(at8<BF>(zv, j)) : 1.0f);
+    }
   };
   auto load = [&](int r, bool whole, uint4& v, uint4& zv) {
     v = load8(dy + r, whole, m - r);
@@ -161,7 +165,7 @@ __global__ void __launch_bounds__(512) act_grad_kernel(const uint16_t* __restric
   int e = 0;
   if (mx > 0.0f) e = min(126, max(-126, ilogbf(mx) - 13));
   const float inv = pow2(-e);
-  if (threadIdx.x == 0) token_scale[t] = pow2_halves(e);
+  if (threadIdx.x == 0) token_scale[t] = pow2_halves(e + HALVED);
   auto store = [&](int r, float (&x)[8]) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) x[j] *= inv;

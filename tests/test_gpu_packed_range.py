@@ -207,3 +207,14 @@ def test_gradient_scales_are_looked_at_in_every_row_and_column(T, m, n, bits, g)
     dY = c.dev(c.rng.normal(0, 1, (T, m)))
     Z = c.dev(np.ones((T, m)))
     gradient_close(c, G.dequant_linear_backward(dY, *c.layer), dY, Z, c.dt, sharp=m < 20000)
+
+
+@pytest.mark.parametrize("T,n", KERNELS)
+@pytest.mark.parametrize("act", ["gelu", "silu", "relu"])
+def test_gradients_at_the_end_of_bf16(T, n, act):
+    """dY up to bf16's largest where the slope is above 1: dz alone is past fp32, dX is not."""
+    c = Case(T, 200, n, 4, 128, "bf16", act, True)
+    dY = torch.from_numpy(c.rng.choice([-3.3e38, 3.3e38, 1e38, -1e37], (T, 200))).to(DEV).to(c.dt)
+    Z = torch.from_numpy(c.rng.uniform(1.2, 2.5, (T, 200))).to(DEV).to(c.dt)
+    rescaled(c, 2.0 ** -10)
+    gradient_close(c, G.dequant_linear_backward(dY, *c.layer, act=H.ACTS[act], preact=Z), dY, Z, c.dt)
