@@ -66,25 +66,18 @@ __device__ __forceinline__ float2 minus_log2e(float hi) {
   const float y = -kLog2e * hi;
   return make_float2(y, fmaf(-kLog2eLow, hi, fmaf(-kLog2e, hi, -y)));
 }
-// The logistic function 1 / (1 + e^-z) and that of -z: relative errors below 2^-20.5 (0 for z below -87.3).
-// Past 88 either way nothing changes, and the exponent's rest would not be a number.
-__device__ __forceinline__ void logistic(float z, float& at_z, float& at_minus_z) {
+// SiLU, z / (1 + e^-z): relative error below 2^-20 (0 for z below -87.3).  Past 88 either way the power
+// changes nothing, and its exponent's rest would not be a number.
+__device__ __forceinline__ float silu(float z) {
   const float2 x = minus_log2e(fminf(fmaxf(z, -88.0f), 88.0f));
   const float p = ex2_ftz(x.x), e = fmaf(p, x.y * kLn2, p);
-  at_z = rcp_ftz(1.0f + e);
-  at_minus_z = e * at_z;
+  return z * rcp_ftz(1.0f + e);
 }
-// SiLU, z / (1 + e^-z): relative error below 2^-20.
-__device__ __forceinline__ float silu(float z) {
-  float s, other;
-  logistic(z, s, other);
-  return z * s;
-}
-// The normal distribution's tail beyond |z|, and e^(-z^2 / 2): relative errors below 2^-19 (0 where the power
-// is below 2^-126, |z| > 13.2).  The complementary error function is the Chebyshev fit of Numerical Recipes,
-// t e^(q(t) - x^2) with a relative error below 1.2e-7 for every x = |z| / sqrt 2; the rounding errors of the
-// square and of its exponent go into the second power.
-__device__ __forceinline__ float normal_tail(float z, float& gauss) {
+// GELU, z times the normal distribution function: relative error below 2^-19 (0 where e^(-z^2 / 2) is below
+// 2^-126, z < -13.2).  The tail beyond |z| by the complementary error function's Chebyshev fit of Numerical
+// Recipes, t e^(q(t) - x^2) with a relative error below 1.2e-7 for every x = |z| / sqrt 2; the rounding errors
+// of the square and of its exponent go into the second power.
+__device__ __forceinline__ float gelu(float z) {
   const float a = fminf(fabsf(z), 20.0f), square = a * a, low = fmaf(a, a, -square);
   const float t = rcp_ftz(1.0f + 0.35355339059327376f * a);
   float q = 0.17087277f;
@@ -98,14 +91,8 @@ __device__ __forceinline__ float normal_tail(float z, float& gauss) {
   q = fmaf(t, q, 1.00002368f);
   q = fmaf(t, q, -1.26551223f);
   const float2 x = minus_log2e(0.5f * square);
-  const float r = fmaf(-0.5f * kLog2e, low, x.y), p = ex2_ftz(x.x);
-  gauss = fmaf(p, r * kLn2, p);
-  return 0.5f * t * (p * ex2_ftz(fmaf(kLog2e, q, r)));
-}
-// GELU: z times the normal distribution function.
-__device__ __forceinline__ float gelu(float z) {
-  float gauss;
-  const float c = normal_tail(z, gauss);
+  const float r = fmaf(-0.5f * kLog2e, low, x.y);
+  const float c = 0.5f * t * (ex2_ftz(x.x) * ex2_ftz(fmaf(kLog2e, q, r)));
   return z * (z < 0.0f ? c : 1.0f - c);
 }
 __device__ __forceinline__ float act_apply(float z, int act) {

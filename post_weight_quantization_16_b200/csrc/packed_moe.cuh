@@ -255,7 +255,8 @@ __global__ void __launch_bounds__(ROUTER_WARPS * 32) moe_router_kernel(const Rou
       v[i] = 0.0;
       if (i < per && lane + 32 * i < p.E) {
         v[i] = __ldcg(p.logits + static_cast<size_t>(t) * p.E + lane + 32 * i);
-        bound = fmaxf(bound, __ldcg(p.bounds + static_cast<size_t>(t) * p.E + lane + 32 * i));
+        const float b = __ldcg(p.bounds + static_cast<size_t>(t) * p.E + lane + 32 * i);
+        bound = fmaxf(bound, b < INFINITY ? b : 0.0f);  // (such a logit is not finite either)
         best = fmax(best, v[i]);
       }
     }

@@ -218,3 +218,86 @@ def test_gradients_at_the_end_of_bf16(T, n, act):
     Z = torch.from_numpy(c.rng.uniform(1.2, 2.5, (T, 200))).to(DEV).to(c.dt)
     rescaled(c, 2.0 ** -10)
     gradient_close(c, G.dequant_linear_backward(dY, *c.layer, act=H.ACTS[act], preact=Z), dY, Z, c.dt)
+
+
+def test_an_expert_whose_router_row_is_infinite_leaves_the_others_order():
+    """Its logit is an infinity of either sign: chosen first or last; the others stand as 64-bit logits say."""
+    c = Moe(40, 32, 4, 512, 128, 4, 64, 64, "bf16", perm=False, seed=9)
+    r = c.router.clone()
+    for e in range(16):
+        r[e + 16] = r[e]
+        r[e + 16, 7 * e] *= 1 + 4 * H.EPS[c.dt]
+    r[5] = 0
+    r[5, 3] = float("inf")
+    x, rr = H.to64(c.X), H.to64(r)
+    rr[5] = 0
+    logits = x @ rr.T
+    logits[:, 5] = np.where(x[:, 3] > 0, np.inf, -np.inf)
+    want = np.argsort(-logits, axis=1, kind="stable")[:, :4]
+    X = c.X.clone()
+    y, ids, w = c.run(X=X, router=r)
+    assert (x[:, 3] != 0).all() and np.array_equal(ids.cpu().numpy(), want)
+
+
+def captured(call):
+    call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = call()
+    return g, out
+
+
+@pytest.mark.parametrize("T", [4, 40])
+def test_a_graph_s_replays_keep_nothing_of_the_one_before(T):
+    """Inputs and weights changed between replays so that what a call finds out about them changes: gated
+    values past fp16 and back, choices that stand close and do not, the weights' largest scale."""
+    c = Moe(T, 8, 2, 256, 256, 4, 64, 128, "fp16", seed=4)
+    c.down[1].mul_(2.0 ** -20)
+    X = c.X.clone()
+    g, out = captured(lambda: c.run(X=X))
+    for factor in (1.0, 200.0, 1.0, 0.0, 200.0, 1.0):
+        X.copy_(c.X * factor)
+        g.replay()
+        torch.cuda.synchronize()
+        fresh = c.run(X=X)
+        for a, b in zip(out, fresh):
+            assert torch.equal(a, b), factor
+        assert out[0].isfinite().all()
+    for T, n in [(T, 256), (300, 9472)]:
+        k = Case(T, 200, n, 4, 128, "bf16", "silu", True)
+        dY, Z = k.dev(k.rng.normal(0, 1, (T, 200))), k.dev(k.rng.normal(0, 1, (T, 200)))
+        scales, grad = k.layer[1].clone(), dY.clone()
+        g, out = captured(lambda: G.dequant_linear_backward(dY, *k.layer, act=G.ACT_SILU, preact=Z, want_dbias=True))
+        for ws, gs in ((1.0, 1.0), (2.0 ** 40, 1.0), (2.0 ** -40, 2.0 ** 50), (0.0, 1.0), (1.0, 0.0), (1.0, 1.0)):
+            k.layer[1].copy_(scales * ws)
+            dY.copy_(grad * gs)
+            g.replay()
+            torch.cuda.synchronize()
+            dx, db = G.dequant_linear_backward(dY, *k.layer, act=G.ACT_SILU, preact=Z, want_dbias=True)
+            assert torch.equal(out[0], dx) and torch.equal(out[1], db), (ws, gs)
+            if ws and gs:
+                k.s = k.layer[1].cpu().numpy()                         # (the tensor stays the graph's)
+                k.W = H.weights64(k.codes, k.s, k.z)
+                gradient_close(k, dx, dY, Z, k.dt)
+
+
+def test_two_streams_at_once():
+    """Gradients and experts of different inputs on two streams that run together, each as alone."""
+    a, b = Case(200, 300, 512, 4, 64, "bf16", "gelu", True, seed=1), Case(200, 300, 512, 4, 64, "fp16", "none", True, seed=2)
+    m1, m2 = Moe(20, 8, 2, 256, 256, 4, 64, 64, "fp16", seed=6), Moe(20, 8, 2, 256, 256, 4, 64, 64, "bf16", seed=7)
+    Z = a.dev(a.rng.normal(0, 1, (200, 300)))
+    d1, d2 = a.dev(a.rng.normal(0, 1, (200, 300))), b.dev(b.rng.normal(0, 1, (200, 300)))
+    calls = [(lambda **k: G.dequant_linear_backward(d1, *a.layer, act=G.ACT_GELU, preact=Z, **k), lambda **k: m1.run(**k)[0]),
+             (lambda **k: G.dequant_linear_backward(d2, *b.layer, **k), lambda **k: m2.run(**k)[0])]
+    want = [[f() for f in fs] for fs in calls]
+    streams = [torch.cuda.Stream(DEV) for _ in calls]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(30):
+        for k, s in enumerate(streams):
+            got[k].append([f(stream=s) for f in calls[k]])
+    torch.cuda.synchronize()
+    for k in range(2):
+        for row in got[k]:
+            assert all(torch.equal(x, y) for x, y in zip(row, want[k]))
