@@ -23,7 +23,7 @@
 // overlaps the next tile's MMAs.
 // Measured, 4 bits: 2048 tokens through 11008 x 4096 in 260 to 269 us (the slower 687 TFLOP/s, 0.42 of the
 // library product's burst rate), 4096 through 8192 x 28672 in 1.7 ms cold and 2.0 ms in a row of them (1.1 and
-// 0.96 PFLOP/s, 0.70 of its sustained rate), the gradient of 4096 through 11008 x 4096 in 345 to 359 us (1.03
+// 0.96 PFLOP/s, 0.70 of its sustained rate), the gradient of 4096 through 11008 x 4096 in 345 to 361 us (1.02
 // PFLOP/s).  The loss is in handing steps over
 // and, where a tile has few chunks, in the epilogues, during which one of two accumulators is waited for.
 #pragma once

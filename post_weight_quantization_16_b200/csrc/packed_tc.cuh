@@ -22,8 +22,8 @@
 // distributed shared memory in a fixed order, in the epilogue that also adds the bias, applies the
 // activation and adds the residual: one launch, deterministic.  77 tokens through 11008 x 4096 with 3
 // bits take 38 us (the bytes and the products would take 4): 32 chunks of unpacking, hand-over and drain
-// one behind the other in 86 blocks; 500 tokens' gradient through 4096 x 4096 40 us with its two other
-// launches, 31 here.
+// one behind the other in 86 blocks; 500 tokens' gradient through 4096 x 4096 39 us with its two other
+// launches, 32 here.
 //
 // Gradient: dX[t][perm[k]] = scale_t * sum over rows r of W16[r][k] * dz[t][r],
 //     W16 = fp16( fp32(u - z) * s * 2^e ) / 2^e,   dz[t][r] = dY[t][r] act'(Z[t][r]) / scale_t  in fp16
