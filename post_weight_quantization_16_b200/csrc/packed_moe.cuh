@@ -122,7 +122,8 @@ constexpr float ROUTER_ERROR = 1.01f / 65536.0f;
 
 // The logit of one expert in fp64, by a warp: products, exact in fp32, are added in 64 bits in a fixed order.
 template <bool BF>
-__device__ __noinline__ double exact_logit(const uint16_t* __restrict__ x, const uint16_t* __restrict__ r, int H, int lane) {
+__device__ __noinline__ double exact_logit(const uint16_t* __restrict__ x, const uint16_t* __restrict__ r, int H,
+                                           int lane) {
   double sum[4] = {0.0, 0.0, 0.0, 0.0};
 #pragma unroll 4
   for (int c = lane * 8; c < H; c += 256) {
@@ -146,8 +147,8 @@ __device__ __noinline__ double exact_logit(const uint16_t* __restrict__ x, const
 // bound the error.  (2) Softmax and top-k: a warp per token, in fp64; equal values go to the lower expert;
 // a NaN logit is chosen last (its weights are NaN).  Where two of the largest top_k + 1 logits stand so
 // close that their errors could swap them, all logits at stake are formed again in fp64: the choices are
-// those of the 64-bit logits.  (3) The lists, in block 0: a thread per choice, whose place is what its expert has before its
-// group of 32 choices and its rank inside it, so positions are deterministic.
+// those of the 64-bit logits.  (3) The lists, in block 0: a thread per choice, whose place is what its expert
+// has before its group of 32 choices and its rank inside it, so positions are deterministic.
 // By its own clock: 7 us for two tokens over 32 experts (2048 wide), 18 for 33 over 64, of which 9 are the
 // logits (eight SMs fetch R and X, four trips to memory each), 5 the softmax and the choices, 4 the
 // lists and barriers (lists by a warp per expert took 7 more); 1 for the errors' bounds and, where a
